@@ -60,7 +60,9 @@ typedef enum jfa_status {
   JFA_ERR_ALIGNMENT = 4,      /* a device pointer is not 16-byte aligned */
   JFA_ERR_WORKSPACE = 5,      /* workspace missing or smaller than jfa_bwd_workspace_bytes */
   JFA_ERR_CUDA = 6,           /* a CUDA runtime call failed */
-  JFA_ERR_DEVICE_TIMEOUT = 7  /* a kernel wait ran out (see jfa_plan_device_status) */
+  JFA_ERR_DEVICE_TIMEOUT = 7, /* a kernel wait ran out (see jfa_plan_device_status) */
+  JFA_ERR_PAGES = 8           /* a paged call met bad lengths, pages or slots, or ran out of pages
+                                 (see jfa_pager_status) */
 } jfa_status;
 
 /* Tile geometry: query rows per forward tile and key rows per backward tile. */
@@ -443,6 +445,173 @@ int jfa_simple_device_status(void* stream, int* raw);
 
 /* Release every cached plan and workspace (synchronises the device). */
 int jfa_simple_release(void);
+
+/*
+ * Rotary positions.  A pair of values (a, b) of a head becomes
+ *     (a cos phi - b sin phi, b cos phi + a sin phi),
+ *     phi = positions[row][axis[i]] * inv_freq[i]
+ * for pair i = 0 .. pairs-1, with one position per row and axis (time, height
+ * and width of a patch, say; axis[i] in 0 .. 3).  Pair i is (x[i], x[i + pairs]),
+ * or (x[2i], x[2i+1]) with JFA_ROTARY_INTERLEAVED; the D - 2*pairs values
+ * behind are copied.  D in {64, 128}; pairs a multiple of 8 with 2*pairs <= D.
+ *
+ * Angles are kept as turns in 64-bit fixed point: inv_freq[i] / (2 pi) is
+ * rounded once to a multiple of 2^-64 when the handle is made, its product
+ * with an int32 position wraps at whole turns without loss, and its upper 32
+ * bits go to the sine and cosine in fp32.  A far position's angle is so exact
+ * to 2^-31 turns.  inv_freq must be finite and below 2^31 in magnitude.
+ *
+ * The handle holds no device memory: it serves every device and stream, and
+ * any number of calls at once.
+ */
+typedef struct jfa_rotary* jfa_rotary_t;
+#define JFA_ROTARY_INTERLEAVED 1u
+int jfa_rotary_create(const double* inv_freq_host, const int32_t* axis_host, int pairs, int D,
+                      unsigned flags, jfa_rotary_t* out);
+int jfa_rotary_destroy(jfa_rotary_t rotary);
+
+/* Host-only: the 64-bit turn fractions a handle made from inv_freq holds. */
+int jfa_rotary_turns(const double* inv_freq_host, int pairs, uint64_t* turns_out);
+
+/*
+ * Rotate up to two tensors of `rows` rows by the same positions in one launch
+ * (x and y: q and k, or their gradients).  x is [rows, x_heads, D] with
+ * x_row elements from row to row, heads contiguous; x_out has the same shape
+ * and type, its rows x_out_row elements apart.  x_out may be x with the same
+ * row distance (in place); otherwise outputs overlap no input.  y == NULL
+ * with y_heads 0: one tensor.  Rows are at least heads * D elements apart and
+ * a multiple of 16 bytes; tensors are 16-byte aligned.
+ * positions: device int32; the position of row r on axis a is
+ * positions[r * pos_row + a * pos_axis] (pos_axis 0: one position for every axis).
+ * flags: JFA_ROTATE_INVERSE rotates by -phi, which is the gradient of the
+ * rotation; JFA_ROTATE_X_FP32 / JFA_ROTATE_Y_FP32: that tensor is fp32 (as
+ * jfa_bwd's dq is), otherwise bf16.  Sums are formed in fp32 and rounded once.
+ */
+#define JFA_ROTATE_INVERSE 1u
+#define JFA_ROTATE_X_FP32 2u
+#define JFA_ROTATE_Y_FP32 4u
+int jfa_rotate(jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row, int64_t pos_axis,
+               int64_t rows, unsigned flags, const void* x, int64_t x_row, void* x_out,
+               int64_t x_out_row, int x_heads, const void* y, int64_t y_row, void* y_out,
+               int64_t y_out_row, int y_heads, void* stream);
+
+/*
+ * A paged key/value cache: the rows of K and V live in num_pages pages of
+ * page_size rows, [num_pages, page_size, Hkv, D] bf16 (any strides, below),
+ * and a request's row t is row t % page_size of page table[b][t / page_size].
+ * Row t of page p is also called slot p * page_size + t.  H query heads share
+ * Hkv key/value heads: query head h reads key/value head h / (H / Hkv).
+ *
+ * The caller owns the pages, tables, lengths and the list of free pages, all
+ * in device memory; the pager owns its geometry, a status word and the
+ * workspace in which the parts of a split row are joined.  A pager belongs to
+ * the device that was current when it was created; calls with another device
+ * current return JFA_ERR_INVALID_ARG.  Its launches must be stream-ordered,
+ * replays of captured graphs among them: use one pager for each stream that
+ * decodes at the same time.  Calls allocate nothing, are asynchronous and may
+ * be captured; the pager must outlive the graph.
+ *
+ * What only the device can see -- lengths, table entries, slots -- is checked
+ * there: nothing outside the given tensors is read or written, the offending
+ * request, page or row is left out as each call says, and a bit is set in the
+ * status word (jfa_pager_status).
+ *
+ *   max_seqs    requests of one call, at most 16384
+ *   max_pages   columns of the table; (max_pages + 1) * page_size < 2^31
+ *   num_pages   pages of the cache; (num_pages + 1) * page_size < 2^31
+ *   page_size   rows of a page, any number >= 1
+ *   H, Hkv, D   heads (H a multiple of Hkv) and head dimension (64 or 128)
+ */
+typedef struct jfa_pager* jfa_pager_t;
+#define JFA_PAGER_MAX_SEQS 16384
+#define JFA_PAGER_NO_PAGES 1   /* status: a request found no free page */
+#define JFA_PAGER_BAD_LENGTH 2 /* status: a length, or its change, outside the table's or the rows' bounds */
+#define JFA_PAGER_BAD_PAGE 4   /* status: a page, slot or free count outside the cache */
+int jfa_pager_create(int max_seqs, int max_pages, int64_t num_pages, int page_size, int H, int Hkv,
+                     int D, void* stream, jfa_pager_t* out);
+/* Release a pager (synchronises the device). */
+int jfa_pager_destroy(jfa_pager_t pager);
+/* Read the status word (synchronises `stream`), then clear it: JFA_ERR_PAGES
+ * when a bit was set; *raw (optional) receives the bits. */
+int jfa_pager_status(jfa_pager_t pager, void* stream, int* raw);
+
+/*
+ * Block tables and slots from request lengths: request b of B goes from
+ * lens[b] to lens[b] + delta[b] rows.  delta > 0 appends that many new rows,
+ * delta < 0 drops the last ones (-lens[b]: the request is done).
+ *
+ * Pages that shrinking requests no longer reach are put on the free list
+ * first -- in the order of the requests, and within one by their place in the
+ * table, at free_list[n_free], free_list[n_free + 1] ... -- then the growing
+ * requests take what they need from its end, in the order of the requests and
+ * of their places.  A request of which the free list cannot serve all pages
+ * is left as it was, and so are the growing ones behind it that need a page
+ * (JFA_PAGER_NO_PAGES).  A request whose length or new length is negative or
+ * beyond max_pages * page_size, or whose new rows do not fit into `rows`, is
+ * left as it was (JFA_PAGER_BAD_LENGTH).  A count of free pages that is
+ * negative or, with the pages given back, above num_pages leaves everything
+ * as it was (JFA_PAGER_BAD_PAGE).
+ *
+ *   lens, delta   int32 [B]
+ *   lens_out      int32 [B], the new lengths; may be lens
+ *   table         int32 [B, max_pages], its rows table_row apart: entries of
+ *                 new pages are written, all others left as they were
+ *   free_list     int32 [num_pages]; n_free, n_free_out: int32 [1], may be equal
+ *   slots         int32 [rows]: the slot of each new row, requests one after
+ *                 the other; -1 for rows of a request left as it was, for rows
+ *                 on a page outside the cache (JFA_PAGER_BAD_PAGE) and for
+ *                 rows behind the last request's
+ *   positions     int32 [rows]: lens[b] + i for the i-th new row; 0 behind
+ *   row_offsets   int32 [B + 1]: the first new row of each request (delta > 0
+ *                 counts whether the request was left as it was or not)
+ * `rows` is the capacity of slots and positions.  Distinct outputs must not
+ * overlap.  A call whose lens_out and n_free_out are not its lens and n_free
+ * can be repeated with the same result.
+ */
+int jfa_paged_tables(jfa_pager_t pager, int B, const int32_t* lens, const int32_t* delta,
+                     int32_t* lens_out, int32_t* table, int64_t table_row, int32_t* free_list,
+                     const int32_t* n_free, int32_t* n_free_out, int64_t rows, int32_t* slots,
+                     int32_t* positions, int32_t* row_offsets, void* stream);
+
+/* Distances, in elements, of a cache's pages, rows and heads (D contiguous),
+ * the same for K and V; multiples of 8. */
+typedef struct jfa_pages {
+  void* k;
+  void* v;
+  int64_t page, row, head;
+} jfa_pages;
+
+/*
+ * Write new rows into the cache: k, v bf16 [rows, Hkv, D] (rows k_row / v_row
+ * elements apart, heads contiguous) go to slots[r]; rows with a negative slot
+ * are left out, and so are those with a slot outside the cache
+ * (JFA_PAGER_BAD_PAGE).  Slots of one call must be distinct, as
+ * jfa_paged_tables makes them.  With a rotary handle the keys are rotated on
+ * the way by positions (as for jfa_rotate), and so is q [rows, H, D] into
+ * q_out when q is given (every row, also those without a slot; q_out may be q
+ * with the same row distance).  rotary == NULL: positions, q and q_out are NULL.
+ */
+int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_row, const void* v,
+                     int64_t v_row, const int32_t* slots, const jfa_pages* pages,
+                     jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row,
+                     int64_t pos_axis, const void* q, int64_t q_row, void* q_out, int64_t q_out_row,
+                     void* stream);
+
+/*
+ * Attention of one new token per request over its cache:
+ *     out[b][h] = softmax(scale * q[b][h] K_b^T) V_b,  lse[h][b] = logsumexp
+ * over rows 0 .. lens[b]-1 of request b.  q bf16 [B, H, D] (rows q_row
+ * elements apart, heads contiguous), out bf16 [B, H, D], lse fp32 [H, B]
+ * (natural log, scale included, as jfa_fwd's).  lens[b] = 0: out 0, lse -inf;
+ * so too for a length outside 0 .. max_pages * page_size
+ * (JFA_PAGER_BAD_LENGTH).  Rows on a page outside the cache are left out
+ * (JFA_PAGER_BAD_PAGE).  Rows of a page behind lens[b] may hold anything, NaN
+ * and infinities included.  Results are the same, bit for bit, from call to
+ * call on the same arguments.
+ */
+int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, const jfa_pages* pages,
+                     const int32_t* table, int64_t table_row, const int32_t* lens, float scale,
+                     void* out, float* lse, void* stream);
 
 /* Human-readable text of a status code (static storage). */
 const char* jfa_status_string(int status);

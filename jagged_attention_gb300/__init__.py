@@ -8,6 +8,18 @@ is missing or the device is not an sm_103 GPU, calls raise.
     plan = Plan(kv_offsets, q_offsets=None, H=4, Lq=256, D=128)   # broadcast-Q
     out, lse = fwd(plan, q, k, v, scale)
     dq, dk, dv = bwd(plan, q, k, v, out, dout, lse, scale)
+
+Positions (before the forward, and back after the backward):
+
+    rotary = Rotary(*rotary_pairs(128, sections=(16, 24, 24)), D=128)
+    q, k = rotate(rotary, positions, q, k)              # positions int32 [rows, axes]
+    dq, dk = rotate(rotary, positions, dq, dk, inverse=True)
+
+Serving from a paged cache, one step:
+
+    lens, n_free, slots, positions, offsets = paged_tables(pager, lens, delta, table, free, n_free, rows=n)
+    q = paged_append(pager, k, v, slots, k_pages, v_pages, rotary=rotary, positions=positions, q=q)
+    out, lse = paged_decode(pager, q, k_pages, v_pages, table, lens, scale)
 """
 from __future__ import annotations
 
@@ -26,6 +38,7 @@ JFA_OK = 0
 STATUS_NAMES = {
     0: "JFA_OK", 1: "JFA_ERR_INVALID_ARG", 2: "JFA_ERR_UNSUPPORTED", 3: "JFA_ERR_BAD_OFFSETS",
     4: "JFA_ERR_ALIGNMENT", 5: "JFA_ERR_WORKSPACE", 6: "JFA_ERR_CUDA", 7: "JFA_ERR_DEVICE_TIMEOUT",
+    8: "JFA_ERR_PAGES",
 }
 BLOCK_M = BLOCK_N = 128
 PLAN_PACK_SHORT = 1  # JFA_PLAN_PACK_SHORT
@@ -37,6 +50,13 @@ PLAN_FWD_PAIRS = 64  # JFA_PLAN_FWD_PAIRS
 PLAN_STATIC = 128  # JFA_PLAN_STATIC
 PLAN_FWD_TWO = 256  # JFA_PLAN_FWD_TWO
 PLAN_FWD_ONE = 512  # JFA_PLAN_FWD_ONE
+ROTARY_INTERLEAVED = 1  # JFA_ROTARY_INTERLEAVED
+ROTATE_INVERSE = 1  # JFA_ROTATE_INVERSE
+ROTATE_X_FP32 = 2  # JFA_ROTATE_X_FP32
+ROTATE_Y_FP32 = 4  # JFA_ROTATE_Y_FP32
+PAGER_NO_PAGES = 1  # JFA_PAGER_NO_PAGES
+PAGER_BAD_LENGTH = 2  # JFA_PAGER_BAD_LENGTH
+PAGER_BAD_PAGE = 4  # JFA_PAGER_BAD_PAGE
 
 
 class JfaError(RuntimeError):
@@ -50,6 +70,15 @@ _lib_lock = threading.Lock()
 _vp = ctypes.c_void_p
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _ip = ctypes.POINTER(ctypes.c_int)
+_f64p = ctypes.POINTER(ctypes.c_double)
+_u64p = ctypes.POINTER(ctypes.c_uint64)
+
+
+class _Pages(ctypes.Structure):
+    """jfa_pages"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page", ctypes.c_int64),
+                ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
 
 
 def build(force: bool = False) -> Path:
@@ -97,6 +126,21 @@ def lib() -> ctypes.CDLL:
             L.jfa_plan_forward_pairs.argtypes = [_vp, _ip]
             L.jfa_plan_claims.argtypes = [_vp, _ip, _ip]
             L.jfa_plan_forward_form.argtypes = [_vp, _ip]
+            _cl, _cu = ctypes.c_int64, ctypes.c_uint
+            L.jfa_rotary_turns.argtypes = [_f64p, _ci, _u64p]
+            L.jfa_rotary_create.argtypes = [_f64p, _i32p, _ci, _ci, _cu, ctypes.POINTER(_vp)]
+            L.jfa_rotary_destroy.argtypes = [_vp]
+            L.jfa_rotate.argtypes = [_vp, _vp, _cl, _cl, _cl, _cu, _vp, _cl, _vp, _cl, _ci, _vp, _cl, _vp,
+                                     _cl, _ci, _vp]
+            L.jfa_pager_create.argtypes = [_ci, _ci, _cl, _ci, _ci, _ci, _ci, _vp, ctypes.POINTER(_vp)]
+            L.jfa_pager_destroy.argtypes = [_vp]
+            L.jfa_pager_status.argtypes = [_vp, _vp, _ip]
+            L.jfa_paged_tables.argtypes = [_vp, _ci, _vp, _vp, _vp, _vp, _cl, _vp, _vp, _vp, _cl, _vp, _vp,
+                                           _vp, _vp]
+            L.jfa_paged_append.argtypes = [_vp, _cl, _vp, _cl, _vp, _cl, _vp, _vp, _vp, _vp, _cl, _cl, _vp,
+                                           _cl, _vp, _cl, _vp]
+            L.jfa_paged_decode.argtypes = [_vp, _ci, _vp, _cl, _vp, _vp, _cl, _vp, ctypes.c_float, _vp, _vp,
+                                           _vp]
             L.jfa_status_string.argtypes = [ctypes.c_int]
             L.jfa_status_string.restype = ctypes.c_char_p
             for name in ("jfa_plan_create", "jfa_plan_create_ex", "jfa_plan_destroy", "jfa_plan_tiles", "jfa_build_tiles",
@@ -104,7 +148,9 @@ def lib() -> ctypes.CDLL:
                          "jfa_plan_device_status", "jfa_delta_in_tiles", "jfa_fwd_simple",
                          "jfa_bwd_simple", "jfa_simple_device_status", "jfa_simple_release",
                          "jfa_plan_selftest", "jfa_plan_forward_pairs", "jfa_plan_claims",
-                         "jfa_plan_forward_form"):
+                         "jfa_plan_forward_form", "jfa_rotary_turns", "jfa_rotary_create",
+                         "jfa_rotary_destroy", "jfa_rotate", "jfa_pager_create", "jfa_pager_destroy",
+                         "jfa_pager_status", "jfa_paged_tables", "jfa_paged_append", "jfa_paged_decode"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -427,3 +473,296 @@ def bwd_main(plan: Plan, q, k, v, dout, lse, scale: float, dq, dk, dv, workspace
                               _dev(dv, "dv", torch.bfloat16), workspace.data_ptr(),
                               workspace.numel() * workspace.element_size(), _stream(stream)),
            "jfa_bwd_main")
+
+
+def rotary_pairs(rotary_dim: int, sections=None, base: float = 10000.0):
+    """(inv_freq, axis) of the usual rotary positions: base^(-2i / rotary_dim) for
+    pair i, the pairs dealt to the axes in runs of ``sections`` (None: one axis)."""
+    half = rotary_dim // 2
+    sections = (half,) if sections is None else tuple(sections)
+    if rotary_dim % 2 or sum(sections) != half:
+        raise ValueError(f"sections {sections} must add up to {rotary_dim}/2 pairs")
+    inv_freq = float(base) ** (-2.0 * np.arange(half) / rotary_dim)
+    return inv_freq, np.repeat(np.arange(len(sections), dtype=np.int32), sections)
+
+
+def _pair_arrays(inv_freq, axis=None):
+    f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64)).reshape(-1)
+    a = np.zeros(f.size, np.int32) if axis is None else np.ascontiguousarray(np.asarray(axis, np.int32)).reshape(-1)
+    if a.size != f.size:
+        raise ValueError(f"{a.size} axes for {f.size} frequencies")
+    return f, a
+
+
+def rotary_turns(inv_freq) -> np.ndarray:
+    """Host-only (no GPU): the 64-bit turn fractions a Rotary holds (jfa_rotary_turns)."""
+    f, _ = _pair_arrays(inv_freq)
+    out = np.zeros(f.size, dtype=np.uint64)
+    _check(lib().jfa_rotary_turns(f.ctypes.data_as(_f64p), f.size, out.ctypes.data_as(_u64p)),
+           "jfa_rotary_turns")
+    return out
+
+
+class Rotary:
+    """A jfa_rotary_t: inverse frequencies and axes of the pairs of a head of D
+    values (see rotary_pairs).  Holds no device memory."""
+
+    def __init__(self, inv_freq, axis=None, *, D: int, interleaved: bool = False):
+        self._h = None
+        f, a = _pair_arrays(inv_freq, axis)
+        self.D, self.pairs, self.interleaved = D, f.size, interleaved
+        self.axes = int(a.max()) + 1 if a.size else 1
+        h = _vp()
+        _check(lib().jfa_rotary_create(f.ctypes.data_as(_f64p), _i32ptr(a), f.size, D,
+                                       ROTARY_INTERLEAVED if interleaved else 0, ctypes.byref(h)),
+               "jfa_rotary_create")
+        self._h = h
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise RuntimeError("rotary already destroyed")
+        return self._h
+
+    def close(self):
+        if self._h is not None:
+            _check(lib().jfa_rotary_destroy(self._h), "jfa_rotary_destroy")
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> tuple[int, int]:
+    """(address, elements from row to row) of a tensor [rows, heads, D] whose heads are contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise TypeError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if t.numel() and (st[2] != 1 or (shape[1] > 1 and st[1] != shape[2])):
+        raise ValueError(f"the heads of {name} must be contiguous")
+    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _ints(t: torch.Tensor, name: str, shape, device) -> int:
+    """Address of a contiguous int32 tensor."""
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be {torch.int32}, got {t.dtype}")
+    if t.device != device:
+        raise TypeError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _table(t: torch.Tensor, pager, B: int, device) -> tuple[int, int]:
+    """(address, entries from row to row) of a block table [B, max_pages]."""
+    if t.dtype != torch.int32 or t.device != device:
+        raise TypeError(f"table must be {torch.int32} on {device}, got {t.dtype} on {t.device}")
+    if t.shape != (B, pager.max_pages) or t.stride(1) != 1 and pager.max_pages > 1:
+        raise ValueError(f"table must be [{B}, {pager.max_pages}] with contiguous rows, got {tuple(t.shape)}")
+    return t.data_ptr(), t.stride(0) if B > 1 else pager.max_pages
+
+
+def _positions(positions: torch.Tensor, rotary: Rotary, rows: int, device) -> tuple[int, int, int]:
+    """(address, row distance, axis distance): int32 [rows, axes], or [rows] for one position on every axis."""
+    if positions.dtype != torch.int32 or positions.device != device:
+        raise TypeError(f"positions must be {torch.int32} on {device}, got {positions.dtype} on {positions.device}")
+    if positions.dim() == 1 and positions.shape[0] == rows:
+        return positions.data_ptr(), positions.stride(0), 0
+    if positions.dim() != 2 or positions.shape[0] != rows or positions.shape[1] < rotary.axes:
+        raise ValueError(f"positions must be [{rows}] or [{rows}, {rotary.axes}], got {tuple(positions.shape)}")
+    return positions.data_ptr(), positions.stride(0), positions.stride(1)
+
+
+def _current(device: torch.device):
+    """Launches go to the current device: the tensors must be there."""
+    if device.type != "cuda":
+        raise TypeError(f"tensors must be CUDA tensors, got {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out=None, k_out=None,
+           stream=None):
+    """q (and k) [rows, heads, D], bf16 or fp32, rotated by their positions through
+    jfa_rotate; ``inverse`` rotates back, which takes dq and dk (of the rotated
+    q and k) to the gradients of the unrotated ones.  Rows may lie apart (slices
+    of a fused projection).  q_out / k_out may be q / k.  Returns q_out, or
+    (q_out, k_out) with k."""
+    dev = q.device
+    _current(dev)
+    if q.dim() != 3 or k is not None and k.dim() != 3:
+        raise ValueError("q and k must be [rows, heads, D]")
+    rows = q.shape[0]
+    flags = ROTATE_INVERSE if inverse else 0
+    address, pos_row, pos_axis = _positions(positions, rotary, rows, dev)
+    args = []
+    for name, t, out, bit in (("q", q, q_out, ROTATE_X_FP32), ("k", k, k_out, ROTATE_Y_FP32)):
+        if t is None:
+            if out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            args += [None, 0, None, 0, 0]
+            continue
+        if t.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"{name} must be {torch.bfloat16} or {torch.float32}, got {t.dtype}")
+        heads = t.shape[1]
+        shape = (rows, heads, rotary.D)
+        if out is None:
+            out = torch.empty(shape, dtype=t.dtype, device=dev)
+        if name == "q":
+            q_out = out
+        else:
+            k_out = out
+        if t.dtype == torch.float32:
+            flags |= bit
+        args += [*_rows(t, name, shape, t.dtype, dev), *_rows(out, f"{name}_out", shape, t.dtype, dev), heads]
+    _check(lib().jfa_rotate(rotary.handle, address, pos_row, pos_axis, rows, flags, *args, _stream(stream)),
+           "jfa_rotate")
+    return q_out if k is None else (q_out, k_out)
+
+
+class Pager:
+    """A jfa_pager_t: the geometry of a paged key/value cache, its status word and
+    workspace on the current device.  One pager for each stream that decodes at
+    the same time: its launches must be stream-ordered."""
+
+    def __init__(self, *, max_seqs: int, max_pages: int, num_pages: int, page_size: int, H: int, Hkv: int,
+                 D: int, stream=None):
+        self._h = None
+        self.max_seqs, self.max_pages, self.num_pages, self.page_size = max_seqs, max_pages, num_pages, page_size
+        self.H, self.Hkv, self.D = H, Hkv, D
+        h = _vp()
+        _check(lib().jfa_pager_create(max_seqs, max_pages, num_pages, page_size, H, Hkv, D,
+                                      _stream(stream) if torch.cuda.is_available() else None, ctypes.byref(h)),
+               "jfa_pager_create")
+        self._h = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise RuntimeError("pager already destroyed")
+        return self._h
+
+    def status(self, stream=None) -> int:
+        """The status bits (PAGER_*) set since the last call, which it clears."""
+        raw = ctypes.c_int()
+        rc = lib().jfa_pager_status(self.handle, _stream(stream), ctypes.byref(raw))
+        if rc != 8:  # JFA_ERR_PAGES: the bits say what
+            _check(rc, "jfa_pager_status")
+        return raw.value
+
+    def close(self):
+        if self._h is not None:
+            _check(lib().jfa_pager_destroy(self._h), "jfa_pager_destroy")
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _pages(pager: Pager, k_pages, v_pages) -> _Pages:
+    shape = (pager.num_pages, pager.page_size, pager.Hkv, pager.D)
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != torch.bfloat16 or t.device != pager.device:
+            raise TypeError(f"{name} must be {torch.bfloat16} on {pager.device}, got {t.dtype} on {t.device}")
+        if t.shape != shape or t.stride(3) != 1:
+            raise ValueError(f"{name} must have shape {shape} with contiguous rows, got {tuple(t.shape)}")
+    st = k_pages.stride()
+    if st != v_pages.stride():
+        raise ValueError(f"k_pages and v_pages must have the same strides, got {st} and {v_pages.stride()}")
+    return _Pages(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2])
+
+
+def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: int, lens_out=None,
+                 n_free_out=None, slots=None, positions=None, row_offsets=None, stream=None):
+    """Lengths, block table, free list, slots and positions of a step through
+    jfa_paged_tables: request b goes from lens[b] to lens[b] + delta[b] rows.
+    table [B, max_pages] and free_list [num_pages] are updated in place; lens and
+    n_free too where lens_out and n_free_out are given as them.  Returns
+    (lens_out, n_free_out, slots, positions, row_offsets)."""
+    dev = pager.device
+    B = lens.shape[0]
+    empty = lambda n: torch.empty((n,), dtype=torch.int32, device=dev)  # noqa: E731
+    if lens_out is None:
+        lens_out = empty(B)
+    if n_free_out is None:
+        n_free_out = empty(1)
+    if slots is None:
+        slots = empty(rows)
+    if positions is None:
+        positions = empty(rows)
+    if row_offsets is None:
+        row_offsets = empty(B + 1)
+    tab, tab_row = _table(table, pager, B, dev)
+    _check(lib().jfa_paged_tables(
+        pager.handle, B, _ints(lens, "lens", (B,), dev), _ints(delta, "delta", (B,), dev),
+        _ints(lens_out, "lens_out", (B,), dev), tab, tab_row,
+        _ints(free_list, "free_list", (pager.num_pages,), dev), _ints(n_free, "n_free", (1,), dev),
+        _ints(n_free_out, "n_free_out", (1,), dev), rows, _ints(slots, "slots", (rows,), dev),
+        _ints(positions, "positions", (rows,), dev), _ints(row_offsets, "row_offsets", (B + 1,), dev),
+        _stream(stream)), "jfa_paged_tables")
+    return lens_out, n_free_out, slots, positions, row_offsets
+
+
+def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary | None = None,
+                 positions=None, q=None, q_out=None, stream=None):
+    """New rows k, v [rows, Hkv, D] into the pages at their slots through
+    jfa_paged_append; with ``rotary``, k and q [rows, H, D] rotated by
+    ``positions`` on the way.  Returns q_out (which may be q), None without q."""
+    dev = pager.device
+    rows = k.shape[0]
+    shape = (rows, pager.Hkv, pager.D)
+    if rotary is None and (positions is not None or q is not None):
+        raise ValueError("positions and q go with rotary")
+    pos, q_args = (None, 0, 0), (None, 0, None, 0)
+    if rotary is not None:
+        if positions is None:
+            raise ValueError("rotary without positions")
+        pos = _positions(positions, rotary, rows, dev)
+    if q is not None:
+        q_shape = (rows, pager.H, pager.D)
+        if q_out is None:
+            q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
+        q_args = (*_rows(q, "q", q_shape, torch.bfloat16, dev), *_rows(q_out, "q_out", q_shape, torch.bfloat16, dev))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    pages = _pages(pager, k_pages, v_pages)
+    _check(lib().jfa_paged_append(
+        pager.handle, rows, *_rows(k, "k", shape, torch.bfloat16, dev), *_rows(v, "v", shape, torch.bfloat16, dev),
+        _ints(slots, "slots", (rows,), dev), ctypes.byref(pages), None if rotary is None else rotary.handle,
+        *pos, *q_args, _stream(stream)), "jfa_paged_append")
+    return q_out
+
+
+def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *, out=None, lse=None,
+                 stream=None):
+    """O (bf16 [B, H, D]) and LSE (fp32 [H, B]) of one new token per request over
+    its cached rows, through jfa_paged_decode.  q [B, H, D]; rows may lie apart."""
+    dev = pager.device
+    B = q.shape[0]
+    shape = (B, pager.H, pager.D)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((pager.H, B), dtype=torch.float32, device=dev)
+    elif lse.dtype != torch.float32 or lse.device != dev or lse.shape != (pager.H, B) or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous float32 [{pager.H}, {B}] on {dev}")
+    address, out_row = _rows(out, "out", shape, torch.bfloat16, dev)
+    if out_row != pager.H * pager.D:
+        raise ValueError("out must be contiguous")
+    pages = _pages(pager, k_pages, v_pages)
+    _check(lib().jfa_paged_decode(pager.handle, B, *_rows(q, "q", shape, torch.bfloat16, dev), ctypes.byref(pages),
+                                  *_table(table, pager, B, dev), _ints(lens, "lens", (B,), dev), float(scale),
+                                  address, lse.data_ptr(), _stream(stream)), "jfa_paged_decode")
+    return out, lse

@@ -263,6 +263,7 @@ const char* jfa_status_string(int s) {
     case JFA_ERR_WORKSPACE: return "workspace missing or too small";
     case JFA_ERR_CUDA: return "CUDA runtime error";
     case JFA_ERR_DEVICE_TIMEOUT: return "device wait timed out";
+    case JFA_ERR_PAGES: return "bad lengths, pages or slots, or no free page";
     default: return "unknown status";
   }
 }
