@@ -228,7 +228,7 @@ def prepare(case, seed):
         s.update(q=q if hq else None, k=k, v=v, slots=slots, k_pages=_normal((pages, page, hk, D), g),
                  v_pages=_normal((pages, page, hk, D), g))
         if own:
-            s["pager"] = s["jfa"].Pager(max_seqs=n, max_pages=pages, num_pages=pages, page_size=page,
+            s["pager"] = s["jfa"].Pager(max_seqs=1, max_pages=pages, num_pages=pages, page_size=page,
                                         H=max(hq, hk), Hkv=hk, D=D)
         return s
     B, hq, hk, D, page = (case[k] for k in ("B", "hq", "hk", "D", "page"))
