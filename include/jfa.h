@@ -503,13 +503,16 @@ int jfa_rotate(jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row, i
  * Hkv key/value heads: query head h reads key/value head h / (H / Hkv).
  *
  * The caller owns the pages, tables, lengths and the list of free pages, all
- * in device memory; the pager owns its geometry, a status word and the
- * workspace in which the parts of a split row are joined.  A pager belongs to
- * the device that was current when it was created; calls with another device
+ * in device memory, and the pager's block: device memory of at least
+ * jfa_pager_block_bytes bytes, 256-byte aligned, which holds the status word
+ * and the workspace in which the parts of a split row are joined.  Creating
+ * the pager clears part of it on `stream`; it belongs to the pager until that
+ * is destroyed and its launches and graphs are done.  A pager belongs to the
+ * device that was current when it was created; calls with another device
  * current return JFA_ERR_INVALID_ARG.  Its launches must be stream-ordered,
  * replays of captured graphs among them: use one pager for each stream that
- * decodes at the same time.  Calls allocate nothing, are asynchronous and may
- * be captured; the pager must outlive the graph.
+ * decodes at the same time.  Nothing here allocates device memory; calls are
+ * asynchronous and may be captured.
  *
  * What only the device can see -- lengths, table entries, slots -- is checked
  * there: nothing outside the given tensors is read or written, the offending
@@ -527,9 +530,10 @@ typedef struct jfa_pager* jfa_pager_t;
 #define JFA_PAGER_NO_PAGES 1   /* status: a request found no free page */
 #define JFA_PAGER_BAD_LENGTH 2 /* status: a length, or its change, outside the table's or the rows' bounds */
 #define JFA_PAGER_BAD_PAGE 4   /* status: a page, slot or free count outside the cache */
+size_t jfa_pager_block_bytes(int H, int Hkv, int D); /* on the current device; 0: unsupported */
 int jfa_pager_create(int max_seqs, int max_pages, int64_t num_pages, int page_size, int H, int Hkv,
-                     int D, void* stream, jfa_pager_t* out);
-/* Release a pager (synchronises the device). */
+                     int D, void* block, size_t block_bytes, void* stream, jfa_pager_t* out);
+/* Release a pager (its block stays the caller's). */
 int jfa_pager_destroy(jfa_pager_t pager);
 /* Read the status word (synchronises `stream`), then clear it: JFA_ERR_PAGES
  * when a bit was set; *raw (optional) receives the bits. */

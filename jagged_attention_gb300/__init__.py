@@ -132,7 +132,10 @@ def lib() -> ctypes.CDLL:
             L.jfa_rotary_destroy.argtypes = [_vp]
             L.jfa_rotate.argtypes = [_vp, _vp, _cl, _cl, _cl, _cu, _vp, _cl, _vp, _cl, _ci, _vp, _cl, _vp,
                                      _cl, _ci, _vp]
-            L.jfa_pager_create.argtypes = [_ci, _ci, _cl, _ci, _ci, _ci, _ci, _vp, ctypes.POINTER(_vp)]
+            L.jfa_pager_block_bytes.argtypes = [_ci, _ci, _ci]
+            L.jfa_pager_block_bytes.restype = ctypes.c_size_t
+            L.jfa_pager_create.argtypes = [_ci, _ci, _cl, _ci, _ci, _ci, _ci, _vp, ctypes.c_size_t, _vp,
+                                           ctypes.POINTER(_vp)]
             L.jfa_pager_destroy.argtypes = [_vp]
             L.jfa_pager_status.argtypes = [_vp, _vp, _ip]
             L.jfa_paged_tables.argtypes = [_vp, _ci, _vp, _vp, _vp, _vp, _cl, _vp, _vp, _vp, _cl, _vp, _vp,
@@ -629,21 +632,22 @@ def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out
 
 
 class Pager:
-    """A jfa_pager_t: the geometry of a paged key/value cache, its status word and
-    workspace on the current device.  One pager for each stream that decodes at
-    the same time: its launches must be stream-ordered."""
+    """A jfa_pager_t: the geometry of a paged key/value cache, with its status word
+    and workspace in ``block``, on the current device.  One pager for each stream
+    that decodes at the same time: its launches must be stream-ordered."""
 
     def __init__(self, *, max_seqs: int, max_pages: int, num_pages: int, page_size: int, H: int, Hkv: int,
                  D: int, stream=None):
         self._h = None
         self.max_seqs, self.max_pages, self.num_pages, self.page_size = max_seqs, max_pages, num_pages, page_size
         self.H, self.Hkv, self.D = H, Hkv, D
-        h = _vp()
-        _check(lib().jfa_pager_create(max_seqs, max_pages, num_pages, page_size, H, Hkv, D,
-                                      _stream(stream) if torch.cuda.is_available() else None, ctypes.byref(h)),
-               "jfa_pager_create")
-        self._h = h
         self.device = torch.device("cuda", torch.cuda.current_device())
+        n = lib().jfa_pager_block_bytes(H, Hkv, D)
+        self.block = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+        h = _vp()
+        _check(lib().jfa_pager_create(max_seqs, max_pages, num_pages, page_size, H, Hkv, D, self.block.data_ptr(), n,
+                                      _stream(stream), ctypes.byref(h)), "jfa_pager_create")
+        self._h = h
 
     @property
     def handle(self):

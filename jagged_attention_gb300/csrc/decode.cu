@@ -1,0 +1,578 @@
+// decode.cu -- attention of one new token per request over the paged cache.
+//
+// Mathematics: with s_t = scale q . k_t, a stretch of rows yields the running
+// maximum m, the sum l = sum exp(s_t - m) and O = sum exp(s_t - m) v_t; stretches
+// of one row of queries join as m = max m_i, l = sum l_i exp(m_i - m), likewise O.
+// Everything but the operands of the tensor cores is fp32.  A weight goes into
+// the product with V as the sum of two bf16 values (its rounding and what that
+// leaves), 16 bits in all: one bf16 alone would add as much error to the output
+// as its own rounding to bf16 does.
+//
+// Bound: every cached row is read once, 4 D bytes for 4 D G flops (G query heads
+// to a key/value head), so memory bandwidth bounds it for G up to the hundreds.
+// The products use mma.sync, transposed -- rows of the cache are the long side
+// of the 16 x 8 tile, up to 8 query heads (16: two tiles) the short one -- which
+// wastes least of the tile and leaves the cache rows in the layout that
+// ldmatrix reads; tcgen05 would want 64 or 128 query rows per product.
+//
+// Split: a tile is 16 cached rows for one key/value head (and, where G > 16, one
+// part of its query heads).  All tiles of all requests in the order (request,
+// head, row) are dealt in equal contiguous shares to the CTAs, and a CTA's share
+// to its warps; a warp streams its tiles through its own ring of cp.async
+// stages, over the ends of rows and requests, and meets no barrier on the way.
+// What is left at the ends of the warps' shares is joined in shared memory, what
+// is left at the ends of the CTAs' shares in global memory by the CTA that
+// arrives last, in the order of the shares: the same arguments give the same
+// bits.  So one row of any length and thousands of short ones spread alike,
+// without a schedule from the host.
+#include <climits>
+
+#include "kernels.h"
+#include "paged.h"
+#include "sm103_ptx.cuh"
+
+namespace jfa {
+namespace {
+
+constexpr int kTile = 16;        // cached rows of a tile
+constexpr int kDecodeWarps = 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int D, int NT>  // NT: tiles of 8 query heads
+struct DecodeCfg {
+  static constexpr int kHeads = 8 * NT;
+  static constexpr int kStageBytes = 2 * kTile * D * 2;  // K and V
+  static constexpr int kStages = D == 128 && NT == 1 ? 3 : 2;
+  static constexpr int kOutBytes = kHeads * D * 4;  // a stretch's O
+  static_assert(kOutBytes <= kStageBytes, "a used stage holds a stretch's O");
+  static constexpr int kWarpBytes = kStages * kStageBytes + kOutBytes;
+  static constexpr int kSmemBytes = kDecodeWarps * kWarpBytes;
+  static constexpr int kCtasPerSm = D == 64 ? 2 : 1;
+};
+
+// Where a warp stands: tile t of n of the rows of (request b, virtual head vh).
+struct Cursor {
+  int b, vh, t, n, len;
+};
+
+// A stretch that does not hold all tiles of its (b, vh): tiles [t0, t1) of n.
+struct Stretch {
+  int64_t u0;  // index of the tile 0 of (b, vh) among all tiles
+  int b, vh, t0, t1, n;  // n 0: none
+};
+
+template <int D, int NT>
+struct DecodeShared {
+  Stretch part[2 * kDecodeWarps];                 // first and last of each warp
+  float m[2 * kDecodeWarps][8 * NT], l[2 * kDecodeWarps][8 * NT];
+  int64_t scan[kDecodeWarps];
+  int64_t start_tiles[kDecodeWarps];  // tiles of the requests before a warp's first
+  int start_b[kDecodeWarps];
+  uint32_t live[kDecodeWarps][DecodeCfg<D, NT>::kStages];  // rows of a stage that count
+  int arrived;
+};
+
+__device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
+  const int len = __ldg(a.lens + b);
+  return len < 0 || len > a.max_pages * a.div.d ? 0 : len;
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  const int bytes = take ? 16 : 0;  // 0: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Place of value (head, d) of a stretch's O in shared memory: the exclusive or
+// sends the 32 lanes of a fragment to 32 banks and keeps runs of 8 together.
+template <int D>
+__device__ __forceinline__ int o_at(int head, int d) {
+  return head * D + (d ^ (((head >> 1) & 3) << 3));
+}
+
+// Shares of `total` dealt to n takers: taker i's first.
+__device__ __forceinline__ int64_t share(int64_t total, int n, int i) {
+  const int64_t per = total / n, more = total - per * n;
+  return per * i + min(int64_t(i), more);
+}
+// The taker of item u.
+__device__ __forceinline__ int taker(int64_t total, int n, int64_t u) {
+  const int64_t per = total / n, more = total - per * n;
+  const int64_t big = more * (per + 1);
+  return static_cast<int>(u < big ? u / (per + 1) : more + (u - big) / per);
+}
+
+// Query heads [first, first + count) of virtual head vh, and its key/value head.
+__device__ __forceinline__ void heads_of(const DecodeArgs& a, int vh, int* kv, int* first, int* count) {
+  const int group = a.H / a.Hkv;
+  *kv = vh / a.parts;
+  const int g0 = (vh - *kv * a.parts) * a.part_heads;
+  *first = *kv * group + g0;
+  *count = min(a.part_heads, group - g0);
+}
+
+// 4 values of out, normalised already.
+__device__ __forceinline__ void store_out4(const DecodeArgs& a, int D, int b, int head, int d, float4 o) {
+  *reinterpret_cast<uint2*>(a.out + (int64_t(b) * a.H + head) * D + d) =
+      make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+}
+__device__ __forceinline__ float lse_of(float m, float l) { return m * kLn2 + logf(l); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kDecodeWarps * 32, DecodeCfg<D, NT>::kCtasPerSm)
+decode_kernel(const __grid_constant__ DecodeArgs a) {
+  using C = DecodeCfg<D, NT>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ DecodeShared<D, NT> sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int vheads = a.Hkv * a.parts;
+
+  // ---- tiles of all requests, and where this CTA's warps begin
+  const int slab = (a.B + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
+  const int b_lo = min(a.B, tid * slab), b_hi = min(a.B, b_lo + slab);
+  int64_t mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(length_of(a, b));
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) sh.scan[warp] = upto;
+  if (tid < 2 * kDecodeWarps) sh.part[tid].n = 0;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecodeWarps; ++w) {
+    if (w < warp) upto += sh.scan[w];
+    total += sh.scan[w];
+  }
+  total *= vheads;
+  // few tiles: fewer CTAs, so that each warp has at least one
+  const int ctas = static_cast<int>(max(int64_t(1), min(int64_t(gridDim.x), total / kDecodeWarps)));
+  const int cta = blockIdx.x;
+  int64_t cta_lo = 0, cta_n = 0;
+  if (cta < ctas) {
+    cta_lo = share(total, ctas, cta);
+    cta_n = share(total, ctas, cta + 1) - cta_lo;
+  }
+  {
+    const int64_t before = upto - mine;
+#pragma unroll
+    for (int w = 0; w < kDecodeWarps; ++w) {
+      const int64_t u = cta_lo + share(cta_n, kDecodeWarps, w);
+      if (before * vheads <= u && u < upto * vheads) {
+        int64_t tiles = before;
+        int b = b_lo;
+        for (; b + 1 < b_hi; ++b) {
+          const int n = tiles_of(length_of(a, b));
+          if (u < (tiles + n) * vheads) break;
+          tiles += n;
+        }
+        sh.start_b[w] = b;
+        sh.start_tiles[w] = tiles;
+      }
+    }
+  }
+  __syncthreads();
+
+  const int64_t lo = cta_lo + share(cta_n, kDecodeWarps, warp);
+  const int64_t hi = cta_lo + share(cta_n, kDecodeWarps, warp + 1);
+  const int64_t count = hi - lo;
+
+  unsigned char* ring = smem + warp * C::kWarpBytes;
+  const uint32_t ring_addr = smem_u32(ring);
+  float* park = reinterpret_cast<float*>(ring + C::kStages * C::kStageBytes);
+
+  if (count > 0) {
+    Cursor at;  // of the tile whose rows are looked up next
+    at.b = sh.start_b[warp];
+    at.len = length_of(a, at.b);
+    at.n = tiles_of(at.len);
+    {
+      const int64_t r = lo - sh.start_tiles[warp] * vheads;
+      at.vh = static_cast<int>(r / at.n);
+      at.t = static_cast<int>(r - int64_t(at.vh) * at.n);
+    }
+    Cursor now = at;  // of the tile computed next
+
+    auto advance = [&](Cursor& c) {  // there is a next tile
+      if (++c.t < c.n) return;
+      c.t = 0;
+      if (++c.vh < vheads) return;
+      c.vh = 0;
+      do {
+        ++c.b;
+        c.len = length_of(a, c.b);
+        c.n = tiles_of(c.len);
+      } while (c.n == 0 && c.b + 1 < a.B);
+    };
+    // offset of row lane % 16 of a tile, -1 where there is none
+    auto look_up = [&](const Cursor& c) -> int64_t {
+      const int pos = c.t * kTile + (lane & 15);
+      if (pos >= c.len) return -1;
+      const int i = a.div.quot(pos);
+      const int page = __ldg(a.table + c.b * a.table_row + i);
+      if (page < 0 || page >= a.num_pages) {
+        atomicOr(a.status, kPagerBadPage);
+        return -1;
+      }
+      return page * a.page + (pos - i * a.div.d) * a.row + (c.vh / a.parts) * a.head;
+    };
+    auto issue = [&](int stage, int64_t off) {
+      constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of an instruction
+      const uint32_t live = __ballot_sync(~0u, off >= 0);
+      if (lane == 0) sh.live[warp][stage] = live;
+      const uint32_t k_at = ring_addr + stage * C::kStageBytes, v_at = k_at + kTile * D * 2;
+      const int c = lane % kLanes;
+#pragma unroll
+      for (int i = 0; i < kTile / kRows; ++i) {
+        const int r = i * kRows + lane / kLanes;
+        const int64_t o = __shfl_sync(~0u, off, r);
+        const bool take = o >= 0;
+        const int64_t src = (take ? o : 0) + c * 8;
+        const uint32_t dst = r * (D * 2) + ((c ^ (r & 7)) << 4);
+        cp_async16(k_at + dst, a.k + src, take);
+        cp_async16(v_at + dst, a.v + src, take);
+      }
+    };
+
+    int64_t asked = 0;  // tiles looked up
+    int64_t off = look_up(at);
+    asked = 1;
+#pragma unroll
+    for (int s = 0; s < C::kStages; ++s) {
+      if (s < count) {
+        issue(s, off);
+        if (asked < count) {
+          advance(at);
+          off = look_up(at);
+          ++asked;
+        }
+      }
+      cp_async_commit();
+    }
+
+    float o_acc[D / 16][NT][4], m[NT][2], l[NT][2];
+    uint32_t qf[D / 16][NT][2];
+    const int g = lane >> 2, j = lane & 3;
+    int stage = 0, t0 = 0, first = 0, heads = 0, kv = 0;
+    bool fresh = true;
+    const float scale_log2 = a.scale * kLog2e;
+
+    for (int64_t done = 0; done < count; ++done) {
+      if (fresh) {
+        fresh = false;
+        t0 = now.t;
+        heads_of(a, now.vh, &kv, &first, &heads);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const bool have = 8 * n + g < heads;
+          const uint16_t* q = a.q + now.b * a.q_row + int64_t(first + 8 * n + (have ? g : 0)) * D + 2 * j;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            qf[ks][n][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks)) : 0u;
+            qf[ks][n][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks + 8)) : 0u;
+          }
+          m[n][0] = m[n][1] = -INFINITY;
+          l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o_acc[i][n][e] = 0.f;
+        }
+      }
+      cp_async_wait<C::kStages - 1>();
+      __syncwarp();
+      const uint32_t k_at = ring_addr + stage * C::kStageBytes, v_at = k_at + kTile * D * 2;
+      const uint32_t live = sh.live[warp][stage];
+
+      // scores of 16 rows (g, g + 8) and heads (2 j, 2 j + 1)
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+      {
+        const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t kf[4];
+          ldmatrix4(kf, k_at + r * (D * 2) + (((2 * ks + c) ^ (r & 7)) << 4));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_16816(s[n], kf, qf[ks][n][0], qf[ks][n][1]);
+        }
+      }
+      const bool live0 = (live >> g) & 1, live1 = (live >> (g + 8)) & 1;
+      uint32_t hi_f[NT][2], lo_f[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float top[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[n][e] = live0 ? s[n][e] * scale_log2 : -INFINITY;
+          s[n][2 + e] = live1 ? s[n][2 + e] * scale_log2 : -INFINITY;
+          top[e] = fmaxf(s[n][e], s[n][2 + e]);
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          top[0] = fmaxf(top[0], __shfl_xor_sync(~0u, top[0], x));
+          top[1] = fmaxf(top[1], __shfl_xor_sync(~0u, top[1], x));
+        }
+        if (__any_sync(~0u, top[0] > m[n][0] || top[1] > m[n][1])) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float up = fmaxf(m[n][e], top[e]);
+            // all scores so far -inf: there is nothing to keep
+            const float keep = m[n][e] == -INFINITY ? 0.f : fast_exp2(m[n][e] - up);
+            m[n][e] = up;
+            l[n][e] *= keep;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o_acc[i][n][e] *= keep, o_acc[i][n][2 + e] *= keep;
+          }
+        }
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float ref = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
+          p[e] = fast_exp2(s[n][e] - ref);
+        }
+        l[n][0] += p[0] + p[2];
+        l[n][1] += p[1] + p[3];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t w = pack_bf16x2(p[2 * e], p[2 * e + 1]);
+          const float r0 = p[2 * e] - __uint_as_float(w << 16);
+          const float r1 = p[2 * e + 1] - __uint_as_float(w & 0xffff0000u);
+          hi_f[n][e] = transpose8x8(w);
+          lo_f[n][e] = transpose8x8(pack_bf16x2(r0, r1));
+        }
+      }
+      {
+        const int r = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t vf[4];
+          ldmatrix4_trans(vf, v_at + r * (D * 2) + (((2 * i + c) ^ (r & 7)) << 4));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_16816(o_acc[i][n], vf, hi_f[n][0], hi_f[n][1]);
+            mma_16816(o_acc[i][n], vf, lo_f[n][0], lo_f[n][1]);
+          }
+        }
+      }
+      __syncwarp();  // the stage is read
+
+      const bool row_ends = now.t + 1 == now.n, share_ends = done + 1 == count;
+      if (row_ends || share_ends) {
+        const bool whole = row_ends && t0 == 0;
+        // a part of a row: the share's first waits in the park, its last in the ring
+        const bool parked = !whole && !share_ends;
+        if (share_ends) cp_async_wait<0>();
+        float* to = parked ? park : reinterpret_cast<float*>(ring + (share_ends ? 0 : stage * C::kStageBytes));
+        const int slot = 2 * warp + (parked ? 0 : 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(~0u, l[n][e], x);
+            const int head = 8 * n + 2 * j + e;
+            if (whole) {
+              if (g == 0 && head < heads) a.lse[int64_t(first + head) * a.B + now.b] = lse_of(m[n][e], l[n][e]);
+            } else if (g == 0) {
+              sh.m[slot][head] = m[n][e];
+              sh.l[slot][head] = l[n][e];
+            }
+            const float by = !whole ? 1.f : l[n][e] == 0.f ? 0.f : 1.f / l[n][e];
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              to[o_at<D>(head, 16 * i + g)] = o_acc[i][n][e] * by;
+              to[o_at<D>(head, 16 * i + g + 8)] = o_acc[i][n][2 + e] * by;
+            }
+          }
+        }
+        __syncwarp();
+        if (whole) {
+          constexpr int kLanes = D / 4;
+          for (int h = lane / kLanes; h < heads; h += 32 / kLanes) {
+            const int d = 4 * (lane % kLanes);
+            store_out4(a, D, now.b, first + h, d, *reinterpret_cast<const float4*>(to + o_at<D>(h, d)));
+          }
+          __syncwarp();
+        } else if (lane == 0) {
+          sh.part[slot] = {lo + done - now.t, now.b, now.vh, t0, now.t + 1, now.n};
+        }
+        fresh = true;
+      }
+      if (!share_ends) advance(now);
+
+      if (done + C::kStages < count) {
+        issue(stage, off);
+        if (asked < count) {
+          advance(at);
+          off = look_up(at);
+          ++asked;
+        }
+      }
+      cp_async_commit();
+      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+  }
+
+  // ---- requests without rows
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (length_of(a, b) > 0) continue;
+    if (tid == 0 && __ldg(a.lens + b) != 0) atomicOr(a.status, kPagerBadLength);
+    for (int i = tid; i < a.H * (D / 4); i += kDecodeWarps * 32)
+      store_out4(a, D, b, i / (D / 4), 4 * (i % (D / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
+    for (int h = tid; h < a.H; h += kDecodeWarps * 32) a.lse[int64_t(h) * a.B + b] = -INFINITY;
+  }
+  if (cta_n == 0) return;
+  __syncthreads();
+
+  // ---- parts of a row within this CTA's share
+  auto part_o = [&](int slot) -> const float* {
+    const unsigned char* base = smem + (slot >> 1) * C::kWarpBytes;
+    return reinterpret_cast<const float*>(slot & 1 ? base : base + C::kStages * C::kStageBytes);
+  };
+  constexpr int kQuads = D / 4;
+  int open[2] = {-1, -1};  // parts that go on in other CTAs, by their place in global memory
+  for (int s = 0; s < 2 * kDecodeWarps;) {
+    if (sh.part[s].n == 0) {
+      ++s;
+      continue;
+    }
+    const Stretch p = sh.part[s];
+    int end = s, t1 = p.t1;  // slots [s, end) of the same (b, vh)
+    for (int x = s; x < 2 * kDecodeWarps; ++x) {
+      if (sh.part[x].n == 0) continue;
+      if (sh.part[x].b != p.b || sh.part[x].vh != p.vh) break;
+      end = x + 1;
+      t1 = sh.part[x].t1;
+    }
+    const bool whole = p.t0 == 0 && t1 == p.n;
+    const int place = p.t0 == 0 ? 1 : 0;
+    int kv, first, heads;
+    heads_of(a, p.vh, &kv, &first, &heads);
+    float* o_out = a.part_o + (int64_t(cta) * 2 + place) * (C::kHeads * D);
+    float* ml_out = a.part_ml + (int64_t(cta) * 2 + place) * (C::kHeads * 2);
+    for (int i = tid; i < heads * kQuads; i += kDecodeWarps * 32) {
+      const int h = i / kQuads, d = 4 * (i % kQuads);
+      float top = -INFINITY;
+      for (int x = s; x < end; ++x)
+        if (sh.part[x].n) top = fmaxf(top, sh.m[x][h]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x = s; x < end; ++x) {
+        if (sh.part[x].n == 0) continue;
+        const float w = fast_exp2(sh.m[x][h] - ref);
+        const float4 v = *reinterpret_cast<const float4*>(part_o(x) + o_at<D>(h, d));
+        sum += w * sh.l[x][h];
+        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+      }
+      if (whole) {
+        const float by = sum == 0.f ? 0.f : 1.f / sum;
+        store_out4(a, D, p.b, first + h, d, make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
+        if (d == 0) a.lse[int64_t(first + h) * a.B + p.b] = lse_of(ref, sum);
+      } else {
+        __stcg(reinterpret_cast<float4*>(o_out + h * D + d), o);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(ml_out + 2 * h), make_float2(top, sum));
+      }
+    }
+    if (!whole) open[place] = s;
+    s = end;
+  }
+
+  // ---- rows that several CTAs share: the last to arrive joins them
+  if (open[0] < 0 && open[1] < 0) return;
+  __threadfence();
+  for (int place = 0; place < 2; ++place) {
+    if (open[place] < 0) continue;
+    const Stretch p = sh.part[open[place]];
+    const int from = taker(total, ctas, p.u0), to = taker(total, ctas, p.u0 + p.n - 1);
+    __syncthreads();
+    if (tid == 0) sh.arrived = atomicAdd(a.counters + from, 1);
+    __syncthreads();
+    if (sh.arrived != to - from) continue;
+    if (tid == 0) a.counters[from] = 0;  // for the next launch
+    __threadfence();
+    int kv, first, heads;
+    heads_of(a, p.vh, &kv, &first, &heads);
+    // the row's part in CTA i: its last share (place 1) where it begins, else its first
+    auto place_of = [&](int i) { return int64_t(i) * 2 + (i == from ? 1 : 0); };
+    for (int i = tid; i < heads * kQuads; i += kDecodeWarps * 32) {
+      const int h = i / kQuads, d = 4 * (i % kQuads);
+      float top = -INFINITY;
+      for (int x = from; x <= to; ++x) top = fmaxf(top, __ldcg(a.part_ml + place_of(x) * (C::kHeads * 2) + 2 * h));
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int x = from; x <= to; ++x) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + place_of(x) * (C::kHeads * 2) + 2 * h));
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + place_of(x) * (C::kHeads * D) + h * D + d));
+        const float w = fast_exp2(ml.x - ref);
+        sum += w * ml.y;
+        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+      }
+      const float by = sum == 0.f ? 0.f : 1.f / sum;
+      store_out4(a, D, p.b, first + h, d, make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
+      if (d == 0) a.lse[int64_t(first + h) * a.B + p.b] = lse_of(ref, sum);
+    }
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
+  using C = DecodeCfg<D, NT>;
+  static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<D, NT>) + 1024) <= 233472, "shared memory of an SM");
+  cudaError_t e = set_smem_limit_once<decode_kernel<D, NT>>(C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  decode_kernel<D, NT><<<sms * C::kCtasPerSm, kDecodeWarps * 32, C::kSmemBytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+DecodeSpace decode_space(int D, int part_heads, int sms) {
+  const int heads = part_heads <= 8 ? 8 : 16;
+  const int ctas = sms * (D == 64 ? DecodeCfg<64, 1>::kCtasPerSm : DecodeCfg<128, 1>::kCtasPerSm);
+  static_assert(DecodeCfg<64, 1>::kCtasPerSm == DecodeCfg<64, 2>::kCtasPerSm &&
+                    DecodeCfg<128, 1>::kCtasPerSm == DecodeCfg<128, 2>::kCtasPerSm, "one grid for each D");
+  return {ctas, int64_t(ctas) * 2 * heads * 2, int64_t(ctas) * 2 * heads * D};
+}
+
+cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t stream) {
+  if (a.part_heads <= 8)
+    return a.D == 128 ? launch<128, 1>(a, sms, stream) : launch<64, 1>(a, sms, stream);
+  return a.D == 128 ? launch<128, 2>(a, sms, stream) : launch<64, 2>(a, sms, stream);
+}
+
+}  // namespace jfa

@@ -1,10 +1,8 @@
-// paged.cu -- block tables and slots from request lengths, and attention of
-// one new token per request over the paged cache.
+// paged.cu -- block tables and slots from request lengths.
 #include <climits>
 
 #include "kernels.h"
 #include "paged.h"
-#include "sm103_ptx.cuh"
 
 namespace jfa {
 namespace {
@@ -177,60 +175,6 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
   if (tid == 0 && problem) atomicOr(a.status, problem);
 }
 
-// ---------------------------------------------------------------------------
-// One new token over the paged cache: a CTA per request and query head, its
-// warps share the cached rows, each with a running maximum and sum.
-// ---------------------------------------------------------------------------
-constexpr int kDecodeWarps = 4;
-
-template <int D>
-__global__ void __launch_bounds__(kDecodeWarps * 32) decode_kernel(const __grid_constant__ DecodeArgs a) {
-  constexpr int E = D / 32;
-  const int b = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int hk = h / (a.H / a.Hkv);
-  int len = a.lens[b];
-  if (len < 0 || len > a.max_pages * a.div.d) {
-    if (threadIdx.x == 0) atomicOr(a.status, kPagerBadLength);
-    len = 0;
-  }
-  float q[E], o[E] = {};
-  for (int e = 0; e < E; ++e)
-    q[e] = __uint_as_float(uint32_t(a.q[b * a.q_row + int64_t(h) * D + lane * E + e]) << 16);
-  float m = -INFINITY, l = 0.f;
-  for (int t = warp; t < len; t += kDecodeWarps) {
-    const int i = a.div.quot(t);
-    const int page = a.table[b * a.table_row + i];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) atomicOr(a.status, kPagerBadPage);
-      continue;
-    }
-    const int64_t at = page * a.page + (t - i * a.div.d) * a.row + hk * a.head + lane * E;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s += q[e] * __uint_as_float(uint32_t(a.k[at + e]) << 16);
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-    s *= a.scale;
-    const float mx = fmaxf(m, s), ms = mx == -INFINITY ? 0.f : mx;
-    const float keep = expf(m - ms), p = expf(s - ms);
-    l = l * keep + p;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p * __uint_as_float(uint32_t(a.v[at + e]) << 16);
-    m = mx;
-  }
-  __shared__ float sm[kDecodeWarps], sl[kDecodeWarps], so[kDecodeWarps][D];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-  __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < kDecodeWarps; ++w) M = fmaxf(M, sm[w]);
-  const float Ms = M == -INFINITY ? 0.f : M;
-  for (int w = 0; w < kDecodeWarps; ++w) L += sl[w] * expf(sm[w] - Ms);
-  for (int d = threadIdx.x; d < D; d += blockDim.x) {
-    float acc = 0.f;
-    for (int w = 0; w < kDecodeWarps; ++w) acc += so[w][d] * expf(sm[w] - Ms);
-    a.out[(int64_t(b) * a.H + h) * D + d] = static_cast<uint16_t>(pack_bf16x2(L == 0.f ? 0.f : acc / L, 0.f));
-  }
-  if (threadIdx.x == 0) a.lse[int64_t(h) * a.B + b] = Ms + logf(L);
-}
-
 }  // namespace
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
@@ -238,16 +182,6 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
   cudaError_t e = set_smem_limit_once<tables_kernel>((3 * 16384 + 1) * 4);
   if (e != cudaSuccess) return e;
   tables_kernel<<<1, kTableThreads, smem, stream>>>(a);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
-  if (a.B == 0) return cudaSuccess;
-  const dim3 grid(a.H, a.B);
-  if (a.D == 128)
-    decode_kernel<128><<<grid, kDecodeWarps * 32, 0, stream>>>(a);
-  else
-    decode_kernel<64><<<grid, kDecodeWarps * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

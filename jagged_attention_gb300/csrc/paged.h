@@ -75,6 +75,7 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream);
 
 struct DecodeArgs {
   int B, H, Hkv, D;
+  int parts, part_heads;  // a key/value head's query heads in parts of at most 16
   int64_t num_pages;
   int max_pages;
   PageDiv div;
@@ -88,7 +89,15 @@ struct DecodeArgs {
   uint16_t* out;
   float* lse;
   int* status;
+  int* counters;             // arrivals at a split row, one for each CTA; zero between launches
+  float *part_ml, *part_o;   // what CTAs leave of split rows
 };
-cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
+// Workspace of a decode launch: counters (int), part_ml and part_o (float).
+struct DecodeSpace {
+  int counters;
+  int64_t part_ml, part_o;
+};
+DecodeSpace decode_space(int D, int part_heads, int sms);
+cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace jfa

@@ -16,10 +16,11 @@ struct jfa_rotary {
 
 struct jfa_pager {
   int max_seqs, max_pages, H, Hkv, D, device, sms;
+  int parts, part_heads;
   int64_t num_pages;
   jfa::PageDiv div;
-  void* dev_block;
-  int* d_status;
+  int *d_status, *d_counters;  // in the caller's block, as the rest
+  float *d_part_ml, *d_part_o;
 };
 
 namespace {
@@ -92,6 +93,29 @@ int check_pages(const jfa_pages* g) {
   return JFA_OK;
 }
 
+// A pager's block: status word, counters, then what split rows leave.
+struct Block {
+  size_t counters, part_ml, part_o, bytes;
+  int parts, part_heads;
+};
+Block block_of(int H, int Hkv, int D, int sms) {
+  Block k;
+  const int group = H / Hkv;
+  k.parts = (group + 15) / 16;
+  k.part_heads = (group + k.parts - 1) / k.parts;
+  const jfa::DecodeSpace n = jfa::decode_space(D, k.part_heads, sms);
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  k.counters = 256;
+  k.part_ml = up(k.counters + n.counters * sizeof(int));
+  k.part_o = up(k.part_ml + n.part_ml * sizeof(float));
+  k.bytes = up(k.part_o + n.part_o * sizeof(float));
+  return k;
+}
+int check_heads(int H, int Hkv, int D) {
+  if (Hkv < 1 || H < Hkv || H % Hkv) return JFA_ERR_INVALID_ARG;
+  return (D != 64 && D != 128) || H > 65535 ? JFA_ERR_UNSUPPORTED : JFA_OK;
+}
+
 jfa::RowJob dense_job(const void* in, int64_t in_row, void* out, int64_t out_row, int heads, int D,
                       bool f32, bool rotate) {
   return {in, out, in_row, out_row, 0, D, heads, f32, false, rotate};
@@ -127,7 +151,7 @@ int jfa_rotary_create(const double* inv_freq_host, const int32_t* axis_host, int
   r.turns.pairs = pairs;
   r.turns.interleaved = (flags & JFA_ROTARY_INTERLEAVED) != 0;
   *out = new (std::nothrow) jfa_rotary(r);
-  return *out ? JFA_OK : JFA_ERR_INVALID_ARG;
+  return *out ? JFA_OK : JFA_ERR_WORKSPACE;
 }
 
 int jfa_rotary_destroy(jfa_rotary_t rotary) {
@@ -171,46 +195,54 @@ int jfa_rotate(jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row, i
   return jfa::launch_rows(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
+size_t jfa_pager_block_bytes(int H, int Hkv, int D) {
+  int sms = 0;
+  if (check_heads(H, Hkv, D) != JFA_OK || sm_count(&sms) != JFA_OK) return 0;
+  return block_of(H, Hkv, D, sms).bytes;
+}
+
 int jfa_pager_create(int max_seqs, int max_pages, int64_t num_pages, int page_size, int H, int Hkv,
-                     int D, void* stream, jfa_pager_t* out) {
+                     int D, void* block, size_t block_bytes, void* stream, jfa_pager_t* out) {
   if (!out) return JFA_ERR_INVALID_ARG;
   *out = nullptr;
-  if (max_seqs < 1 || max_pages < 1 || num_pages < 1 || page_size < 1 || Hkv < 1 || H < Hkv || H % Hkv)
-    return JFA_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || max_seqs > JFA_PAGER_MAX_SEQS || H > 65535 ||
-      num_pages > INT_MAX || (int64_t(max_pages) + 1) * page_size > INT_MAX ||
-      (num_pages + 1) * page_size > INT_MAX)
+  if (max_seqs < 1 || max_pages < 1 || num_pages < 1 || page_size < 1) return JFA_ERR_INVALID_ARG;
+  if (int rc = check_heads(H, Hkv, D)) return rc;
+  if (max_seqs > JFA_PAGER_MAX_SEQS || num_pages > INT_MAX ||
+      (int64_t(max_pages) + 1) * page_size > INT_MAX || (num_pages + 1) * page_size > INT_MAX)
     return JFA_ERR_UNSUPPORTED;
-  int sms = 0;
+  if (!aligned(block, 256)) return JFA_ERR_ALIGNMENT;
+  int sms = 0, dev = 0;
   if (int rc = sm_count(&sms)) return rc;
-  jfa_pager p{};
-  p.max_seqs = max_seqs;
-  p.max_pages = max_pages;
-  p.num_pages = num_pages;
-  p.H = H;
-  p.Hkv = Hkv;
-  p.D = D;
-  p.sms = sms;
-  p.div = jfa::make_page_div(page_size);
-  if (cudaGetDevice(&p.device) != cudaSuccess) return JFA_ERR_CUDA;
-  const size_t bytes = 256;
-  if (cudaMalloc(&p.dev_block, bytes) != cudaSuccess) return JFA_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  jfa_pager* made = nullptr;
-  if (cudaMemsetAsync(p.dev_block, 0, bytes, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess ||
-      !(p.d_status = static_cast<int*>(p.dev_block), made = new (std::nothrow) jfa_pager(p))) {
-    cudaFree(p.dev_block);
-    return JFA_ERR_CUDA;
-  }
-  *out = made;
+  if (cudaGetDevice(&dev) != cudaSuccess) return JFA_ERR_CUDA;
+  const Block k = block_of(H, Hkv, D, sms);
+  if (!block || block_bytes < k.bytes) return JFA_ERR_WORKSPACE;
+  auto* base = static_cast<unsigned char*>(block);
+  if (cudaMemsetAsync(base, 0, k.part_ml, static_cast<cudaStream_t>(stream)) != cudaSuccess) return JFA_ERR_CUDA;
+  auto* p = new (std::nothrow) jfa_pager;
+  if (!p) return JFA_ERR_WORKSPACE;
+  p->max_seqs = max_seqs;
+  p->max_pages = max_pages;
+  p->H = H;
+  p->Hkv = Hkv;
+  p->D = D;
+  p->device = dev;
+  p->sms = sms;
+  p->parts = k.parts;
+  p->part_heads = k.part_heads;
+  p->num_pages = num_pages;
+  p->div = jfa::make_page_div(page_size);
+  p->d_status = reinterpret_cast<int*>(base);
+  p->d_counters = reinterpret_cast<int*>(base + k.counters);
+  p->d_part_ml = reinterpret_cast<float*>(base + k.part_ml);
+  p->d_part_o = reinterpret_cast<float*>(base + k.part_o);
+  *out = p;
   return JFA_OK;
 }
 
 int jfa_pager_destroy(jfa_pager_t pager) {
   if (!pager) return JFA_ERR_INVALID_ARG;
-  const int rc = cudaFree(pager->dev_block) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
   delete pager;
-  return rc;
+  return JFA_OK;
 }
 
 int jfa_pager_status(jfa_pager_t pager, void* stream, int* raw) {
@@ -312,6 +344,8 @@ int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, con
   a.H = pager->H;
   a.Hkv = pager->Hkv;
   a.D = pager->D;
+  a.parts = pager->parts;
+  a.part_heads = pager->part_heads;
   a.num_pages = pager->num_pages;
   a.max_pages = pager->max_pages;
   a.div = pager->div;
@@ -329,7 +363,10 @@ int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, con
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = pager->d_status;
-  return jfa::launch_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+  a.counters = pager->d_counters;
+  a.part_ml = pager->d_part_ml;
+  a.part_o = pager->d_part_o;
+  return jfa::launch_decode(a, pager->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
 }  // extern "C"

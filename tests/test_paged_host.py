@@ -28,7 +28,7 @@ def test_create_refuses(change, code):
     a.update(change)
     h = ctypes.c_void_p()
     rc = jfa.lib().jfa_pager_create(a["max_seqs"], a["max_pages"], a["num_pages"], a["page_size"], a["H"], a["Hkv"],
-                                    a["D"], None, ctypes.byref(h))
+                                    a["D"], 4096, 1 << 30, None, ctypes.byref(h))
     assert rc == code and h.value is None
 
 
