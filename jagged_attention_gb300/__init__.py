@@ -539,57 +539,61 @@ class Rotary:
             pass
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> tuple[int, int]:
-    """(address, elements from row to row) of a tensor [rows, heads, D] whose heads are contiguous."""
+def _refuse(name: str, t, dtype, device: int, shape):
+    """Raises what is wrong with a tensor, in the order type, device, shape."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise TypeError(f"{name} must be on {device}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if t.numel() and (st[2] != 1 or (shape[1] > 1 and st[1] != shape[2])):
-        raise ValueError(f"the heads of {name} must be contiguous")
-    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
+    if t.get_device() != device:
+        raise TypeError(f"{name} must be on cuda:{device}, got {t.device}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, innermost dimensions contiguous, got {tuple(t.shape)} "
+                     f"with strides {t.stride()}")
 
 
-def _ints(t: torch.Tensor, name: str, shape, device) -> int:
-    """Address of a contiguous int32 tensor."""
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be {torch.int32}, got {t.dtype}")
-    if t.device != device:
-        raise TypeError(f"{name} must be on {device}, got {t.device}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+def _rows(name: str, t: torch.Tensor, shape, dtype, device: int) -> tuple[int, int]:
+    """(address, elements from row to row) of a tensor [rows, heads, D] whose heads are contiguous."""
+    if t.dtype != dtype or t.get_device() != device or t.shape != shape:
+        _refuse(name, t, dtype, device, shape)
+    row, head, one = t.stride()
+    rows, heads, D = shape
+    if one != 1 or head != D and heads > 1:
+        if t.numel():
+            _refuse(name, t, dtype, device, shape)
+    return t.data_ptr(), row if rows > 1 else heads * D
+
+
+def _ints(name: str, t: torch.Tensor, n: int, device: int) -> int:
+    """Address of a contiguous int32 tensor of n values."""
+    if t.dtype != torch.int32 or t.get_device() != device or t.shape != (n,) or n > 1 and t.stride(0) != 1:
+        _refuse(name, t, torch.int32, device, (n,))
     return t.data_ptr()
 
 
-def _table(t: torch.Tensor, pager, B: int, device) -> tuple[int, int]:
+def _table(t: torch.Tensor, pager, B: int, device: int) -> tuple[int, int]:
     """(address, entries from row to row) of a block table [B, max_pages]."""
-    if t.dtype != torch.int32 or t.device != device:
-        raise TypeError(f"table must be {torch.int32} on {device}, got {t.dtype} on {t.device}")
-    if t.shape != (B, pager.max_pages) or t.stride(1) != 1 and pager.max_pages > 1:
-        raise ValueError(f"table must be [{B}, {pager.max_pages}] with contiguous rows, got {tuple(t.shape)}")
-    return t.data_ptr(), t.stride(0) if B > 1 else pager.max_pages
+    width = pager.max_pages
+    if t.dtype != torch.int32 or t.get_device() != device or t.shape != (B, width):
+        _refuse("table", t, torch.int32, device, (B, width))
+    row, one = t.stride()
+    if one != 1 and width > 1:
+        _refuse("table", t, torch.int32, device, (B, width))
+    return t.data_ptr(), row if B > 1 else width
 
 
-def _positions(positions: torch.Tensor, rotary: Rotary, rows: int, device) -> tuple[int, int, int]:
+def _positions(positions: torch.Tensor, rotary: Rotary, rows: int, device: int) -> tuple[int, int, int]:
     """(address, row distance, axis distance): int32 [rows, axes], or [rows] for one position on every axis."""
-    if positions.dtype != torch.int32 or positions.device != device:
-        raise TypeError(f"positions must be {torch.int32} on {device}, got {positions.dtype} on {positions.device}")
-    if positions.dim() == 1 and positions.shape[0] == rows:
-        return positions.data_ptr(), positions.stride(0), 0
-    if positions.dim() != 2 or positions.shape[0] != rows or positions.shape[1] < rotary.axes:
-        raise ValueError(f"positions must be [{rows}] or [{rows}, {rotary.axes}], got {tuple(positions.shape)}")
-    return positions.data_ptr(), positions.stride(0), positions.stride(1)
+    if positions.dtype != torch.int32 or positions.get_device() != device:
+        _refuse("positions", positions, torch.int32, device, (rows, rotary.axes))
+    shape, stride = positions.shape, positions.stride()
+    if len(shape) == 1 and shape[0] == rows:
+        return positions.data_ptr(), stride[0], 0
+    if len(shape) != 2 or shape[0] != rows or shape[1] < rotary.axes:
+        raise ValueError(f"positions must be [{rows}] or [{rows}, {rotary.axes}], got {tuple(shape)}")
+    return positions.data_ptr(), stride[0], stride[1]
 
 
-def _current(device: torch.device):
-    """Launches go to the current device: the tensors must be there."""
-    if device.type != "cuda":
-        raise TypeError(f"tensors must be CUDA tensors, got {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+def _raw_stream(stream, device: int) -> int:
+    """As _stream, for calls whose tensors are on `device`."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out=None, k_out=None,
@@ -599,35 +603,41 @@ def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out
     q and k) to the gradients of the unrotated ones.  Rows may lie apart (slices
     of a fused projection).  q_out / k_out may be q / k.  Returns q_out, or
     (q_out, k_out) with k."""
-    dev = q.device
-    _current(dev)
+    dev = q.get_device()
+    if dev < 0:
+        raise TypeError(f"q must be a CUDA tensor, got {q.device}")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"q on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
     if q.dim() != 3 or k is not None and k.dim() != 3:
         raise ValueError("q and k must be [rows, heads, D]")
-    rows = q.shape[0]
+    rows, hq, _ = q.shape
     flags = ROTATE_INVERSE if inverse else 0
-    address, pos_row, pos_axis = _positions(positions, rotary, rows, dev)
-    args = []
-    for name, t, out, bit in (("q", q, q_out, ROTATE_X_FP32), ("k", k, k_out, ROTATE_Y_FP32)):
-        if t is None:
-            if out is not None:
-                raise ValueError(f"{name}_out without {name}")
-            args += [None, 0, None, 0, 0]
-            continue
-        if t.dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError(f"{name} must be {torch.bfloat16} or {torch.float32}, got {t.dtype}")
-        heads = t.shape[1]
-        shape = (rows, heads, rotary.D)
-        if out is None:
-            out = torch.empty(shape, dtype=t.dtype, device=dev)
-        if name == "q":
-            q_out = out
-        else:
-            k_out = out
-        if t.dtype == torch.float32:
-            flags |= bit
-        args += [*_rows(t, name, shape, t.dtype, dev), *_rows(out, f"{name}_out", shape, t.dtype, dev), heads]
-    _check(lib().jfa_rotate(rotary.handle, address, pos_row, pos_axis, rows, flags, *args, _stream(stream)),
-           "jfa_rotate")
+    if q.dtype == torch.float32:
+        flags |= ROTATE_X_FP32
+    elif q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be {torch.bfloat16} or {torch.float32}, got {q.dtype}")
+    shape = (rows, hq, rotary.D)
+    if q_out is None:
+        q_out = q.new_empty(shape)
+    args = (*_rows("q", q, shape, q.dtype, dev), *_rows("q_out", q_out, shape, q.dtype, dev), hq)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        args += (None, 0, None, 0, 0)
+    else:
+        hk = k.shape[1]
+        if k.dtype == torch.float32:
+            flags |= ROTATE_Y_FP32
+        elif k.dtype != torch.bfloat16:
+            raise TypeError(f"k must be {torch.bfloat16} or {torch.float32}, got {k.dtype}")
+        shape = (rows, hk, rotary.D)
+        if k_out is None:
+            k_out = k.new_empty(shape)
+        args += (*_rows("k", k, shape, k.dtype, dev), *_rows("k_out", k_out, shape, k.dtype, dev), hk)
+    rc = (_lib or lib()).jfa_rotate(rotary.handle, *_positions(positions, rotary, rows, dev), rows, flags, *args,
+                                    _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "jfa_rotate")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -642,6 +652,7 @@ class Pager:
         self.max_seqs, self.max_pages, self.num_pages, self.page_size = max_seqs, max_pages, num_pages, page_size
         self.H, self.Hkv, self.D = H, Hkv, D
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self.index = self.device.index
         n = lib().jfa_pager_block_bytes(H, Hkv, D)
         self.block = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
         h = _vp()
@@ -676,13 +687,11 @@ class Pager:
 
 
 def _pages(pager: Pager, k_pages, v_pages) -> _Pages:
-    shape = (pager.num_pages, pager.page_size, pager.Hkv, pager.D)
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype != torch.bfloat16 or t.device != pager.device:
-            raise TypeError(f"{name} must be {torch.bfloat16} on {pager.device}, got {t.dtype} on {t.device}")
-        if t.shape != shape or t.stride(3) != 1:
-            raise ValueError(f"{name} must have shape {shape} with contiguous rows, got {tuple(t.shape)}")
+    shape, dev = (pager.num_pages, pager.page_size, pager.Hkv, pager.D), pager.index
     st = k_pages.stride()
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != shape or st[3] != 1:
+            _refuse(name, t, torch.bfloat16, dev, shape)
     if st != v_pages.stride():
         raise ValueError(f"k_pages and v_pages must have the same strides, got {st} and {v_pages.stride()}")
     return _Pages(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2])
@@ -695,28 +704,23 @@ def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: i
     table [B, max_pages] and free_list [num_pages] are updated in place; lens and
     n_free too where lens_out and n_free_out are given as them.  Returns
     (lens_out, n_free_out, slots, positions, row_offsets)."""
-    dev = pager.device
+    dev = pager.index
     B = lens.shape[0]
-    empty = lambda n: torch.empty((n,), dtype=torch.int32, device=dev)  # noqa: E731
-    if lens_out is None:
-        lens_out = empty(B)
-    if n_free_out is None:
-        n_free_out = empty(1)
-    if slots is None:
-        slots = empty(rows)
-    if positions is None:
-        positions = empty(rows)
-    if row_offsets is None:
-        row_offsets = empty(B + 1)
-    tab, tab_row = _table(table, pager, B, dev)
-    _check(lib().jfa_paged_tables(
-        pager.handle, B, _ints(lens, "lens", (B,), dev), _ints(delta, "delta", (B,), dev),
-        _ints(lens_out, "lens_out", (B,), dev), tab, tab_row,
-        _ints(free_list, "free_list", (pager.num_pages,), dev), _ints(n_free, "n_free", (1,), dev),
-        _ints(n_free_out, "n_free_out", (1,), dev), rows, _ints(slots, "slots", (rows,), dev),
-        _ints(positions, "positions", (rows,), dev), _ints(row_offsets, "row_offsets", (B + 1,), dev),
-        _stream(stream)), "jfa_paged_tables")
-    return lens_out, n_free_out, slots, positions, row_offsets
+    outs = (lens_out, n_free_out, slots, positions, row_offsets)
+    if lens_out is None or n_free_out is None or slots is None or positions is None or row_offsets is None:
+        made = delta.new_empty(2 * B + 2 + 2 * rows).split((B, 1, rows, rows, B + 1))
+        outs = tuple(m if o is None else o for m, o in zip(made, outs))
+    lens_out, n_free_out, slots, positions, row_offsets = outs
+    rc = (_lib or lib()).jfa_paged_tables(
+        pager.handle, B, _ints("lens", lens, B, dev), _ints("delta", delta, B, dev),
+        _ints("lens_out", lens_out, B, dev), *_table(table, pager, B, dev),
+        _ints("free_list", free_list, pager.num_pages, dev), _ints("n_free", n_free, 1, dev),
+        _ints("n_free_out", n_free_out, 1, dev), rows, _ints("slots", slots, rows, dev),
+        _ints("positions", positions, rows, dev), _ints("row_offsets", row_offsets, B + 1, dev),
+        _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "jfa_paged_tables")
+    return outs
 
 
 def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary | None = None,
@@ -724,28 +728,29 @@ def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary 
     """New rows k, v [rows, Hkv, D] into the pages at their slots through
     jfa_paged_append; with ``rotary``, k and q [rows, H, D] rotated by
     ``positions`` on the way.  Returns q_out (which may be q), None without q."""
-    dev = pager.device
+    dev = pager.index
     rows = k.shape[0]
     shape = (rows, pager.Hkv, pager.D)
-    if rotary is None and (positions is not None or q is not None):
-        raise ValueError("positions and q go with rotary")
-    pos, q_args = (None, 0, 0), (None, 0, None, 0)
+    rot, pos, q_args = None, (None, 0, 0), (None, 0, None, 0)
     if rotary is not None:
         if positions is None:
             raise ValueError("rotary without positions")
-        pos = _positions(positions, rotary, rows, dev)
+        rot, pos = rotary.handle, _positions(positions, rotary, rows, dev)
+    elif positions is not None or q is not None:
+        raise ValueError("positions and q go with rotary")
     if q is not None:
         q_shape = (rows, pager.H, pager.D)
         if q_out is None:
-            q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
-        q_args = (*_rows(q, "q", q_shape, torch.bfloat16, dev), *_rows(q_out, "q_out", q_shape, torch.bfloat16, dev))
+            q_out = q.new_empty(q_shape)
+        q_args = (*_rows("q", q, q_shape, torch.bfloat16, dev), *_rows("q_out", q_out, q_shape, torch.bfloat16, dev))
     elif q_out is not None:
         raise ValueError("q_out without q")
-    pages = _pages(pager, k_pages, v_pages)
-    _check(lib().jfa_paged_append(
-        pager.handle, rows, *_rows(k, "k", shape, torch.bfloat16, dev), *_rows(v, "v", shape, torch.bfloat16, dev),
-        _ints(slots, "slots", (rows,), dev), ctypes.byref(pages), None if rotary is None else rotary.handle,
-        *pos, *q_args, _stream(stream)), "jfa_paged_append")
+    rc = (_lib or lib()).jfa_paged_append(
+        pager.handle, rows, *_rows("k", k, shape, torch.bfloat16, dev), *_rows("v", v, shape, torch.bfloat16, dev),
+        _ints("slots", slots, rows, dev), ctypes.byref(_pages(pager, k_pages, v_pages)), rot, *pos, *q_args,
+        _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "jfa_paged_append")
     return q_out
 
 
@@ -753,20 +758,22 @@ def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *
                  stream=None):
     """O (bf16 [B, H, D]) and LSE (fp32 [H, B]) of one new token per request over
     its cached rows, through jfa_paged_decode.  q [B, H, D]; rows may lie apart."""
-    dev = pager.device
+    dev, H, D = pager.index, pager.H, pager.D
     B = q.shape[0]
-    shape = (B, pager.H, pager.D)
+    shape = (B, H, D)
+    q_at = _rows("q", q, shape, torch.bfloat16, dev)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = q.new_empty(shape)
     if lse is None:
-        lse = torch.empty((pager.H, B), dtype=torch.float32, device=dev)
-    elif lse.dtype != torch.float32 or lse.device != dev or lse.shape != (pager.H, B) or not lse.is_contiguous():
-        raise ValueError(f"lse must be contiguous float32 [{pager.H}, {B}] on {dev}")
-    address, out_row = _rows(out, "out", shape, torch.bfloat16, dev)
-    if out_row != pager.H * pager.D:
+        lse = q.new_empty((H, B), dtype=torch.float32)
+    elif lse.dtype != torch.float32 or lse.get_device() != dev or lse.shape != (H, B) or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous float32 [{H}, {B}] on {pager.device}")
+    out_at, out_row = _rows("out", out, shape, torch.bfloat16, dev)
+    if out_row != H * D:
         raise ValueError("out must be contiguous")
-    pages = _pages(pager, k_pages, v_pages)
-    _check(lib().jfa_paged_decode(pager.handle, B, *_rows(q, "q", shape, torch.bfloat16, dev), ctypes.byref(pages),
-                                  *_table(table, pager, B, dev), _ints(lens, "lens", (B,), dev), float(scale),
-                                  address, lse.data_ptr(), _stream(stream)), "jfa_paged_decode")
+    rc = (_lib or lib()).jfa_paged_decode(
+        pager.handle, B, *q_at, ctypes.byref(_pages(pager, k_pages, v_pages)), *_table(table, pager, B, dev),
+        _ints("lens", lens, B, dev), float(scale), out_at, lse.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "jfa_paged_decode")
     return out, lse

@@ -50,26 +50,57 @@ struct DecodeCfg {
   static constexpr int kCtasPerSm = D == 64 ? 2 : 1;
 };
 
-// Where a warp stands: tile t of n of the rows of (request b, virtual head vh).
+// Units of work: a (request, virtual head) of n tiles counts n units for them,
+// and kRowUnits behind them for its beginning and end.
+constexpr int kRowUnits = 1;
+
+// Where a warp stands: tile t of n of the rows of (request b, virtual head vh),
+// unit u of all.
+template <typename U>
 struct Cursor {
+  U u;
   int b, vh, t, n, len;
 };
 
 // A stretch that does not hold all tiles of its (b, vh): tiles [t0, t1) of n.
 struct Stretch {
-  int64_t u0;  // index of the tile 0 of (b, vh) among all tiles
+  int64_t u0;  // unit of its tile 0
   int b, vh, t0, t1, n;  // n 0: none
+};
+
+// Sum of stretches of one row for 4 values of a head, taken up in batches.
+struct Joined {
+  float top = -INFINITY, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  template <int N>
+  __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&v)[N]) {  // ml: maximum, sum
+    float up = top;
+#pragma unroll
+    for (int i = 0; i < N; ++i) up = fmaxf(up, ml[i].x);
+    const float ref = up == -INFINITY ? 0.f : up;
+    const float keep = fast_exp2(top - ref);
+    sum *= keep;
+    o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float w = fast_exp2(ml[i].x - ref);
+      sum += w * ml[i].y;
+      o.x += w * v[i].x, o.y += w * v[i].y, o.z += w * v[i].z, o.w += w * v[i].w;
+    }
+    top = up;
+  }
 };
 
 template <int D, int NT>
 struct DecodeShared {
   Stretch part[2 * kDecodeWarps];                 // first and last of each warp
   float m[2 * kDecodeWarps][8 * NT], l[2 * kDecodeWarps][8 * NT];
-  int64_t scan[kDecodeWarps];
-  int64_t start_tiles[kDecodeWarps];  // tiles of the requests before a warp's first
-  int start_b[kDecodeWarps];
+  int64_t scan_units[kDecodeWarps];
+  int scan_rows[kDecodeWarps], scan_most[kDecodeWarps];
+  int64_t start_unit[kDecodeWarps];  // where the request begins in which a warp's share does
+  int start_b[kDecodeWarps], start_len[kDecodeWarps];
   uint32_t live[kDecodeWarps][DecodeCfg<D, NT>::kStages];  // rows of a stage that count
-  int arrived;
+  int arrived[2], from[2], to[2];
 };
 
 __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
@@ -114,16 +145,23 @@ __device__ __forceinline__ int o_at(int head, int d) {
   return head * D + (d ^ (((head >> 1) & 3) << 3));
 }
 
-// Shares of `total` dealt to n takers: taker i's first.
-__device__ __forceinline__ int64_t share(int64_t total, int n, int i) {
-  const int64_t per = total / n, more = total - per * n;
-  return per * i + min(int64_t(i), more);
+// Shares of `total` items dealt to n takers: taker i's first.
+template <typename U>
+__device__ __forceinline__ U share(U total, int n, int i) {
+  const U per = total / U(n), more = total - per * U(n);
+  return per * U(i) + min(U(i), more);
 }
 // The taker of item u.
-__device__ __forceinline__ int taker(int64_t total, int n, int64_t u) {
-  const int64_t per = total / n, more = total - per * n;
-  const int64_t big = more * (per + 1);
+template <typename U>
+__device__ __forceinline__ int taker(U total, int n, U u) {
+  const U per = total / U(n), more = total - per * U(n);
+  const U big = more * (per + 1);
   return static_cast<int>(u < big ? u / (per + 1) : more + (u - big) / per);
+}
+// CTAs that take part: fewer than `most` where each warp would not have a unit.
+template <typename U>
+__device__ __forceinline__ int ctas_of(U total, int most) {
+  return total >= U(most) * kDecodeWarps ? most : max(1, static_cast<int>(total) / kDecodeWarps);
 }
 
 // Query heads [first, first + count) of virtual head vh, and its key/value head.
@@ -140,9 +178,25 @@ __device__ __forceinline__ void store_out4(const DecodeArgs& a, int D, int b, in
   *reinterpret_cast<uint2*>(a.out + (int64_t(b) * a.H + head) * D + d) =
       make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
+// Adds one to a counter, releasing this thread's view of memory and acquiring the
+// others': what was there before.
+__device__ __forceinline__ int arrive(int* counter) {
+  int was;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(was) : "l"(counter) : "memory");
+  return was;
+}
 __device__ __forceinline__ float lse_of(float m, float l) { return m * kLn2 + logf(l); }
 
-template <int D, int NT>
+// A finished row: normalised, with its log-sum-exp.
+__device__ __forceinline__ void store_joined(const DecodeArgs& a, int D, int b, int head, int d, const Joined& s) {
+  const float by = s.sum == 0.f ? 0.f : 1.f / s.sum;
+  store_out4(a, D, b, head, d, make_float4(s.o.x * by, s.o.y * by, s.o.z * by, s.o.w * by));
+  if (d == 0) a.lse[int64_t(head) * a.B + b] = lse_of(s.top == -INFINITY ? 0.f : s.top, s.sum);
+}
+
+// U: unsigned type that counts all units.  32 bits hold them unless the table is
+// wide enough for more; divisions and scans in 64 bits cost a short call 1 us.
+template <int D, int NT, typename U>
 __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeCfg<D, NT>::kCtasPerSm)
 decode_kernel(const __grid_constant__ DecodeArgs a) {
   using C = DecodeCfg<D, NT>;
@@ -154,74 +208,90 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   // ---- tiles of all requests, and where this CTA's warps begin
   const int slab = (a.B + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
   const int b_lo = min(a.B, tid * slab), b_hi = min(a.B, b_lo + slab);
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(length_of(a, b));
-  int64_t upto = mine;
+  U units = 0;
+  int rows = 0, most = 0;  // rows: requests that have any
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int n = tiles_of(length_of(a, b));
+    units += n > 0 ? n + kRowUnits : 0;
+    rows += n > 0;
+    most = max(most, n);
+  }
+  U units_to = units;
+  int rows_to = rows;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(~0u, upto, o);
-    if (lane >= o) upto += v;
+    const U x = __shfl_up_sync(~0u, units_to, o);
+    const int y = __shfl_up_sync(~0u, rows_to, o);
+    if (lane >= o) units_to += x, rows_to += y;
   }
-  if (lane == 31) sh.scan[warp] = upto;
+  most = __reduce_max_sync(~0u, most);
+  if (lane == 31) {
+    sh.scan_units[warp] = units_to;
+    sh.scan_rows[warp] = rows_to;
+    sh.scan_most[warp] = most;
+  }
   if (tid < 2 * kDecodeWarps) sh.part[tid].n = 0;
   __syncthreads();
-  int64_t total = 0;
+  U total = 0;
+  int all_rows = 0;
 #pragma unroll
   for (int w = 0; w < kDecodeWarps; ++w) {
-    if (w < warp) upto += sh.scan[w];
-    total += sh.scan[w];
+    const U x = static_cast<U>(sh.scan_units[w]);
+    const int y = sh.scan_rows[w];
+    if (w < warp) units_to += x, rows_to += y;
+    total += x;
+    all_rows += y;
+    most = max(most, sh.scan_most[w]);
   }
+  // few and short rows: a CTA for each, whose warps have no more tiles than their
+  // rings hold; nothing is left to be joined between CTAs then
+  const bool apart = most <= C::kStages * kDecodeWarps && int64_t(all_rows) * vheads <= gridDim.x;
+  if (apart) {
+    units = U(rows) * (C::kStages * kDecodeWarps);
+    units_to = U(rows_to) * (C::kStages * kDecodeWarps);
+    total = U(all_rows) * (C::kStages * kDecodeWarps);
+  }
+  auto units_of = [&](int n) -> U { return n == 0 ? 0 : apart ? C::kStages * kDecodeWarps : n + kRowUnits; };
   total *= vheads;
-  // few tiles: fewer CTAs, so that each warp has at least one
-  const int ctas = static_cast<int>(max(int64_t(1), min(int64_t(gridDim.x), total / kDecodeWarps)));
+  const int ctas = apart ? max(1, all_rows * vheads) : ctas_of(total, static_cast<int>(gridDim.x));
   const int cta = blockIdx.x;
-  int64_t cta_lo = 0, cta_n = 0;
+  U cta_lo = 0, cta_n = 0;
   if (cta < ctas) {
     cta_lo = share(total, ctas, cta);
     cta_n = share(total, ctas, cta + 1) - cta_lo;
   }
   {
-    const int64_t before = upto - mine;
-#pragma unroll
-    for (int w = 0; w < kDecodeWarps; ++w) {
-      const int64_t u = cta_lo + share(cta_n, kDecodeWarps, w);
-      if (before * vheads <= u && u < upto * vheads) {
-        int64_t tiles = before;
-        int b = b_lo;
-        for (; b + 1 < b_hi; ++b) {
-          const int n = tiles_of(length_of(a, b));
-          if (u < (tiles + n) * vheads) break;
-          tiles += n;
+    // the thread in whose requests a warp's share begins says where
+    const U first = (units_to - units) * vheads, end = units_to * vheads;
+    if (first < cta_lo + cta_n && end > cta_lo) {
+      for (int w = 0; w < kDecodeWarps; ++w) {
+        const U u = cta_lo + share(cta_n, kDecodeWarps, w);
+        if (u < first || u >= end) continue;
+        U at = first;
+        int b = b_lo, len = length_of(a, b);
+        while (b + 1 < b_hi && u >= at + units_of(tiles_of(len)) * vheads) {
+          at += units_of(tiles_of(len)) * vheads;
+          len = length_of(a, ++b);
         }
         sh.start_b[w] = b;
-        sh.start_tiles[w] = tiles;
+        sh.start_len[w] = len;
+        sh.start_unit[w] = at;
       }
     }
   }
   __syncthreads();
 
-  const int64_t lo = cta_lo + share(cta_n, kDecodeWarps, warp);
-  const int64_t hi = cta_lo + share(cta_n, kDecodeWarps, warp + 1);
-  const int64_t count = hi - lo;
+  const U lo = cta_lo + share(cta_n, kDecodeWarps, warp), hi = cta_lo + share(cta_n, kDecodeWarps, warp + 1);
 
   unsigned char* ring = smem + warp * C::kWarpBytes;
   const uint32_t ring_addr = smem_u32(ring);
   float* park = reinterpret_cast<float*>(ring + C::kStages * C::kStageBytes);
 
-  if (count > 0) {
-    Cursor at;  // of the tile whose rows are looked up next
-    at.b = sh.start_b[warp];
-    at.len = length_of(a, at.b);
-    at.n = tiles_of(at.len);
-    {
-      const int64_t r = lo - sh.start_tiles[warp] * vheads;
-      at.vh = static_cast<int>(r / at.n);
-      at.t = static_cast<int>(r - int64_t(at.vh) * at.n);
-    }
-    Cursor now = at;  // of the tile computed next
-
-    auto advance = [&](Cursor& c) {  // there is a next tile
-      if (++c.t < c.n) return;
+  if (lo < hi) {
+    // on to the next (b, vh); beyond the share only the unit counts
+    auto next_row = [&](Cursor<U>& c) {
+      c.u += units_of(c.n) - U(c.t);
+      if (c.u >= hi) return;
       c.t = 0;
       if (++c.vh < vheads) return;
       c.vh = 0;
@@ -231,21 +301,45 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         c.n = tiles_of(c.len);
       } while (c.n == 0 && c.b + 1 < a.B);
     };
-    // offset of row lane % 16 of a tile, -1 where there is none
-    auto look_up = [&](const Cursor& c) -> int64_t {
-      const int pos = c.t * kTile + (lane & 15);
-      if (pos >= c.len) return -1;
-      const int i = a.div.quot(pos);
-      const int page = __ldg(a.table + c.b * a.table_row + i);
-      if (page < 0 || page >= a.num_pages) {
-        atomicOr(a.status, kPagerBadPage);
-        return -1;
-      }
-      return page * a.page + (pos - i * a.div.d) * a.row + (c.vh / a.parts) * a.head;
+    auto advance = [&](Cursor<U>& c) {
+      ++c.t;
+      ++c.u;
+      if (c.t >= c.n) next_row(c);
     };
-    auto issue = [&](int stage, int64_t off) {
+    Cursor<U> at;  // of the tile whose rows are looked up next
+    at.u = lo;
+    at.b = sh.start_b[warp];
+    at.len = sh.start_len[warp];
+    at.n = tiles_of(at.len);
+    {
+      const U r = lo - static_cast<U>(sh.start_unit[warp]), per = units_of(at.n);
+      at.vh = static_cast<int>(r / per);
+      at.t = static_cast<int>(r - U(at.vh) * per);
+    }
+    if (at.t >= at.n) next_row(at);
+    Cursor<U> now = at;  // of the tile computed next
+    // Row lane % 16 of a tile: its page, kNoRow behind the last row, and its offset
+    // in the page.  The page is not looked at before the rows are asked for, so
+    // that the load from the table is under way meanwhile.
+    struct Row {
+      int page;
+      int64_t in_page;
+    };
+    constexpr int kNoRow = INT_MIN;
+    auto look_up = [&](const Cursor<U>& c) -> Row {
+      const int pos = c.t * kTile + (lane & 15);
+      if (pos >= c.len) return {kNoRow, 0};
+      const int i = a.div.quot(pos);
+      // a table entry of INT_MIN is as bad as any negative one
+      return {max(__ldg(a.table + c.b * a.table_row + i), kNoRow + 1),
+              (pos - i * a.div.d) * a.row + (c.vh / a.parts) * a.head};
+    };
+    auto issue = [&](int stage, const Row& row) {
       constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of an instruction
-      const uint32_t live = __ballot_sync(~0u, off >= 0);
+      const bool in_cache = row.page >= 0 && row.page < a.num_pages;
+      if (!in_cache && row.page != kNoRow) atomicOr(a.status, kPagerBadPage);
+      const int64_t off = in_cache ? row.page * a.page + row.in_page : -1;
+      const uint32_t live = __ballot_sync(~0u, in_cache);
       if (lane == 0) sh.live[warp][stage] = live;
       const uint32_t k_at = ring_addr + stage * C::kStageBytes, v_at = k_at + kTile * D * 2;
       const int c = lane % kLanes;
@@ -261,21 +355,24 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       }
     };
 
-    int64_t asked = 0;  // tiles looked up
-    int64_t off = look_up(at);
-    asked = 1;
+    Row ahead[C::kStages];
+    uint32_t have = 0;
 #pragma unroll
     for (int s = 0; s < C::kStages; ++s) {
-      if (s < count) {
-        issue(s, off);
-        if (asked < count) {
-          advance(at);
-          off = look_up(at);
-          ++asked;
-        }
+      if (at.u < hi) {
+        have |= 1u << s;
+        ahead[s] = look_up(at);
+        advance(at);
       }
+    }
+#pragma unroll
+    for (int s = 0; s < C::kStages; ++s) {
+      if (have >> s & 1) issue(s, ahead[s]);
       cp_async_commit();
     }
+    bool more = at.u < hi;
+    Row next{kNoRow, 0};  // of the tile issued next
+    if (more) next = look_up(at);
 
     float o_acc[D / 16][NT][4], m[NT][2], l[NT][2];
     uint32_t qf[D / 16][NT][2];
@@ -284,7 +381,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     bool fresh = true;
     const float scale_log2 = a.scale * kLog2e;
 
-    for (int64_t done = 0; done < count; ++done) {
+    while (now.u < hi) {
       if (fresh) {
         fresh = false;
         t0 = now.t;
@@ -387,7 +484,8 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       }
       __syncwarp();  // the stage is read
 
-      const bool row_ends = now.t + 1 == now.n, share_ends = done + 1 == count;
+      const bool row_ends = now.t + 1 == now.n;
+      const bool share_ends = (row_ends ? now.u + (units_of(now.n) - U(now.t)) : now.u + 1) >= hi;
       if (row_ends || share_ends) {
         const bool whole = row_ends && t0 == 0;
         // a part of a row: the share's first waits in the park, its last in the ring
@@ -425,19 +523,17 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
           }
           __syncwarp();
         } else if (lane == 0) {
-          sh.part[slot] = {lo + done - now.t, now.b, now.vh, t0, now.t + 1, now.n};
+          sh.part[slot] = {int64_t(now.u - U(now.t)), now.b, now.vh, t0, now.t + 1, now.n};
         }
         fresh = true;
       }
-      if (!share_ends) advance(now);
+      advance(now);
 
-      if (done + C::kStages < count) {
-        issue(stage, off);
-        if (asked < count) {
-          advance(at);
-          off = look_up(at);
-          ++asked;
-        }
+      if (more) {
+        issue(stage, next);
+        advance(at);
+        more = at.u < hi;
+        if (more) next = look_up(at);
       }
       cp_async_commit();
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
@@ -462,21 +558,24 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     return reinterpret_cast<const float*>(slot & 1 ? base : base + C::kStages * C::kStageBytes);
   };
   constexpr int kQuads = D / 4;
-  int open[2] = {-1, -1};  // parts that go on in other CTAs, by their place in global memory
-  for (int s = 0; s < 2 * kDecodeWarps;) {
-    if (sh.part[s].n == 0) {
-      ++s;
-      continue;
-    }
+  uint32_t held, heads_at;  // slots that hold a part, and those where a row's first part is
+  {
+    const Stretch p = sh.part[lane & (2 * kDecodeWarps - 1)];
+    const bool have = lane < 2 * kDecodeWarps && p.n > 0;
+    held = __ballot_sync(~0u, have);
+    const uint32_t below = held & ((1u << lane) - 1);
+    const int prev = below ? 31 - __clz(below) : lane;
+    const int prev_b = __shfl_sync(~0u, p.b, prev), prev_vh = __shfl_sync(~0u, p.vh, prev);
+    heads_at = __ballot_sync(~0u, have && (!below || prev_b != p.b || prev_vh != p.vh));
+  }
+  int open[2] = {-1, -1};  // slots of parts that go on in other CTAs, by their place in global memory
+  while (heads_at) {
+    const int s = __ffs(heads_at) - 1;
+    heads_at &= heads_at - 1;
+    const int end = heads_at ? __ffs(heads_at) - 1 : 2 * kDecodeWarps;
+    const uint32_t parts = held & ((1u << end) - (1u << s));
     const Stretch p = sh.part[s];
-    int end = s, t1 = p.t1;  // slots [s, end) of the same (b, vh)
-    for (int x = s; x < 2 * kDecodeWarps; ++x) {
-      if (sh.part[x].n == 0) continue;
-      if (sh.part[x].b != p.b || sh.part[x].vh != p.vh) break;
-      end = x + 1;
-      t1 = sh.part[x].t1;
-    }
-    const bool whole = p.t0 == 0 && t1 == p.n;
+    const bool whole = p.t0 == 0 && sh.part[31 - __clz(parts)].t1 == p.n;
     const int place = p.t0 == 0 ? 1 : 0;
     int kv, first, heads;
     heads_of(a, p.vh, &kv, &first, &heads);
@@ -484,78 +583,146 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     float* ml_out = a.part_ml + (int64_t(cta) * 2 + place) * (C::kHeads * 2);
     for (int i = tid; i < heads * kQuads; i += kDecodeWarps * 32) {
       const int h = i / kQuads, d = 4 * (i % kQuads);
-      float top = -INFINITY;
-      for (int x = s; x < end; ++x)
-        if (sh.part[x].n) top = fmaxf(top, sh.m[x][h]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = s; x < end; ++x) {
-        if (sh.part[x].n == 0) continue;
-        const float w = fast_exp2(sh.m[x][h] - ref);
-        const float4 v = *reinterpret_cast<const float4*>(part_o(x) + o_at<D>(h, d));
-        sum += w * sh.l[x][h];
-        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+      Joined sum;
+      for (uint32_t left = parts; left;) {
+        constexpr int kBatch = 4;
+        float2 ml[kBatch];
+        float4 v[kBatch];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          ml[x] = make_float2(-INFINITY, 0.f);
+          v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (left) {
+            const int slot = __ffs(left) - 1;
+            left &= left - 1;
+            ml[x] = make_float2(sh.m[slot][h], sh.l[slot][h]);
+            v[x] = *reinterpret_cast<const float4*>(part_o(slot) + o_at<D>(h, d));
+          }
+        }
+        sum.add(ml, v);
       }
       if (whole) {
-        const float by = sum == 0.f ? 0.f : 1.f / sum;
-        store_out4(a, D, p.b, first + h, d, make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
-        if (d == 0) a.lse[int64_t(first + h) * a.B + p.b] = lse_of(ref, sum);
+        store_joined(a, D, p.b, first + h, d, sum);
       } else {
-        __stcg(reinterpret_cast<float4*>(o_out + h * D + d), o);
-        if (d == 0) __stcg(reinterpret_cast<float2*>(ml_out + 2 * h), make_float2(top, sum));
+        __stcg(reinterpret_cast<float4*>(o_out + h * D + d), sum.o);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(ml_out + 2 * h), make_float2(sum.top, sum.sum));
       }
     }
-    if (!whole) open[place] = s;
-    s = end;
+    if (!whole) (place == 0 ? open[0] : open[1]) = s;
   }
 
   // ---- rows that several CTAs share: the last to arrive joins them
   if (open[0] < 0 && open[1] < 0) return;
-  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    const int slot = tid == 0 ? open[0] : open[1];
+    if (slot >= 0) {
+      const Stretch p = sh.part[slot];
+      const int from = taker(total, ctas, static_cast<U>(p.u0)), to = taker(total, ctas, static_cast<U>(p.u0) + p.n - 1);
+      // releases what this CTA wrote (the barrier above orders its threads' writes
+      // before), and acquires what the others did
+      const int others = arrive(a.counters + from);
+      sh.arrived[tid] = others == to - from ? 1 : 0;
+      sh.from[tid] = from;
+      sh.to[tid] = to;
+      if (others == to - from) a.counters[from] = 0;  // for the next launch
+    }
+  }
+  __syncthreads();
+#pragma unroll
   for (int place = 0; place < 2; ++place) {
-    if (open[place] < 0) continue;
+    if (open[place] < 0 || !sh.arrived[place]) continue;
     const Stretch p = sh.part[open[place]];
-    const int from = taker(total, ctas, p.u0), to = taker(total, ctas, p.u0 + p.n - 1);
-    __syncthreads();
-    if (tid == 0) sh.arrived = atomicAdd(a.counters + from, 1);
-    __syncthreads();
-    if (sh.arrived != to - from) continue;
-    if (tid == 0) a.counters[from] = 0;  // for the next launch
-    __threadfence();
+    const int from = sh.from[place], to = sh.to[place];
     int kv, first, heads;
     heads_of(a, p.vh, &kv, &first, &heads);
     // the row's part in CTA i: its last share (place 1) where it begins, else its first
     auto place_of = [&](int i) { return int64_t(i) * 2 + (i == from ? 1 : 0); };
+    auto ml_of = [&](int x, int h) {
+      return __ldcg(reinterpret_cast<const float2*>(a.part_ml + place_of(x) * (C::kHeads * 2) + 2 * h));
+    };
+    auto o_of = [&](int x, int h, int d) {
+      return __ldcg(reinterpret_cast<const float4*>(a.part_o + place_of(x) * (C::kHeads * D) + h * D + d));
+    };
+    constexpr int kBatch = 16, kDeep = 16;
+    if (to - from < kBatch) {  // a few parts: everything in one round of loads
+      for (int i = tid; i < heads * kQuads; i += kDecodeWarps * 32) {
+        const int h = i / kQuads, d = 4 * (i % kQuads);
+        float2 ml[kBatch];
+        float4 v[kBatch];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const bool have = from + x <= to;
+          ml[x] = have ? ml_of(from + x, h) : make_float2(-INFINITY, 0.f);
+          v[x] = have ? o_of(from + x, h, d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        Joined sum;
+        sum.add(ml, v);
+        store_joined(a, D, p.b, first + h, d, sum);
+      }
+      continue;
+    }
+    // many: the parts' weights first, a warp for each head, then sums that wait
+    // for nothing but their loads
+    float* weight = reinterpret_cast<float*>(smem);  // [part][head]
+    const int parts = to - from + 1;
+    for (int h = warp; h < heads; h += kDecodeWarps) {
+      constexpr int kMost = 10;  // of the parts of up to 320 CTAs a lane has this many
+      float2 ml[kMost];
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        const int x = lane + 32 * i;
+        ml[i] = x < parts ? ml_of(from + x, h) : make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) top = fmaxf(top, ml[i].x);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int i = 0; i < kMost; ++i) {
+        const int x = lane + 32 * i;
+        const float w = fast_exp2(ml[i].x - ref);
+        sum += w * ml[i].y;
+        if (x < parts) weight[x * C::kHeads + h] = w;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      if (lane == 0) {
+        a.lse[int64_t(first + h) * a.B + p.b] = lse_of(ref, sum);
+        sh.l[0][h] = sum == 0.f ? 0.f : 1.f / sum;
+      }
+    }
+    __syncthreads();
     for (int i = tid; i < heads * kQuads; i += kDecodeWarps * 32) {
       const int h = i / kQuads, d = 4 * (i % kQuads);
-      float top = -INFINITY;
-      for (int x = from; x <= to; ++x) top = fmaxf(top, __ldcg(a.part_ml + place_of(x) * (C::kHeads * 2) + 2 * h));
-      const float ref = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int x = from; x <= to; ++x) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + place_of(x) * (C::kHeads * 2) + 2 * h));
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + place_of(x) * (C::kHeads * D) + h * D + d));
-        const float w = fast_exp2(ml.x - ref);
-        sum += w * ml.y;
-        o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+      for (int x0 = 0; x0 < parts; x0 += kDeep) {
+        float4 v[kDeep];
+#pragma unroll
+        for (int x = 0; x < kDeep; ++x) v[x] = o_of(min(from + x0 + x, to), h, d);
+#pragma unroll
+        for (int x = 0; x < kDeep; ++x) {
+          const float w = weight[(x0 + x) * C::kHeads + h];
+          if (x0 + x < parts) o.x += w * v[x].x, o.y += w * v[x].y, o.z += w * v[x].z, o.w += w * v[x].w;
+        }
       }
-      const float by = sum == 0.f ? 0.f : 1.f / sum;
+      const float by = sh.l[0][h];
       store_out4(a, D, p.b, first + h, d, make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
-      if (d == 0) a.lse[int64_t(first + h) * a.B + p.b] = lse_of(ref, sum);
     }
+    __syncthreads();  // the weights are read
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, typename U>
 cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
   using C = DecodeCfg<D, NT>;
+  if (sms * C::kCtasPerSm > 320) return cudaErrorNotSupported;  // what one warp joins
   static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<D, NT>) + 1024) <= 233472, "shared memory of an SM");
-  cudaError_t e = set_smem_limit_once<decode_kernel<D, NT>>(C::kSmemBytes);
+  cudaError_t e = set_smem_limit_once<decode_kernel<D, NT, U>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, NT><<<sms * C::kCtasPerSm, kDecodeWarps * 32, C::kSmemBytes, stream>>>(a);
+  decode_kernel<D, NT, U><<<sms * C::kCtasPerSm, kDecodeWarps * 32, C::kSmemBytes, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -570,9 +737,13 @@ DecodeSpace decode_space(int D, int part_heads, int sms) {
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t stream) {
-  if (a.part_heads <= 8)
-    return a.D == 128 ? launch<128, 1>(a, sms, stream) : launch<64, 1>(a, sms, stream);
-  return a.D == 128 ? launch<128, 2>(a, sms, stream) : launch<64, 2>(a, sms, stream);
+  // the units of B full table rows
+  const int64_t most = int64_t(a.B) * (int64_t(a.max_pages) * a.div.d / kTile + 1 + kRowUnits);
+  const bool wide = most > UINT32_MAX / (a.Hkv * a.parts);
+#define JFA_DECODE(D, NT) (wide ? launch<D, NT, uint64_t>(a, sms, stream) : launch<D, NT, uint32_t>(a, sms, stream))
+  if (a.part_heads <= 8) return a.D == 128 ? JFA_DECODE(128, 1) : JFA_DECODE(64, 1);
+  return a.D == 128 ? JFA_DECODE(128, 2) : JFA_DECODE(64, 2);
+#undef JFA_DECODE
 }
 
 }  // namespace jfa

@@ -12,177 +12,219 @@ namespace {
 //
 // Per request: pages(n) = ceil(n / page_size), held = pages(lens),
 // need = pages(lens + delta).  Three prefix sums in the order of the requests
-// -- new rows, pages given back, pages taken -- place everything: a page given
-// back goes to free_list[n_free + give + i], the i-th page a request takes is
-// free_list[top - 1 - take - i] with top = n_free + all pages given back.
+// -- new rows, pages given back, pages taken -- place everything: the p-th page
+// given back goes to free_list[n_free + p], the p-th page taken is
+// free_list[top - 1 - p] with top = n_free + all pages given back.  A page or row
+// finds its request by a search in the sums.
+//
+// Bound: a handful of dependent loads.  One launch does it all: one CTA, or for
+// many rows a cluster of 8 that each form the sums for themselves -- cheaper than
+// a second launch -- and share out pages and rows; the cluster's barrier stands
+// between giving and taking, and before lengths are overwritten in place.
 // ---------------------------------------------------------------------------
-constexpr int kTableThreads = 1024;
+constexpr int kTableThreads = 1024, kTableCluster = 8;
 
 struct Need {
   int64_t rows, give, take;
+  __device__ __forceinline__ void add(const Need& o) { rows += o.rows, give += o.give, take += o.take; }
 };
 
 __device__ __forceinline__ int clamp_int(int64_t v) { return v > INT_MAX ? INT_MAX : static_cast<int>(v); }
 
+__device__ __forceinline__ Need warp_scan(Need v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Need u{__shfl_up_sync(~0u, v.rows, o), __shfl_up_sync(~0u, v.give, o), __shfl_up_sync(~0u, v.take, o)};
+    if (lane >= o) v.add(u);
+  }
+  return v;
+}
+
 // Inclusive sums over the block's threads; *total receives the block's sum.
 __device__ Need block_scan(Need v, Need (&warp_sum)[32], Need* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t r = __shfl_up_sync(~0u, v.rows, o), g = __shfl_up_sync(~0u, v.give, o),
-                  t = __shfl_up_sync(~0u, v.take, o);
-    if (lane >= o) v.rows += r, v.give += g, v.take += t;
-  }
+  v = warp_scan(v);
   if (lane == 31) warp_sum[warp] = v;
   __syncthreads();
-  Need before{0, 0, 0}, all{0, 0, 0};
-  for (int w = 0; w < kTableThreads / 32; ++w) {
-    const Need s = warp_sum[w];
-    if (w < warp) before.rows += s.rows, before.give += s.give, before.take += s.take;
-    all.rows += s.rows, all.give += s.give, all.take += s.take;
-  }
-  __syncthreads();
-  *total = all;
-  return {v.rows + before.rows, v.give + before.give, v.take + before.take};
+  const Need sums = warp_scan(warp_sum[lane]);
+  auto from = [&](int w) -> Need {
+    return {__shfl_sync(~0u, sums.rows, w), __shfl_sync(~0u, sums.give, w), __shfl_sync(~0u, sums.take, w)};
+  };
+  *total = from(31);
+  const Need before = from(max(warp - 1, 0));
+  if (warp > 0) v.add(before);
+  __syncthreads();  // the sums are read
+  return v;
 }
 
+// The last b in [lo, n) with at[b] <= p; at[lo] <= p.
+__device__ __forceinline__ int owner_of(const int* at, int lo, int n, int p) {
+  int hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at[mid] <= p) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void all_arrive(bool cluster) {
+  if (cluster) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+}
+
+// No pointer is __restrict__ and nothing goes through the read-only cache: lens
+// and n_free may be overwritten in place.
 __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_constant__ TablesArgs a) {
   extern __shared__ int sm[];
-  int* row_at = sm;              // [B + 1] first new row of each request
-  int* give_at = sm + a.B + 1;   // [B] pages given back before it; -1: left as it was
-  int* take_at = give_at + a.B;  // [B] pages taken before it; -1: left as it was
+  int* row_at = sm;              // [B + 1] new rows before each request
+  int* give_at = sm + a.B + 1;   // [B] pages given back before it; later: whether it is served
+  int* take_at = give_at + a.B;  // [B] pages taken before it
   __shared__ Need warp_sum[32];
-  __shared__ int problem;
+  __shared__ int problem, taken;
   const int capacity = a.max_pages * a.div.d;
-  const int tid = threadIdx.x;
-  if (tid == 0) problem = 0;
-  __syncthreads();
+  const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x;
+  const int all = tid + rank * kTableThreads, stride = ranks * kTableThreads;
+  const int64_t n_free = a.n_free[0];
+  if (tid == 0) problem = taken = 0;
+  auto pages = [&](int n) { return a.div.quot(n + a.div.d - 1); };
 
+  // Sums over all requests.  The first round takes it that `rows` holds the new
+  // rows; where it does not, a second one leaves out those that do not fit.
+  auto sound_length = [&](int64_t len, int64_t after) {
+    return len >= 0 && len <= capacity && after >= 0 && after <= capacity;
+  };
   Need carry{0, 0, 0};
-  for (int base = 0; base < a.B; base += kTableThreads) {
-    const int b = base + tid;
-    Need n{0, 0, 0};
-    int64_t len = 0, after = 0;
-    if (b < a.B) {
-      len = a.lens[b];
-      after = len + a.delta[b];
-      n.rows = max(a.delta[b], 0);
-    }
-    Need total;
-    Need rows_only{n.rows, 0, 0};
-    const int64_t row_end = carry.rows + block_scan(rows_only, warp_sum, &total).rows;
-    const int64_t rows_total = total.rows;
-    bool ok = false;
-    if (b < a.B) {
-      ok = len >= 0 && len <= capacity && after >= 0 && after <= capacity &&
-           (after <= len || row_end <= a.rows);
-      if (ok) {
-        const int held = a.div.quot(static_cast<int>(len) + a.div.d - 1);
-        const int need = a.div.quot(static_cast<int>(after) + a.div.d - 1);
-        n.give = max(held - need, 0);
-        n.take = max(need - held, 0);
-      } else {
-        atomicOr(&problem, kPagerBadLength);
+  bool fits = true;
+  for (int round = 0; round < 2; ++round) {
+    carry = {0, 0, 0};
+    for (int base = 0; base < a.B; base += kTableThreads) {
+      const int b = base + tid;
+      Need n{0, 0, 0};
+      if (b < a.B) {
+        const int64_t len = a.lens[b], delta = a.delta[b];
+        n.rows = max(delta, int64_t(0));
+        if (sound_length(len, len + delta) && (fits || delta <= 0 || row_at[b] + n.rows <= a.rows)) {
+          const int held = pages(static_cast<int>(len)), need = pages(static_cast<int>(len + delta));
+          n.give = max(held - need, 0);
+          n.take = max(need - held, 0);
+        }
       }
+      Need total;
+      const Need to = block_scan(n, warp_sum, &total);
+      if (b < a.B) {
+        row_at[b] = clamp_int(carry.rows + to.rows - n.rows);
+        give_at[b] = clamp_int(carry.give + to.give - n.give);
+        take_at[b] = clamp_int(carry.take + to.take - n.take);
+      }
+      carry.add(total);
     }
-    const Need incl = block_scan({0, n.give, n.take}, warp_sum, &total);
-    if (b < a.B) {
-      row_at[b] = clamp_int(row_end - n.rows);
-      give_at[b] = ok ? clamp_int(carry.give + incl.give - n.give) : -1;
-      take_at[b] = ok ? clamp_int(carry.take + incl.take - n.take) : -1;
-    }
-    carry.rows += rows_total;
-    carry.give += total.give;
-    carry.take += total.take;
+    if (carry.rows <= a.rows) break;
+    fits = false;
   }
   if (tid == 0) row_at[a.B] = clamp_int(carry.rows);
-  __syncthreads();
-
-  const int64_t n_free = a.n_free[0];
   const int64_t top = n_free + carry.give;
   const bool sound = n_free >= 0 && top <= a.num_pages;
-  if (!sound && tid == 0) atomicOr(&problem, kPagerBadPage);
-
-  // pages given back, a warp per request
-  const int lane = tid & 31;
-  if (sound) {
-    for (int b = tid >> 5; b < a.B; b += kTableThreads / 32) {
-      if (give_at[b] < 0 || a.delta[b] >= 0) continue;
-      const int len = a.lens[b];
-      const int held = a.div.quot(len + a.div.d - 1), need = a.div.quot(len + a.delta[b] + a.div.d - 1);
-      for (int i = need + lane; i < held; i += 32)
-        a.free_list[n_free + give_at[b] + (i - need)] = a.table[b * a.table_row + i];
-    }
-  }
   __syncthreads();
 
-  // pages taken, and the new lengths
-  for (int b = tid >> 5; b < a.B; b += kTableThreads / 32) {
-    const int len = a.lens[b], delta = a.delta[b];
-    bool ok = sound && give_at[b] >= 0;
-    if (ok && delta > 0) {
-      const int held = a.div.quot(len + a.div.d - 1), need = a.div.quot(len + delta + a.div.d - 1);
-      if (need > held && int64_t(take_at[b]) + (need - held) > top) {
-        ok = false;
-        if (lane == 0) atomicOr(&problem, kPagerNoPages);
-      } else {
-        for (int i = held + lane; i < need; i += 32)
-          a.table[b * a.table_row + i] = a.free_list[top - 1 - take_at[b] - (i - held)];
-      }
+  if (sound && carry.give > 0) {
+    for (int p = all; p < carry.give; p += stride) {
+      const int b = owner_of(give_at, 0, a.B, p);
+      a.free_list[n_free + p] = a.table[b * a.table_row + pages(a.lens[b] + a.delta[b]) + (p - give_at[b])];
     }
-    __syncwarp();
-    if (lane == 0 && !ok) give_at[b] = -1;  // from here on: whether the request was served
+    all_arrive(ranks > 1);  // what is given back may be taken again; give_at is read
   }
-  __syncthreads();
 
-  // the lowest refused need marks where the takers stop
-  if (tid == 0) {
-    int64_t taken = 0;
-    for (int b = 0; b < a.B; ++b) {
-      if (give_at[b] < 0) continue;
-      const int len = a.lens[b];
-      taken += max(a.div.quot(len + a.delta[b] + a.div.d - 1) - a.div.quot(len + a.div.d - 1), 0);
-    }
-    a.n_free_out[0] = static_cast<int>(sound ? top - taken : n_free);
-  }
-  for (int64_t r = tid; r < a.rows; r += kTableThreads) {
-    int slot = -1, position = 0;
-    if (r < row_at[a.B]) {
-      int lo = 0, hi = a.B;  // the last request whose rows begin at or before r, and has rows
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (row_at[mid] <= r) lo = mid; else hi = mid;
-      }
-      position = static_cast<int>(int64_t(a.lens[lo]) + (r - row_at[lo]));
-      if (give_at[lo] >= 0) {
-        const int i = a.div.quot(position);
-        const int page = a.table[lo * a.table_row + i];
-        if (page >= 0 && page < a.num_pages)
-          slot = page * a.div.d + (position - i * a.div.d);
-        else
-          atomicOr(&problem, kPagerBadPage);
-      }
-    }
-    a.slots[r] = slot;
-    a.positions[r] = position;
-  }
-  for (int b = tid; b <= a.B; b += kTableThreads) a.row_offsets[b] = row_at[b];
-  __syncthreads();
+  // who is served: give_at becomes that flag
   for (int b = tid; b < a.B; b += kTableThreads) {
-    const int len = a.lens[b];
-    a.lens_out[b] = give_at[b] >= 0 ? len + a.delta[b] : len;
+    const int64_t len = a.lens[b], delta = a.delta[b], after = len + delta;
+    bool ok = sound_length(len, after) && (fits || delta <= 0 || row_at[b] + delta <= a.rows);
+    if (!ok) {
+      if (rank == 0) atomicOr(&problem, kPagerBadLength);
+    } else if (!sound) {
+      ok = false;
+    } else if (const int n = pages(static_cast<int>(after)) - pages(static_cast<int>(len)); n > 0) {
+      if (int64_t(take_at[b]) + n <= top) {
+        atomicMax(&taken, take_at[b] + n);
+      } else {
+        ok = false;
+        if (rank == 0) atomicOr(&problem, kPagerNoPages);
+      }
+    }
+    give_at[b] = ok;
   }
-  if (tid == 0 && problem) atomicOr(a.status, problem);
+  __syncthreads();
+
+  for (int p = all; p < taken; p += stride) {
+    const int b = owner_of(take_at, 0, a.B, p);
+    a.table[b * a.table_row + pages(a.lens[b]) + (p - take_at[b])] = a.free_list[top - 1 - p];
+  }
+
+  // A warp has runs of 32 * kRun rows, a lane every 32nd of them: it searches for
+  // the first one's request and walks on from there.
+  constexpr int kRun = 4;
+  const int lane = tid & 31;
+  const int new_rows = row_at[a.B];
+  for (int64_t base = int64_t(all - lane) * kRun; base < a.rows; base += int64_t(stride) * kRun) {
+    int b = -1;
+    for (int k = 0; k < kRun; ++k) {
+      const int64_t r = base + 32 * k + lane;
+      if (r >= a.rows) break;
+      int slot = -1, position = 0;
+      if (r < new_rows) {
+        const int row = static_cast<int>(r);
+        if (b < 0) b = owner_of(row_at, 0, a.B, row);
+        while (row_at[b + 1] <= row) ++b;
+        const int len = a.lens[b];
+        position = static_cast<int>(int64_t(len) + (row - row_at[b]));
+        if (give_at[b]) {
+          const int i = a.div.quot(position), held = pages(len);
+          // entries of new pages are on their way into the table: take them where they come from
+          const int page = i < held ? a.table[b * a.table_row + i] : a.free_list[top - 1 - take_at[b] - (i - held)];
+          if (page >= 0 && page < a.num_pages)
+            slot = page * a.div.d + (position - i * a.div.d);
+          else
+            atomicOr(&problem, kPagerBadPage);
+        }
+      }
+      a.slots[r] = slot;
+      a.positions[r] = position;
+    }
+  }
+  for (int b = all; b <= a.B; b += stride) a.row_offsets[b] = row_at[b];
+  all_arrive(ranks > 1);  // lens and n_free are read
+  for (int b = all; b < a.B; b += stride)
+    a.lens_out[b] = give_at[b] ? a.lens[b] + a.delta[b] : a.lens[b];
+  if (tid == 0) {
+    const int bits = problem | (sound ? 0 : kPagerBadPage);
+    if (rank == 0) a.n_free_out[0] = static_cast<int>(sound ? top - taken : n_free);
+    if (bits) atomicOr(a.status, bits);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
-  const int smem = (3 * a.B + 1) * 4;
   cudaError_t e = set_smem_limit_once<tables_kernel>((3 * 16384 + 1) * 4);
   if (e != cudaSuccess) return e;
-  tables_kernel<<<1, kTableThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  // one CTA while its threads have no more than one run of rows each
+  const bool many = a.rows > 4 * kTableThreads;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(many ? kTableCluster : 1);
+  cfg.blockDim = dim3(kTableThreads);
+  cfg.dynamicSmemBytes = (3 * a.B + 1) * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = many ? kTableCluster : 1;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tables_kernel, a);
 }
 
 }  // namespace jfa

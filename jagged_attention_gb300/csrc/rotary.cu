@@ -23,32 +23,85 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-__device__ __forceinline__ void load8(const void* base, int64_t at, bool f32, float (&x)[8]) {
-  if (f32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// 8 values as they lie in memory.
+template <bool kF32>
+struct Run {
+  uint4 w[kF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + at * (kF32 ? 4 : 2));
+    w[0] = p[0];
+    if (kF32) w[kF32 ? 1 : 0] = p[1];
+  }
+  __device__ __forceinline__ void store(void* base, int64_t at) const {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + at * (kF32 ? 4 : 2));
+    p[0] = w[0];
+    if (kF32) p[1] = w[kF32 ? 1 : 0];
+  }
+  __device__ __forceinline__ void unpack(float (&x)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 8; ++i) {
+      const uint4& q = w[kF32 ? i / 4 : 0];
+      const int e = kF32 ? i % 4 : i / 2;
+      const uint32_t v = e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w;
+      x[i] = __uint_as_float(kF32 ? v : i % 2 ? v & 0xffff0000u : v << 16);
     }
   }
-}
+  __device__ __forceinline__ void pack(const float (&x)[8]) {
+    if (kF32) {
+      w[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+      w[kF32 ? 1 : 0] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    } else {
+      w[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+  }
+};
 
-__device__ __forceinline__ void store8(void* base, int64_t at, bool f32, const float (&x)[8]) {
-  if (f32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-    p[0] = make_float4(x[0], x[1], x[2], x[3]);
-    p[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) =
-        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                   pack_bf16x2(x[6], x[7]));
+// Heads [h0, h1) of one row of a job; `in` and `out` are the row's offsets.
+// The loads of kAtOnce heads are under way together.
+template <bool kInterleaved, bool kF32>
+__device__ __forceinline__ void walk_heads(const RowJob& job, int D, int64_t in, int64_t out, int h0, int h1, int lo,
+                                           int hi, bool turn, const float (&c)[8], const float (&s)[8]) {
+  constexpr int kAtOnce = kF32 ? 2 : 4;
+  for (int h = h0; h < h1; h += kAtOnce) {
+    Run<kF32> a[kAtOnce], b[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (h + i < h1) {
+        a[i].load(job.in, in + int64_t(h + i) * D + lo);
+        b[i].load(job.in, in + int64_t(h + i) * D + hi);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (h + i >= h1) break;
+      if (turn) {
+        float x[8], y[8];
+        a[i].unpack(x);
+        b[i].unpack(y);
+        if (kInterleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = x[2 * e], q = x[2 * e + 1], v = y[2 * e], w = y[2 * e + 1];
+            x[2 * e] = p * c[e] - q * s[e];
+            x[2 * e + 1] = q * c[e] + p * s[e];
+            y[2 * e] = v * c[4 + e] - w * s[4 + e];
+            y[2 * e + 1] = w * c[4 + e] + v * s[4 + e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float p = x[e], q = y[e];
+            x[e] = p * c[e] - q * s[e];
+            y[e] = q * c[e] + p * s[e];
+          }
+        }
+        a[i].pack(x);
+        b[i].pack(y);
+      }
+      const int64_t to = out + (h + i) * job.out_head;
+      a[i].store(job.out, to + lo);
+      b[i].store(job.out, to + hi);
+    }
   }
 }
 
@@ -102,33 +155,10 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
     if (job.scatter && page_at < 0) continue;
     const int64_t in = row * job.in_row;
     const int64_t out = job.scatter ? page * job.out_page + in_page * job.out_row : row * job.out_row;
-    for (int h = h0; h < h1; ++h) {
-      float x[8], y[8];
-      const int64_t from = in + int64_t(h) * a.D, to = out + h * job.out_head;
-      load8(job.in, from + lo, job.f32, x);
-      load8(job.in, from + hi, job.f32, y);
-      if (turning && job.rotate) {
-        if (kInterleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p = x[2 * i], q = x[2 * i + 1], v = y[2 * i], w = y[2 * i + 1];
-            x[2 * i] = p * c[i] - q * s[i];
-            x[2 * i + 1] = q * c[i] + p * s[i];
-            y[2 * i] = v * c[4 + i] - w * s[4 + i];
-            y[2 * i + 1] = w * c[4 + i] + v * s[4 + i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float p = x[i], q = y[i];
-            x[i] = p * c[i] - q * s[i];
-            y[i] = q * c[i] + p * s[i];
-          }
-        }
-      }
-      store8(job.out, to + lo, job.f32, x);
-      store8(job.out, to + hi, job.f32, y);
-    }
+    if (job.f32)
+      walk_heads<kInterleaved, true>(job, a.D, in, out, h0, h1, lo, hi, turning && job.rotate, c, s);
+    else
+      walk_heads<kInterleaved, false>(job, a.D, in, out, h0, h1, lo, hi, turning && job.rotate, c, s);
   }
 }
 
@@ -138,7 +168,11 @@ cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   if (a.rows == 0 || a.heads == 0) return cudaSuccess;
   const int64_t per_block = kRowThreads / (a.D / 16);
   const int64_t blocks = (a.rows + per_block - 1) / per_block;
-  const int split = 1;
+  // A thread walks over all heads of its row where the rows alone fill the SMs
+  // (1024 threads each); of fewer rows the heads are dealt to more threads, which
+  // form their sines again.
+  const int64_t fill = int64_t(sms) * 1024 / kRowThreads;
+  const int split = static_cast<int>(std::min<int64_t>(a.heads, std::max<int64_t>(1, fill / blocks)));
   const int per = (a.heads + split - 1) / split;
   const dim3 grid(static_cast<unsigned>(blocks), (a.heads + per - 1) / per);
   if (a.turns.interleaved)

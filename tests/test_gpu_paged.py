@@ -559,3 +559,15 @@ def test_serving_run(captured):
                 assert abs(float(lse[h, b]) - float(torch.logsumexp(s, 0))) <= moved + 1e-5
         lens_now = lens.cpu().numpy()
         assert [len(x) for x in kept] == lens_now.tolist()
+
+
+def test_decode_tables_wide_enough_for_64_bit_counts():
+    """A table of which full rows would hold more than 2^32 tiles."""
+    pager, q, kp, vp, table, lens = _decode_case([300, 5000, 0, 17], 16, 8, 64, 1024, False, 12)
+    wide = torch.full((4, 1 << 20), -1, dtype=I32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    big = jfa.Pager(max_seqs=4, max_pages=1 << 20, num_pages=kp.shape[0], page_size=1024, H=16, Hkv=8, D=64)
+    assert 4 * ((1 << 20) * 1024 // 16 + 1) * 8 > 2**32 - 1 - 2**31
+    out, lse = _check_decode(big, q, kp, vp, wide, lens)
+    narrow = jfa.paged_decode(pager, q, kp, vp, table, lens, 0.125)
+    assert torch.equal(out, narrow[0]) and torch.equal(lse, narrow[1])
