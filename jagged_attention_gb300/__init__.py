@@ -618,7 +618,7 @@ def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out
         raise TypeError(f"q must be {torch.bfloat16} or {torch.float32}, got {q.dtype}")
     shape = (rows, hq, rotary.D)
     if q_out is None:
-        q_out = q.new_empty(shape)
+        q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
     args = (*_rows("q", q, shape, q.dtype, dev), *_rows("q_out", q_out, shape, q.dtype, dev), hq)
     if k is None:
         if k_out is not None:
@@ -632,7 +632,7 @@ def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out
             raise TypeError(f"k must be {torch.bfloat16} or {torch.float32}, got {k.dtype}")
         shape = (rows, hk, rotary.D)
         if k_out is None:
-            k_out = k.new_empty(shape)
+            k_out = torch.empty(shape, dtype=k.dtype, device=k.device)
         args += (*_rows("k", k, shape, k.dtype, dev), *_rows("k_out", k_out, shape, k.dtype, dev), hk)
     rc = (_lib or lib()).jfa_rotate(rotary.handle, *_positions(positions, rotary, rows, dev), rows, flags, *args,
                                     _raw_stream(stream, dev))
@@ -706,11 +706,16 @@ def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: i
     (lens_out, n_free_out, slots, positions, row_offsets)."""
     dev = pager.index
     B = lens.shape[0]
-    outs = (lens_out, n_free_out, slots, positions, row_offsets)
-    if lens_out is None or n_free_out is None or slots is None or positions is None or row_offsets is None:
-        made = delta.new_empty(2 * B + 2 + 2 * rows).split((B, 1, rows, rows, B + 1))
-        outs = tuple(m if o is None else o for m, o in zip(made, outs))
-    lens_out, n_free_out, slots, positions, row_offsets = outs
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+    if n_free_out is None:
+        n_free_out = torch.empty_like(n_free)
+    if slots is None:
+        slots = torch.empty(rows, dtype=torch.int32, device=pager.device)
+    if positions is None:
+        positions = torch.empty_like(slots)
+    if row_offsets is None:
+        row_offsets = torch.empty(B + 1, dtype=torch.int32, device=pager.device)
     rc = (_lib or lib()).jfa_paged_tables(
         pager.handle, B, _ints("lens", lens, B, dev), _ints("delta", delta, B, dev),
         _ints("lens_out", lens_out, B, dev), *_table(table, pager, B, dev),
@@ -720,7 +725,7 @@ def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: i
         _raw_stream(stream, dev))
     if rc:
         _check(rc, "jfa_paged_tables")
-    return outs
+    return lens_out, n_free_out, slots, positions, row_offsets
 
 
 def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary | None = None,
@@ -741,7 +746,7 @@ def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary 
     if q is not None:
         q_shape = (rows, pager.H, pager.D)
         if q_out is None:
-            q_out = q.new_empty(q_shape)
+            q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=pager.device)
         q_args = (*_rows("q", q, q_shape, torch.bfloat16, dev), *_rows("q_out", q_out, q_shape, torch.bfloat16, dev))
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -763,9 +768,9 @@ def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *
     shape = (B, H, D)
     q_at = _rows("q", q, shape, torch.bfloat16, dev)
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=pager.device)
     if lse is None:
-        lse = q.new_empty((H, B), dtype=torch.float32)
+        lse = torch.empty((H, B), dtype=torch.float32, device=pager.device)
     elif lse.dtype != torch.float32 or lse.get_device() != dev or lse.shape != (H, B) or not lse.is_contiguous():
         raise ValueError(f"lse must be contiguous float32 [{H}, {B}] on {pager.device}")
     out_at, out_row = _rows("out", out, shape, torch.bfloat16, dev)

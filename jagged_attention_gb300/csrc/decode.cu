@@ -42,7 +42,7 @@ template <int D, int NT>  // NT: tiles of 8 query heads
 struct DecodeCfg {
   static constexpr int kHeads = 8 * NT;
   static constexpr int kStageBytes = 2 * kTile * D * 2;  // K and V
-  static constexpr int kStages = D == 128 && NT == 1 ? 3 : 2;
+  static constexpr int kStages = 2;
   static constexpr int kOutBytes = kHeads * D * 4;  // a stretch's O
   static_assert(kOutBytes <= kStageBytes, "a used stage holds a stretch's O");
   static constexpr int kWarpBytes = kStages * kStageBytes + kOutBytes;
@@ -52,7 +52,13 @@ struct DecodeCfg {
 
 // Units of work: a (request, virtual head) of n tiles counts n units for them,
 // and kRowUnits behind them for its beginning and end.
-constexpr int kRowUnits = 1;
+constexpr int kRowUnits = 2;
+
+// Parts of a row that one CTA joins at a time, where a row has more than twice as many.
+constexpr int kGroup = 8;
+
+// Few rows of at most this many tiles get a CTA each.
+constexpr int kApartTiles = 3 * kDecodeWarps;
 
 // Where a warp stands: tile t of n of the rows of (request b, virtual head vh),
 // unit u of all.
@@ -100,7 +106,7 @@ struct DecodeShared {
   int64_t start_unit[kDecodeWarps];  // where the request begins in which a warp's share does
   int start_b[kDecodeWarps], start_len[kDecodeWarps];
   uint32_t live[kDecodeWarps][DecodeCfg<D, NT>::kStages];  // rows of a stage that count
-  int arrived[2], from[2], to[2];
+  int from[2], to[2], last[2];
 };
 
 __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
@@ -110,9 +116,17 @@ __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
 
 __device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+// The cache is read once a launch: its lines are the first to leave L2, before the
+// lengths, tables and queries.
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take, uint64_t policy) {
   const int bytes = take ? 16 : 0;  // 0: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes),
+               "l"(policy) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -185,6 +199,13 @@ __device__ __forceinline__ int arrive(int* counter) {
   asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(was) : "l"(counter) : "memory");
   return was;
 }
+// Whether the caller is the last of `count` at a counter, which starts again then.
+// A barrier before orders the other threads' writes, one behind their reads.
+__device__ __forceinline__ bool last_of(int* counter, int count) {
+  if (arrive(counter) != count - 1) return false;
+  *counter = 0;
+  return true;
+}
 __device__ __forceinline__ float lse_of(float m, float l) { return m * kLn2 + logf(l); }
 
 // A finished row: normalised, with its log-sum-exp.
@@ -243,15 +264,14 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     all_rows += y;
     most = max(most, sh.scan_most[w]);
   }
-  // few and short rows: a CTA for each, whose warps have no more tiles than their
-  // rings hold; nothing is left to be joined between CTAs then
-  const bool apart = most <= C::kStages * kDecodeWarps && int64_t(all_rows) * vheads <= gridDim.x;
+  // few and short rows: a CTA for each, so that nothing is left to be joined between CTAs
+  const bool apart = most <= kApartTiles && int64_t(all_rows) * vheads <= gridDim.x;
   if (apart) {
-    units = U(rows) * (C::kStages * kDecodeWarps);
-    units_to = U(rows_to) * (C::kStages * kDecodeWarps);
-    total = U(all_rows) * (C::kStages * kDecodeWarps);
+    units = U(rows) * (kApartTiles);
+    units_to = U(rows_to) * (kApartTiles);
+    total = U(all_rows) * (kApartTiles);
   }
-  auto units_of = [&](int n) -> U { return n == 0 ? 0 : apart ? C::kStages * kDecodeWarps : n + kRowUnits; };
+  auto units_of = [&](int n) -> U { return n == 0 ? 0 : apart ? kApartTiles : n + kRowUnits; };
   total *= vheads;
   const int ctas = apart ? max(1, all_rows * vheads) : ctas_of(total, static_cast<int>(gridDim.x));
   const int cta = blockIdx.x;
@@ -334,6 +354,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       return {max(__ldg(a.table + c.b * a.table_row + i), kNoRow + 1),
               (pos - i * a.div.d) * a.row + (c.vh / a.parts) * a.head};
     };
+    const uint64_t policy = read_once_policy();
     auto issue = [&](int stage, const Row& row) {
       constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of an instruction
       const bool in_cache = row.page >= 0 && row.page < a.num_pages;
@@ -350,8 +371,8 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         const bool take = o >= 0;
         const int64_t src = (take ? o : 0) + c * 8;
         const uint32_t dst = r * (D * 2) + ((c ^ (r & 7)) << 4);
-        cp_async16(k_at + dst, a.k + src, take);
-        cp_async16(v_at + dst, a.v + src, take);
+        cp_async16(k_at + dst, a.k + src, take, policy);
+        cp_async16(v_at + dst, a.v + src, take, policy);
       }
     };
 
@@ -611,114 +632,88 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     if (!whole) (place == 0 ? open[0] : open[1]) = s;
   }
 
-  // ---- rows that several CTAs share: the last to arrive joins them
+  // ---- rows that several CTAs share: the last to arrive joins them.  Of many parts
+  // groups of kGroup are joined first, each by its own last: what one SM reads in a
+  // row costs more than a second arrival does.
   if (open[0] < 0 && open[1] < 0) return;
   __syncthreads();
   if (tid < 2) {
     const int slot = tid == 0 ? open[0] : open[1];
+    sh.last[tid] = 0;
     if (slot >= 0) {
-      const Stretch p = sh.part[slot];
+      const Stretch& p = sh.part[slot];
       const int from = taker(total, ctas, static_cast<U>(p.u0)), to = taker(total, ctas, static_cast<U>(p.u0) + p.n - 1);
-      // releases what this CTA wrote (the barrier above orders its threads' writes
-      // before), and acquires what the others did
-      const int others = arrive(a.counters + from);
-      sh.arrived[tid] = others == to - from ? 1 : 0;
+      const bool grouped = to - from + 1 > 2 * kGroup;
+      const int lead = grouped ? from + (cta - from) / kGroup * kGroup : from;
       sh.from[tid] = from;
       sh.to[tid] = to;
-      if (others == to - from) a.counters[from] = 0;  // for the next launch
+      sh.last[tid] = grouped ? last_of(a.counters + gridDim.x + 2 * lead + (lead == from), min(kGroup, to + 1 - lead))
+                             : last_of(a.counters + from, to - from + 1);
     }
   }
   __syncthreads();
-#pragma unroll
+#pragma unroll 1
   for (int place = 0; place < 2; ++place) {
-    if (open[place] < 0 || !sh.arrived[place]) continue;
-    const Stretch p = sh.part[open[place]];
+    if (!sh.last[place]) continue;
+    const Stretch& p = sh.part[place == 0 ? open[0] : open[1]];
     const int from = sh.from[place], to = sh.to[place];
     int kv, first, heads;
     heads_of(a, p.vh, &kv, &first, &heads);
-    // the row's part in CTA i: its last share (place 1) where it begins, else its first
-    auto place_of = [&](int i) { return int64_t(i) * 2 + (i == from ? 1 : 0); };
-    auto ml_of = [&](int x, int h) {
-      return __ldcg(reinterpret_cast<const float2*>(a.part_ml + place_of(x) * (C::kHeads * 2) + 2 * h));
-    };
-    auto o_of = [&](int x, int h, int d) {
-      return __ldcg(reinterpret_cast<const float4*>(a.part_o + place_of(x) * (C::kHeads * D) + h * D + d));
-    };
-    constexpr int kBatch = 16, kDeep = 16;
-    if (to - from < kBatch) {  // a few parts: everything in one round of loads
-      for (int i = tid; i < heads * kQuads; i += kDecodeWarps * 32) {
-        const int h = i / kQuads, d = 4 * (i % kQuads);
-        float2 ml[kBatch];
-        float4 v[kBatch];
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-          const bool have = from + x <= to;
-          ml[x] = have ? ml_of(from + x, h) : make_float2(-INFINITY, 0.f);
-          v[x] = have ? o_of(from + x, h, d) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+    bool grouped = to - from + 1 > 2 * kGroup;
+    int base = grouped ? from + (cta - from) / kGroup * kGroup : from, step = 1;
+    int count = grouped ? min(kGroup, to + 1 - base) : to - from + 1;
+    for (;;) {
+      // the parts of CTAs base, base + step ... : a CTA's last share (place 1) where
+      // the row begins, else its first
+      for (int i0 = 0; i0 < heads * kQuads; i0 += kDecodeWarps * 32) {
+        const int i = i0 + tid, h = i / kQuads, d = 4 * (i % kQuads);
+        const bool mine = i < heads * kQuads;
+        constexpr int kBatch = D == 128 ? 16 : 8;
         Joined sum;
-        sum.add(ml, v);
-        store_joined(a, D, p.b, first + h, d, sum);
-      }
-      continue;
-    }
-    // many: the parts' weights first, a warp for each head, then sums that wait
-    // for nothing but their loads
-    float* weight = reinterpret_cast<float*>(smem);  // [part][head]
-    const int parts = to - from + 1;
-    for (int h = warp; h < heads; h += kDecodeWarps) {
-      constexpr int kMost = 10;  // of the parts of up to 320 CTAs a lane has this many
-      float2 ml[kMost];
-      float top = -INFINITY, sum = 0.f;
+        for (int x0 = 0; mine && x0 < count; x0 += kBatch) {
+          float2 ml[kBatch];
+          float4 v[kBatch];
 #pragma unroll
-      for (int i = 0; i < kMost; ++i) {
-        const int x = lane + 32 * i;
-        ml[i] = x < parts ? ml_of(from + x, h) : make_float2(-INFINITY, 0.f);
-      }
-#pragma unroll
-      for (int i = 0; i < kMost; ++i) top = fmaxf(top, ml[i].x);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-      const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-      for (int i = 0; i < kMost; ++i) {
-        const int x = lane + 32 * i;
-        const float w = fast_exp2(ml[i].x - ref);
-        sum += w * ml[i].y;
-        if (x < parts) weight[x * C::kHeads + h] = w;
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-      if (lane == 0) {
-        a.lse[int64_t(first + h) * a.B + p.b] = lse_of(ref, sum);
-        sh.l[0][h] = sum == 0.f ? 0.f : 1.f / sum;
-      }
-    }
-    __syncthreads();
-    for (int i = tid; i < heads * kQuads; i += kDecodeWarps * 32) {
-      const int h = i / kQuads, d = 4 * (i % kQuads);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x0 = 0; x0 < parts; x0 += kDeep) {
-        float4 v[kDeep];
-#pragma unroll
-        for (int x = 0; x < kDeep; ++x) v[x] = o_of(min(from + x0 + x, to), h, d);
-#pragma unroll
-        for (int x = 0; x < kDeep; ++x) {
-          const float w = weight[(x0 + x) * C::kHeads + h];
-          if (x0 + x < parts) o.x += w * v[x].x, o.y += w * v[x].y, o.z += w * v[x].z, o.w += w * v[x].w;
+          for (int x = 0; x < kBatch; ++x) {
+            ml[x] = make_float2(-INFINITY, 0.f);
+            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x0 + x < count) {
+              const int c = base + (x0 + x) * step;
+              const int64_t at = int64_t(c) * 2 + (c == from ? 1 : 0);
+              ml[x] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h));
+              v[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * (C::kHeads * D) + h * D + d));
+            }
+          }
+          sum.add(ml, v);
+        }
+        // a group's sum takes the place of its first part, which this warp alone reads
+        static_assert(32 % kQuads == 0, "a head's values lie in one warp");
+        __syncwarp();
+        if (mine && grouped) {
+          const int64_t at = int64_t(base) * 2 + (base == from ? 1 : 0);
+          __stcg(reinterpret_cast<float4*>(a.part_o + at * (C::kHeads * D) + h * D + d), sum.o);
+          if (d == 0)
+            __stcg(reinterpret_cast<float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h), make_float2(sum.top, sum.sum));
+        } else if (mine) {
+          store_joined(a, D, p.b, first + h, d, sum);
         }
       }
-      const float by = sh.l[0][h];
-      store_out4(a, D, p.b, first + h, d, make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
+      if (!grouped) break;
+      grouped = false;
+      base = from;
+      step = kGroup;
+      count = (to - from) / kGroup + 1;
+      __syncthreads();
+      if (tid == 0) sh.last[place] = last_of(a.counters + from, count);
+      __syncthreads();
+      if (!sh.last[place]) break;
     }
-    __syncthreads();  // the weights are read
   }
 }
 
 template <int D, int NT, typename U>
 cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
   using C = DecodeCfg<D, NT>;
-  if (sms * C::kCtasPerSm > 320) return cudaErrorNotSupported;  // what one warp joins
   static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<D, NT>) + 1024) <= 233472, "shared memory of an SM");
   cudaError_t e = set_smem_limit_once<decode_kernel<D, NT, U>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -733,7 +728,8 @@ DecodeSpace decode_space(int D, int part_heads, int sms) {
   const int ctas = sms * (D == 64 ? DecodeCfg<64, 1>::kCtasPerSm : DecodeCfg<128, 1>::kCtasPerSm);
   static_assert(DecodeCfg<64, 1>::kCtasPerSm == DecodeCfg<64, 2>::kCtasPerSm &&
                     DecodeCfg<128, 1>::kCtasPerSm == DecodeCfg<128, 2>::kCtasPerSm, "one grid for each D");
-  return {ctas, int64_t(ctas) * 2 * heads * 2, int64_t(ctas) * 2 * heads * D};
+  // a counter for the row that begins in a CTA's share, two for groups that a CTA leads
+  return {3 * ctas, int64_t(ctas) * 2 * heads * 2, int64_t(ctas) * 2 * heads * D};
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t stream) {

@@ -24,12 +24,16 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int kTableThreads = 1024, kTableCluster = 8;
 
+// Sums that stop at 2^32 - 1: what goes beyond is refused whatever its size.
 struct Need {
-  int64_t rows, give, take;
-  __device__ __forceinline__ void add(const Need& o) { rows += o.rows, give += o.give, take += o.take; }
+  uint32_t rows, give, take;
+  static __device__ __forceinline__ uint32_t sum(uint32_t a, uint32_t b) { return a + b < a ? UINT_MAX : a + b; }
+  __device__ __forceinline__ void add(const Need& o) {
+    rows = sum(rows, o.rows), give = sum(give, o.give), take = sum(take, o.take);
+  }
 };
 
-__device__ __forceinline__ int clamp_int(int64_t v) { return v > INT_MAX ? INT_MAX : static_cast<int>(v); }
+__device__ __forceinline__ int clamp_int(uint32_t v) { return static_cast<int>(min(v, uint32_t(INT_MAX))); }
 
 __device__ __forceinline__ Need warp_scan(Need v) {
   const int lane = threadIdx.x & 31;
@@ -41,21 +45,23 @@ __device__ __forceinline__ Need warp_scan(Need v) {
   return v;
 }
 
-// Inclusive sums over the block's threads; *total receives the block's sum.
+// Sums over the threads of the block before this one; *total receives the block's.
 __device__ Need block_scan(Need v, Need (&warp_sum)[32], Need* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  v = warp_scan(v);
-  if (lane == 31) warp_sum[warp] = v;
+  const Need upto = warp_scan(v);
+  if (lane == 31) warp_sum[warp] = upto;
   __syncthreads();
   const Need sums = warp_scan(warp_sum[lane]);
-  auto from = [&](int w) -> Need {
-    return {__shfl_sync(~0u, sums.rows, w), __shfl_sync(~0u, sums.give, w), __shfl_sync(~0u, sums.take, w)};
+  auto from = [&](const Need& n, int w) -> Need {
+    return {__shfl_sync(~0u, n.rows, w), __shfl_sync(~0u, n.give, w), __shfl_sync(~0u, n.take, w)};
   };
-  *total = from(31);
-  const Need before = from(max(warp - 1, 0));
-  if (warp > 0) v.add(before);
+  *total = from(sums, 31);
+  Need before = from(sums, max(warp - 1, 0));
+  if (warp == 0) before = {0, 0, 0};
+  Need lower{__shfl_up_sync(~0u, upto.rows, 1), __shfl_up_sync(~0u, upto.give, 1), __shfl_up_sync(~0u, upto.take, 1)};
+  if (lane > 0) before.add(lower);
   __syncthreads();  // the sums are read
-  return v;
+  return before;
 }
 
 // The last b in [lo, n) with at[b] <= p; at[lo] <= p.
@@ -107,19 +113,20 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
       Need n{0, 0, 0};
       if (b < a.B) {
         const int64_t len = a.lens[b], delta = a.delta[b];
-        n.rows = max(delta, int64_t(0));
-        if (sound_length(len, len + delta) && (fits || delta <= 0 || row_at[b] + n.rows <= a.rows)) {
+        n.rows = static_cast<uint32_t>(max(delta, int64_t(0)));
+        if (sound_length(len, len + delta) && (fits || delta <= 0 || row_at[b] + delta <= a.rows)) {
           const int held = pages(static_cast<int>(len)), need = pages(static_cast<int>(len + delta));
           n.give = max(held - need, 0);
           n.take = max(need - held, 0);
         }
       }
       Need total;
-      const Need to = block_scan(n, warp_sum, &total);
+      Need before = block_scan(n, warp_sum, &total);
+      before.add(carry);
       if (b < a.B) {
-        row_at[b] = clamp_int(carry.rows + to.rows - n.rows);
-        give_at[b] = clamp_int(carry.give + to.give - n.give);
-        take_at[b] = clamp_int(carry.take + to.take - n.take);
+        row_at[b] = clamp_int(before.rows);
+        give_at[b] = clamp_int(before.give);
+        take_at[b] = clamp_int(before.take);
       }
       carry.add(total);
     }
@@ -132,7 +139,8 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
   __syncthreads();
 
   if (sound && carry.give > 0) {
-    for (int p = all; p < carry.give; p += stride) {
+    const int give = static_cast<int>(carry.give);
+    for (int p = all; p < give; p += stride) {
       const int b = owner_of(give_at, 0, a.B, p);
       a.free_list[n_free + p] = a.table[b * a.table_row + pages(a.lens[b] + a.delta[b]) + (p - give_at[b])];
     }
@@ -164,14 +172,14 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
     a.table[b * a.table_row + pages(a.lens[b]) + (p - take_at[b])] = a.free_list[top - 1 - p];
   }
 
-  // A warp has runs of 32 * kRun rows, a lane every 32nd of them: it searches for
-  // the first one's request and walks on from there.
-  constexpr int kRun = 4;
+  // A warp has stretches of 32 * run rows, a lane every 32nd of them: it searches
+  // for the first one's request and walks on from there.
   const int lane = tid & 31;
+  const int run = static_cast<int>(min(int64_t(8), (a.rows + stride - 1) / stride));
   const int new_rows = row_at[a.B];
-  for (int64_t base = int64_t(all - lane) * kRun; base < a.rows; base += int64_t(stride) * kRun) {
+  for (int64_t base = int64_t(all - lane) * run; base < a.rows; base += int64_t(stride) * run) {
     int b = -1;
-    for (int k = 0; k < kRun; ++k) {
+    for (int k = 0; k < run; ++k) {
       const int64_t r = base + 32 * k + lane;
       if (r >= a.rows) break;
       int slot = -1, position = 0;

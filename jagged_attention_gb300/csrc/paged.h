@@ -89,7 +89,7 @@ struct DecodeArgs {
   uint16_t* out;
   float* lse;
   int* status;
-  int* counters;             // arrivals at a split row, one for each CTA; zero between launches
+  int* counters;             // arrivals at the parts of split rows; zero between launches
   float *part_ml, *part_o;   // what CTAs leave of split rows
 };
 // Workspace of a decode launch: counters (int), part_ml and part_o (float).

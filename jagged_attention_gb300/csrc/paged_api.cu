@@ -2,6 +2,7 @@
 // in include/jfa.h: argument checks, handles and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <new>
@@ -69,14 +70,20 @@ int check_device(const jfa_pager* p) {
   return dev == p->device ? JFA_OK : JFA_ERR_INVALID_ARG;
 }
 
+// SMs of the current device, JFA_ERR_UNSUPPORTED where this library does not run on it.
 int sm_count(int* sms) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];  // 0: not asked yet; what a device is does not change
   int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+  if (cudaGetDevice(&dev) != cudaSuccess) return JFA_ERR_CUDA;
+  if (dev < kDevices && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return JFA_OK;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return JFA_ERR_CUDA;
-  return major == 10 && minor == 3 ? JFA_OK : JFA_ERR_UNSUPPORTED;  // built for sm_103a only
+  if (major != 10 || minor != 3) return JFA_ERR_UNSUPPORTED;  // built for sm_103a only
+  if (dev < kDevices) known[dev].store(*sms, std::memory_order_relaxed);
+  return JFA_OK;
 }
 
 // One tensor of `heads` heads a row, `row` elements from row to row.

@@ -571,3 +571,14 @@ def test_decode_tables_wide_enough_for_64_bit_counts():
     out, lse = _check_decode(big, q, kp, vp, wide, lens)
     narrow = jfa.paged_decode(pager, q, kp, vp, table, lens, 0.125)
     assert torch.equal(out, narrow[0]) and torch.equal(lse, narrow[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,hk", [(16, 1), (12, 1), (3, 1), (40, 2)])
+def test_decode_rows_of_many_parts(D, hq, hk):
+    """Rows that all CTAs share: their parts are joined in groups first."""
+    case = _decode_case([20000, 0, 7000, 9001], hq, hk, D, 24, False, 31)
+    out, lse = _check_decode(*case)
+    for _ in range(5):
+        o, l = jfa.paged_decode(*case, 1 / math.sqrt(D))
+        assert torch.equal(o, out) and torch.equal(l, lse)
