@@ -110,7 +110,7 @@ struct DecodeShared {
 };
 
 __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
-  const int len = __ldg(a.lens + b);
+  const int len = a.lens[b];
   return len < 0 || len > a.max_pages * a.div.d ? 0 : len;
 }
 
@@ -225,6 +225,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   __shared__ DecodeShared<D, NT> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int vheads = a.Hkv * a.parts;
+  wait_for_launch_before();
 
   // ---- tiles of all requests, and where this CTA's warps begin
   const int slab = (a.B + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
@@ -351,7 +352,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       if (pos >= c.len) return {kNoRow, 0};
       const int i = a.div.quot(pos);
       // a table entry of INT_MIN is as bad as any negative one
-      return {max(__ldg(a.table + c.b * a.table_row + i), kNoRow + 1),
+      return {max(a.table[c.b * a.table_row + i], kNoRow + 1),
               (pos - i * a.div.d) * a.row + (c.vh / a.parts) * a.head};
     };
     const uint64_t policy = read_once_policy();
@@ -413,8 +414,8 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
           const uint16_t* q = a.q + now.b * a.q_row + int64_t(first + 8 * n + (have ? g : 0)) * D + 2 * j;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            qf[ks][n][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks)) : 0u;
-            qf[ks][n][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * ks + 8)) : 0u;
+            qf[ks][n][0] = have ? *reinterpret_cast<const uint32_t*>(q + 16 * ks) : 0u;
+            qf[ks][n][1] = have ? *reinterpret_cast<const uint32_t*>(q + 16 * ks + 8) : 0u;
           }
           m[n][0] = m[n][1] = -INFINITY;
           l[n][0] = l[n][1] = 0.f;
@@ -565,7 +566,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   // ---- requests without rows
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (length_of(a, b) > 0) continue;
-    if (tid == 0 && __ldg(a.lens + b) != 0) atomicOr(a.status, kPagerBadLength);
+    if (tid == 0 && a.lens[b] != 0) atomicOr(a.status, kPagerBadLength);
     for (int i = tid; i < a.H * (D / 4); i += kDecodeWarps * 32)
       store_out4(a, D, b, i / (D / 4), 4 * (i % (D / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
     for (int h = tid; h < a.H; h += kDecodeWarps * 32) a.lse[int64_t(h) * a.B + b] = -INFINITY;
@@ -589,20 +590,24 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     const int prev_b = __shfl_sync(~0u, p.b, prev), prev_vh = __shfl_sync(~0u, p.vh, prev);
     heads_at = __ballot_sync(~0u, have && (!below || prev_b != p.b || prev_vh != p.vh));
   }
+  // as many rows at once as have threads for their heads
+  int row_threads = 32;
+  while (row_threads < a.part_heads * kQuads && row_threads < kDecodeWarps * 32) row_threads *= 2;
+  const int row_tid = tid & (row_threads - 1), my_turn = tid / row_threads, turns = kDecodeWarps * 32 / row_threads;
   int open[2] = {-1, -1};  // slots of parts that go on in other CTAs, by their place in global memory
-  while (heads_at) {
+  for (int turn = 0; heads_at; ++turn) {
     const int s = __ffs(heads_at) - 1;
     heads_at &= heads_at - 1;
     const int end = heads_at ? __ffs(heads_at) - 1 : 2 * kDecodeWarps;
     const uint32_t parts = held & ((1u << end) - (1u << s));
-    const Stretch p = sh.part[s];
+    const Stretch& p = sh.part[s];
     const bool whole = p.t0 == 0 && sh.part[31 - __clz(parts)].t1 == p.n;
     const int place = p.t0 == 0 ? 1 : 0;
+    if (!whole) (place == 0 ? open[0] : open[1]) = s;
+    if ((turn & (turns - 1)) != my_turn) continue;
     int kv, first, heads;
     heads_of(a, p.vh, &kv, &first, &heads);
-    float* o_out = a.part_o + (int64_t(cta) * 2 + place) * (C::kHeads * D);
-    float* ml_out = a.part_ml + (int64_t(cta) * 2 + place) * (C::kHeads * 2);
-    for (int i = tid; i < heads * kQuads; i += kDecodeWarps * 32) {
+    for (int i = row_tid; i < heads * kQuads; i += row_threads) {
       const int h = i / kQuads, d = 4 * (i % kQuads);
       Joined sum;
       for (uint32_t left = parts; left;) {
@@ -625,11 +630,12 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       if (whole) {
         store_joined(a, D, p.b, first + h, d, sum);
       } else {
-        __stcg(reinterpret_cast<float4*>(o_out + h * D + d), sum.o);
-        if (d == 0) __stcg(reinterpret_cast<float2*>(ml_out + 2 * h), make_float2(sum.top, sum.sum));
+        const int64_t at = int64_t(cta) * 2 + place;
+        __stcg(reinterpret_cast<float4*>(a.part_o + at * (C::kHeads * D) + h * D + d), sum.o);
+        if (d == 0)
+          __stcg(reinterpret_cast<float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h), make_float2(sum.top, sum.sum));
       }
     }
-    if (!whole) (place == 0 ? open[0] : open[1]) = s;
   }
 
   // ---- rows that several CTAs share: the last to arrive joins them.  Of many parts
@@ -665,37 +671,48 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     for (;;) {
       // the parts of CTAs base, base + step ... : a CTA's last share (place 1) where
       // the row begins, else its first
-      for (int i0 = 0; i0 < heads * kQuads; i0 += kDecodeWarps * 32) {
-        const int i = i0 + tid, h = i / kQuads, d = 4 * (i % kQuads);
-        const bool mine = i < heads * kQuads;
-        constexpr int kBatch = D == 128 ? 16 : 8;
-        Joined sum;
-        for (int x0 = 0; mine && x0 < count; x0 += kBatch) {
-          float2 ml[kBatch];
-          float4 v[kBatch];
+      // 4 values of kItems heads to a thread, their loads under way together
+      constexpr int kThreads = kDecodeWarps * 32;
+      constexpr int kItems = C::kHeads * kQuads > kThreads ? C::kHeads * kQuads / kThreads : 1;
+      constexpr int kBatch = D == 128 ? 16 / kItems : 8;
+      static_assert(kItems * kThreads >= C::kHeads * kQuads, "one round for all heads");
+      Joined sum[kItems];
+      for (int x0 = 0; x0 < count; x0 += kBatch) {
+        float2 ml[kItems][kBatch];
+        float4 v[kItems][kBatch];
+#pragma unroll
+        for (int z = 0; z < kItems; ++z) {
+          const int i = tid + z * kThreads, h = i / kQuads, d = 4 * (i % kQuads);
 #pragma unroll
           for (int x = 0; x < kBatch; ++x) {
-            ml[x] = make_float2(-INFINITY, 0.f);
-            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x0 + x < count) {
+            ml[z][x] = make_float2(-INFINITY, 0.f);
+            v[z][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x0 + x < count && h < heads) {
               const int c = base + (x0 + x) * step;
               const int64_t at = int64_t(c) * 2 + (c == from ? 1 : 0);
-              ml[x] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h));
-              v[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * (C::kHeads * D) + h * D + d));
+              ml[z][x] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h));
+              v[z][x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * (C::kHeads * D) + h * D + d));
             }
           }
-          sum.add(ml, v);
         }
-        // a group's sum takes the place of its first part, which this warp alone reads
-        static_assert(32 % kQuads == 0, "a head's values lie in one warp");
-        __syncwarp();
-        if (mine && grouped) {
+#pragma unroll
+        for (int z = 0; z < kItems; ++z) sum[z].add(ml[z], v[z]);
+      }
+      // a group's sum takes the place of its first part, which a head's warp alone reads
+      static_assert(32 % kQuads == 0, "a head's values lie in one warp");
+      __syncwarp();
+#pragma unroll
+      for (int z = 0; z < kItems; ++z) {
+        const int i = tid + z * kThreads, h = i / kQuads, d = 4 * (i % kQuads);
+        if (h >= heads) continue;
+        if (grouped) {
           const int64_t at = int64_t(base) * 2 + (base == from ? 1 : 0);
-          __stcg(reinterpret_cast<float4*>(a.part_o + at * (C::kHeads * D) + h * D + d), sum.o);
+          __stcg(reinterpret_cast<float4*>(a.part_o + at * (C::kHeads * D) + h * D + d), sum[z].o);
           if (d == 0)
-            __stcg(reinterpret_cast<float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h), make_float2(sum.top, sum.sum));
-        } else if (mine) {
-          store_joined(a, D, p.b, first + h, d, sum);
+            __stcg(reinterpret_cast<float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h),
+                   make_float2(sum[z].top, sum[z].sum));
+        } else {
+          store_joined(a, D, p.b, first + h, d, sum[z]);
         }
       }
       if (!grouped) break;
@@ -717,8 +734,7 @@ cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
   static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<D, NT>) + 1024) <= 233472, "shared memory of an SM");
   cudaError_t e = set_smem_limit_once<decode_kernel<D, NT, U>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, NT, U><<<sms * C::kCtasPerSm, kDecodeWarps * 32, C::kSmemBytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(decode_kernel<D, NT, U>, dim3(sms * C::kCtasPerSm), kDecodeWarps * 32, C::kSmemBytes, 1, stream, a);
 }
 
 }  // namespace

@@ -86,6 +86,7 @@ __device__ __forceinline__ void all_arrive(bool cluster) {
 // No pointer is __restrict__ and nothing goes through the read-only cache: lens
 // and n_free may be overwritten in place.
 __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_constant__ TablesArgs a) {
+  wait_for_launch_before();
   extern __shared__ int sm[];
   int* row_at = sm;              // [B + 1] new rows before each request
   int* give_at = sm + a.B + 1;   // [B] pages given back before it; later: whether it is served
@@ -221,18 +222,8 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // one CTA while its threads have no more than one run of rows each
   const bool many = a.rows > 4 * kTableThreads;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(many ? kTableCluster : 1);
-  cfg.blockDim = dim3(kTableThreads);
-  cfg.dynamicSmemBytes = (3 * a.B + 1) * 4;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = many ? kTableCluster : 1;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tables_kernel, a);
+  const int ctas = many ? kTableCluster : 1;
+  return launch_overlapped(tables_kernel, dim3(ctas), kTableThreads, (3 * a.B + 1) * 4, ctas, stream, a);
 }
 
 }  // namespace jfa

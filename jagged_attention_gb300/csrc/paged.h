@@ -6,6 +6,36 @@
 
 namespace jfa {
 
+// These kernels are launched before the one ahead of them in the stream has quite
+// ended: they are set up while its last writes settle, and wait for those before
+// they touch memory.  Back to back that takes 0.2 to 0.5 us off a call of 3 to 8 us
+// (letting go of the next kernel earlier, while this one still runs, gains nothing
+// more).  As a kernel so begins before its inputs are final, nothing is read
+// through the non-coherent cache.
+#ifdef __CUDACC__
+__device__ __forceinline__ void wait_for_launch_before() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename K, typename... A>
+cudaError_t launch_overlapped(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                              const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 // Bits of a pager's status word (JFA_PAGER_* in jfa.h).
 enum PagerBits : int { kPagerNoPages = 1, kPagerBadLength = 2, kPagerBadPage = 4 };
 

@@ -108,6 +108,7 @@ __device__ __forceinline__ void walk_heads(const RowJob& job, int D, int64_t in,
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kRowThreads)
 rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
+  wait_for_launch_before();
   const int units = a.D / 16;  // threads of a row: 4 or 8
   const int u = threadIdx.x % units;
   const int64_t row = int64_t(blockIdx.x) * (kRowThreads / units) + threadIdx.x / units;
@@ -175,11 +176,8 @@ cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   const int split = static_cast<int>(std::min<int64_t>(a.heads, std::max<int64_t>(1, fill / blocks)));
   const int per = (a.heads + split - 1) / split;
   const dim3 grid(static_cast<unsigned>(blocks), (a.heads + per - 1) / per);
-  if (a.turns.interleaved)
-    rows_kernel<true><<<grid, kRowThreads, 0, stream>>>(a, per);
-  else
-    rows_kernel<false><<<grid, kRowThreads, 0, stream>>>(a, per);
-  return cudaGetLastError();
+  return launch_overlapped(a.turns.interleaved ? rows_kernel<true> : rows_kernel<false>, grid, kRowThreads, 0, 1, stream,
+                           a, per);
 }
 
 }  // namespace jfa
