@@ -168,41 +168,59 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
   }
   __syncthreads();
 
-  for (int p = all; p < taken; p += stride) {
-    const int b = owner_of(take_at, 0, a.B, p);
-    a.table[b * a.table_row + pages(a.lens[b]) + (p - take_at[b])] = a.free_list[top - 1 - p];
-  }
+  // The p-th page taken, loaded now and stored behind the rows.
+  const int page_taken = all < taken ? a.free_list[top - 1 - all] : 0;
 
   // A warp has stretches of 32 * run rows, a lane every 32nd of them: it searches
-  // for the first one's request and walks on from there.
+  // for the first one's request and walks on from there, the pages of kTogether
+  // rows under way at once.
+  constexpr int kTogether = 4;
   const int lane = tid & 31;
   const int run = static_cast<int>(min(int64_t(8), (a.rows + stride - 1) / stride));
   const int new_rows = row_at[a.B];
   for (int64_t base = int64_t(all - lane) * run; base < a.rows; base += int64_t(stride) * run) {
     int b = -1;
-    for (int k = 0; k < run; ++k) {
-      const int64_t r = base + 32 * k + lane;
-      if (r >= a.rows) break;
-      int slot = -1, position = 0;
-      if (r < new_rows) {
-        const int row = static_cast<int>(r);
-        if (b < 0) b = owner_of(row_at, 0, a.B, row);
-        while (row_at[b + 1] <= row) ++b;
-        const int len = a.lens[b];
-        position = static_cast<int>(int64_t(len) + (row - row_at[b]));
-        if (give_at[b]) {
-          const int i = a.div.quot(position), held = pages(len);
-          // entries of new pages are on their way into the table: take them where they come from
-          const int page = i < held ? a.table[b * a.table_row + i] : a.free_list[top - 1 - take_at[b] - (i - held)];
-          if (page >= 0 && page < a.num_pages)
-            slot = page * a.div.d + (position - i * a.div.d);
+    for (int k0 = 0; k0 < run; k0 += kTogether) {
+      int position[kTogether], page[kTogether];
+      bool served[kTogether];
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k) {
+        const int64_t r = base + 32 * (k0 + k) + lane;
+        position[k] = page[k] = 0;
+        served[k] = false;
+        if (k0 + k < run && r < new_rows) {
+          const int row = static_cast<int>(r);
+          if (b < 0) b = owner_of(row_at, 0, a.B, row);
+          while (row_at[b + 1] <= row) ++b;
+          const int len = a.lens[b];
+          position[k] = static_cast<int>(int64_t(len) + (row - row_at[b]));
+          served[k] = give_at[b];
+          if (served[k]) {
+            const int i = a.div.quot(position[k]), held = pages(len);
+            // entries of new pages are on their way into the table: take them where they come from
+            page[k] = i < held ? a.table[b * a.table_row + i] : a.free_list[top - 1 - take_at[b] - (i - held)];
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k) {
+        const int64_t r = base + 32 * (k0 + k) + lane;
+        if (k0 + k >= run || r >= a.rows) continue;
+        int slot = -1;
+        if (served[k]) {
+          if (page[k] >= 0 && page[k] < a.num_pages)
+            slot = page[k] * a.div.d + (position[k] - a.div.quot(position[k]) * a.div.d);
           else
             atomicOr(&problem, kPagerBadPage);
         }
+        a.slots[r] = slot;
+        a.positions[r] = position[k];
       }
-      a.slots[r] = slot;
-      a.positions[r] = position;
     }
+  }
+  for (int p = all; p < taken; p += stride) {
+    const int b = owner_of(take_at, 0, a.B, p);
+    a.table[b * a.table_row + pages(a.lens[b]) + (p - take_at[b])] = p == all ? page_taken : a.free_list[top - 1 - p];
   }
   for (int b = all; b <= a.B; b += stride) a.row_offsets[b] = row_at[b];
   all_arrive(ranks > 1);  // lens and n_free are read

@@ -128,8 +128,8 @@ jfa::RowJob dense_job(const void* in, int64_t in_row, void* out, int64_t out_row
   return {in, out, in_row, out_row, 0, D, heads, f32, false, rotate};
 }
 
-// rows of one launch: the grid's first dimension holds 2^31 - 1 blocks of at least 32 rows
-constexpr int64_t kMaxRows = int64_t(1) << 35;
+// rows of one launch: the grid's first dimension holds 2^31 - 1 blocks of at least 8 rows
+constexpr int64_t kMaxRows = int64_t(1) << 33;
 
 }  // namespace
 

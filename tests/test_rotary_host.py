@@ -101,7 +101,7 @@ def test_rotate_refuses_before_any_launch():
     r = jfa.Rotary(*jfa.rotary_pairs(64), D=128)
     good = [r.handle, 4096, 1, 0, 10, 0, 4096, 256, 8192, 256, 2, 4096, 256, 8192, 256, 2, None]
     for at, value, code in [(0, None, INVALID), (1, None, INVALID), (1, 4098, ALIGNMENT), (2, -1, INVALID),
-                            (3, -1, INVALID), (4, -1, INVALID), (4, 1 << 35, INVALID), (5, 8, INVALID),
+                            (3, -1, INVALID), (4, -1, INVALID), (4, 1 << 33, INVALID), (5, 8, INVALID),
                             (6, None, INVALID), (6, 4104, ALIGNMENT), (7, 255, INVALID), (7, 260, ALIGNMENT),
                             (8, None, INVALID), (8, 8200, ALIGNMENT), (9, 128, INVALID), (10, 0, INVALID),
                             (10, 2**31 - 1, INVALID), (11, None, INVALID), (15, 0, INVALID), (15, -1, INVALID),
