@@ -591,9 +591,17 @@ def _positions(positions: torch.Tensor, rotary: Rotary, rows: int, device: int) 
     return positions.data_ptr(), stride[0], stride[1]
 
 
-def _raw_stream(stream, device: int) -> int:
-    """As _stream, for calls whose tensors are on `device`."""
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+def _on(stream):
+    """The context in which `stream` (a torch stream or a cudaStream_t) is current:
+    outputs made there belong to it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _raw_stream(device: int) -> int:
+    """The current stream's handle, as torch.cuda.current_stream(device).cuda_stream, in a tenth of the time."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out=None, k_out=None,
@@ -603,6 +611,9 @@ def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out
     q and k) to the gradients of the unrotated ones.  Rows may lie apart (slices
     of a fused projection).  q_out / k_out may be q / k.  Returns q_out, or
     (q_out, k_out) with k."""
+    if stream is not None:
+        with _on(stream):
+            return rotate(rotary, positions, q, k, inverse=inverse, q_out=q_out, k_out=k_out)
     dev = q.get_device()
     if dev < 0:
         raise TypeError(f"q must be a CUDA tensor, got {q.device}")
@@ -635,7 +646,7 @@ def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out
             k_out = torch.empty(shape, dtype=k.dtype, device=k.device)
         args += (*_rows("k", k, shape, k.dtype, dev), *_rows("k_out", k_out, shape, k.dtype, dev), hk)
     rc = (_lib or lib()).jfa_rotate(rotary.handle, *_positions(positions, rotary, rows, dev), rows, flags, *args,
-                                    _raw_stream(stream, dev))
+                                    _raw_stream(dev))
     if rc:
         _check(rc, "jfa_rotate")
     return q_out if k is None else (q_out, k_out)
@@ -643,11 +654,12 @@ def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out
 
 class Pager:
     """A jfa_pager_t: the geometry of a paged key/value cache, with its status word
-    and workspace in ``block``, on the current device.  One pager for each stream
-    that decodes at the same time: its launches must be stream-ordered."""
+    and workspace in ``block``, which is cleared on the current stream of the
+    current device.  One pager for each stream that decodes at the same time: its
+    launches must be stream-ordered.  Keep it as long as graphs that captured them."""
 
     def __init__(self, *, max_seqs: int, max_pages: int, num_pages: int, page_size: int, H: int, Hkv: int,
-                 D: int, stream=None):
+                 D: int):
         self._h = None
         self.max_seqs, self.max_pages, self.num_pages, self.page_size = max_seqs, max_pages, num_pages, page_size
         self.H, self.Hkv, self.D = H, Hkv, D
@@ -657,7 +669,7 @@ class Pager:
         self.block = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
         h = _vp()
         _check(lib().jfa_pager_create(max_seqs, max_pages, num_pages, page_size, H, Hkv, D, self.block.data_ptr(), n,
-                                      _stream(stream), ctypes.byref(h)), "jfa_pager_create")
+                                      _stream(None), ctypes.byref(h)), "jfa_pager_create")
         self._h = h
 
     @property
@@ -704,6 +716,10 @@ def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: i
     table [B, max_pages] and free_list [num_pages] are updated in place; lens and
     n_free too where lens_out and n_free_out are given as them.  Returns
     (lens_out, n_free_out, slots, positions, row_offsets)."""
+    if stream is not None:
+        with _on(stream):
+            return paged_tables(pager, lens, delta, table, free_list, n_free, rows=rows, lens_out=lens_out,
+                                n_free_out=n_free_out, slots=slots, positions=positions, row_offsets=row_offsets)
     dev = pager.index
     B = lens.shape[0]
     if lens_out is None:
@@ -722,7 +738,7 @@ def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: i
         _ints("free_list", free_list, pager.num_pages, dev), _ints("n_free", n_free, 1, dev),
         _ints("n_free_out", n_free_out, 1, dev), rows, _ints("slots", slots, rows, dev),
         _ints("positions", positions, rows, dev), _ints("row_offsets", row_offsets, B + 1, dev),
-        _raw_stream(stream, dev))
+        _raw_stream(dev))
     if rc:
         _check(rc, "jfa_paged_tables")
     return lens_out, n_free_out, slots, positions, row_offsets
@@ -733,6 +749,10 @@ def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary 
     """New rows k, v [rows, Hkv, D] into the pages at their slots through
     jfa_paged_append; with ``rotary``, k and q [rows, H, D] rotated by
     ``positions`` on the way.  Returns q_out (which may be q), None without q."""
+    if stream is not None:
+        with _on(stream):
+            return paged_append(pager, k, v, slots, k_pages, v_pages, rotary=rotary, positions=positions, q=q,
+                                q_out=q_out)
     dev = pager.index
     rows = k.shape[0]
     shape = (rows, pager.Hkv, pager.D)
@@ -753,7 +773,7 @@ def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary 
     rc = (_lib or lib()).jfa_paged_append(
         pager.handle, rows, *_rows("k", k, shape, torch.bfloat16, dev), *_rows("v", v, shape, torch.bfloat16, dev),
         _ints("slots", slots, rows, dev), ctypes.byref(_pages(pager, k_pages, v_pages)), rot, *pos, *q_args,
-        _raw_stream(stream, dev))
+        _raw_stream(dev))
     if rc:
         _check(rc, "jfa_paged_append")
     return q_out
@@ -763,6 +783,9 @@ def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *
                  stream=None):
     """O (bf16 [B, H, D]) and LSE (fp32 [H, B]) of one new token per request over
     its cached rows, through jfa_paged_decode.  q [B, H, D]; rows may lie apart."""
+    if stream is not None:
+        with _on(stream):
+            return paged_decode(pager, q, k_pages, v_pages, table, lens, scale, out=out, lse=lse)
     dev, H, D = pager.index, pager.H, pager.D
     B = q.shape[0]
     shape = (B, H, D)
@@ -778,7 +801,7 @@ def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *
         raise ValueError("out must be contiguous")
     rc = (_lib or lib()).jfa_paged_decode(
         pager.handle, B, *q_at, ctypes.byref(_pages(pager, k_pages, v_pages)), *_table(table, pager, B, dev),
-        _ints("lens", lens, B, dev), float(scale), out_at, lse.data_ptr(), _raw_stream(stream, dev))
+        _ints("lens", lens, B, dev), float(scale), out_at, lse.data_ptr(), _raw_stream(dev))
     if rc:
         _check(rc, "jfa_paged_decode")
     return out, lse

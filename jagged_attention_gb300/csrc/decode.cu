@@ -184,7 +184,7 @@ __device__ __forceinline__ void heads_of(const DecodeArgs& a, int vh, int* kv, i
   *kv = vh / a.parts;
   const int g0 = (vh - *kv * a.parts) * a.part_heads;
   *first = *kv * group + g0;
-  *count = min(a.part_heads, group - g0);
+  *count = min(a.part_heads, group - g0);  // >= 1: part_heads is the least that does
 }
 
 // 4 values of out, normalised already.

@@ -273,7 +273,8 @@ EDGES = [0, 1, 2, 7, 8, 9, 15, 16, 17, 31, 33, 63, 64, 65, 100, 127, 128, 129, 2
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("hq,hk", [(1, 1), (4, 4), (8, 4), (6, 2), (4, 1), (15, 3), (6, 1), (14, 2), (8, 1), (9, 1),
-                                   (24, 2), (16, 1), (17, 1), (40, 1)])
+                                   (24, 2), (16, 1), (17, 1), (40, 1), (48, 1), (66, 2), (128, 1), (130, 1),
+                                   (300, 1)])
 def test_decode_head_groups(D, hq, hk):
     _check_decode(*_decode_case(EDGES, hq, hk, D, 16, False, hq * 100 + hk))
 
@@ -574,7 +575,7 @@ def test_decode_tables_wide_enough_for_64_bit_counts():
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("hq,hk", [(16, 1), (12, 1), (3, 1), (40, 2)])
+@pytest.mark.parametrize("hq,hk", [(16, 1), (12, 1), (3, 1), (40, 2), (100, 1)])
 def test_decode_rows_of_many_parts(D, hq, hk):
     """Rows that all CTAs share: their parts are joined in groups first."""
     case = _decode_case([20000, 0, 7000, 9001], hq, hk, D, 24, False, 31)
@@ -582,3 +583,25 @@ def test_decode_rows_of_many_parts(D, hq, hk):
     for _ in range(5):
         o, l = jfa.paged_decode(*case, 1 / math.sqrt(D))
         assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_a_stream_of_its_own():
+    """stream= runs a call there, and makes its outputs there."""
+    pager, q, kp, vp, table, lens = _decode_case([700, 33], 4, 2, 64, 16, False, 14)
+    want = jfa.paged_decode(pager, q, kp, vp, table, lens, 0.125)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = jfa.paged_decode(pager, q, kp, vp, table, lens, 0.125, stream=stream)
+        rot = jfa.Rotary(*jfa.rotary_pairs(64), D=64)
+        turned = jfa.rotate(rot, lens, q, stream=stream)
+        jfa.paged_append(pager, kp[0, :2], vp[0, :2], _ints([-1, -1]), kp, vp, stream=stream)
+        side.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(turned, jfa.rotate(rot, lens, q))
+        assert pager.status(stream=stream) == 0
+    table2, free = _ints(np.zeros((2, pager.max_pages))), _ints(np.arange(pager.num_pages))
+    got = jfa.paged_tables(pager, _ints([0, 0]), _ints([3, 5]), table2, free, _ints([pager.num_pages]), rows=8,
+                           stream=side.cuda_stream)
+    side.synchronize()
+    assert got[0].tolist() == [3, 5]
