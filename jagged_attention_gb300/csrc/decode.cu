@@ -15,11 +15,12 @@
 // wastes least of the tile and leaves the cache rows in the layout that
 // ldmatrix reads; tcgen05 would want 64 or 128 query rows per product.
 //
-// Split: a tile is 16 cached rows for one key/value head (and, where G > 16, one
+// Split: a tile is 32 cached rows for one key/value head (and, where G > 16, one
 // part of its query heads).  All tiles of all requests in the order (request,
 // head, row) are dealt in equal contiguous shares to the CTAs, and a CTA's share
-// to its warps; a warp streams its tiles through its own ring of cp.async
-// stages, over the ends of rows and requests, and meets no barrier on the way.
+// to its warps; a warp streams its tiles by cp.async through a stage for K and one
+// for V -- the next K is on its way while V is used, and the other way round --
+// over the ends of rows and requests, and meets no barrier on the way.
 // What is left at the ends of the warps' shares is joined in shared memory, what
 // is left at the ends of the CTAs' shares in global memory by the CTA that
 // arrives last, in the order of the shares: the same arguments give the same
@@ -34,31 +35,30 @@
 namespace jfa {
 namespace {
 
-constexpr int kTile = 16;        // cached rows of a tile
+constexpr int kTile = 32;        // cached rows of a tile
 constexpr int kDecodeWarps = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D, int NT>  // NT: tiles of 8 query heads
 struct DecodeCfg {
   static constexpr int kHeads = 8 * NT;
-  static constexpr int kStageBytes = 2 * kTile * D * 2;  // K and V
-  static constexpr int kStages = 2;
-  static constexpr int kOutBytes = kHeads * D * 4;  // a stretch's O
-  static_assert(kOutBytes <= kStageBytes, "a used stage holds a stretch's O");
-  static constexpr int kWarpBytes = kStages * kStageBytes + kOutBytes;
+  static constexpr int kStageBytes = kTile * D * 2;  // a tile's K, or its V
+  static constexpr int kOutBytes = kHeads * D * 4;   // a stretch's O
+  static_assert(kOutBytes <= kStageBytes, "the stage of V holds a stretch's O when it is read");
+  static constexpr int kWarpBytes = 2 * kStageBytes + kOutBytes;  // K, V, park
   static constexpr int kSmemBytes = kDecodeWarps * kWarpBytes;
   static constexpr int kCtasPerSm = D == 64 ? 2 : 1;
 };
 
 // Units of work: a (request, virtual head) of n tiles counts n units for them,
 // and kRowUnits behind them for its beginning and end.
-constexpr int kRowUnits = 2;
+constexpr int kRowUnits = 1;
 
 // Parts of a row that one CTA joins at a time, where a row has more than twice as many.
 constexpr int kGroup = 8;
 
 // Few rows of at most this many tiles get a CTA each.
-constexpr int kApartTiles = 3 * kDecodeWarps;
+constexpr int kApartTiles = 12;
 
 // Where a warp stands: tile t of n of the rows of (request b, virtual head vh),
 // unit u of all.
@@ -105,7 +105,6 @@ struct DecodeShared {
   int scan_rows[kDecodeWarps], scan_most[kDecodeWarps];
   int64_t start_unit[kDecodeWarps];  // where the request begins in which a warp's share does
   int start_b[kDecodeWarps], start_len[kDecodeWarps];
-  uint32_t live[kDecodeWarps][DecodeCfg<D, NT>::kStages];  // rows of a stage that count
   int from[2], to[2], last[2];
 };
 
@@ -221,7 +220,7 @@ template <int D, int NT, typename U>
 __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeCfg<D, NT>::kCtasPerSm)
 decode_kernel(const __grid_constant__ DecodeArgs a) {
   using C = DecodeCfg<D, NT>;
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(256) unsigned char smem[];
   __shared__ DecodeShared<D, NT> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int vheads = a.Hkv * a.parts;
@@ -268,11 +267,11 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   // few and short rows: a CTA for each, so that nothing is left to be joined between CTAs
   const bool apart = most <= kApartTiles && int64_t(all_rows) * vheads <= gridDim.x;
   if (apart) {
-    units = U(rows) * (kApartTiles);
-    units_to = U(rows_to) * (kApartTiles);
-    total = U(all_rows) * (kApartTiles);
+    units = U(rows) * U(most);
+    units_to = U(rows_to) * U(most);
+    total = U(all_rows) * U(most);
   }
-  auto units_of = [&](int n) -> U { return n == 0 ? 0 : apart ? kApartTiles : n + kRowUnits; };
+  auto units_of = [&](int n) -> U { return n == 0 ? 0 : apart ? most : n + kRowUnits; };
   total *= vheads;
   const int ctas = apart ? max(1, all_rows * vheads) : ctas_of(total, static_cast<int>(gridDim.x));
   const int cta = blockIdx.x;
@@ -304,9 +303,10 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
 
   const U lo = cta_lo + share(cta_n, kDecodeWarps, warp), hi = cta_lo + share(cta_n, kDecodeWarps, warp + 1);
 
-  unsigned char* ring = smem + warp * C::kWarpBytes;
-  const uint32_t ring_addr = smem_u32(ring);
-  float* park = reinterpret_cast<float*>(ring + C::kStages * C::kStageBytes);
+  unsigned char* mine_smem = smem + warp * C::kWarpBytes;
+  const uint32_t k_stage = smem_u32(mine_smem), v_stage = k_stage + C::kStageBytes;
+  float* v_floats = reinterpret_cast<float*>(mine_smem + C::kStageBytes);
+  float* park = reinterpret_cast<float*>(mine_smem + 2 * C::kStageBytes);
 
   if (lo < hi) {
     // on to the next (b, vh); beyond the share only the unit counts
@@ -322,11 +322,6 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         c.n = tiles_of(c.len);
       } while (c.n == 0 && c.b + 1 < a.B);
     };
-    auto advance = [&](Cursor<U>& c) {
-      ++c.t;
-      ++c.u;
-      if (c.t >= c.n) next_row(c);
-    };
     Cursor<U> at;  // of the tile whose rows are looked up next
     at.u = lo;
     at.b = sh.start_b[warp];
@@ -339,69 +334,85 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     }
     if (at.t >= at.n) next_row(at);
     Cursor<U> now = at;  // of the tile computed next
-    // Row lane % 16 of a tile: its page, kNoRow behind the last row, and its offset
-    // in the page.  The page is not looked at before the rows are asked for, so
-    // that the load from the table is under way meanwhile.
-    struct Row {
-      int page;
-      int64_t in_page;
+    const int32_t* table = nullptr;  // at's
+    int64_t head_off = 0;
+    auto row_of_at = [&] {
+      table = a.table + at.b * a.table_row;
+      head_off = (at.vh / a.parts) * a.head;
     };
+    row_of_at();
+
+    // What is known of the next tile's row `lane`: its page (kNoRow behind the last
+    // row) and its offset from the page's first value.  The page is not looked at
+    // before the row is asked for, so that the load from the table is under way
+    // meanwhile.
     constexpr int kNoRow = INT_MIN;
-    auto look_up = [&](const Cursor<U>& c) -> Row {
-      const int pos = c.t * kTile + (lane & 15);
-      if (pos >= c.len) return {kNoRow, 0};
+    int page = kNoRow;
+    int64_t in_page = 0;
+    auto look_up = [&] {
+      const int pos = at.t * kTile + lane;
+      page = kNoRow;
+      if (pos >= at.len) return;
       const int i = a.div.quot(pos);
-      // a table entry of INT_MIN is as bad as any negative one
-      return {max(a.table[c.b * a.table_row + i], kNoRow + 1),
-              (pos - i * a.div.d) * a.row + (c.vh / a.parts) * a.head};
+      page = max(table[i], kNoRow + 1);  // an entry of INT_MIN is as bad as any negative one
+      in_page = static_cast<uint32_t>(pos - i * a.div.d) * static_cast<uint64_t>(static_cast<uint32_t>(a.row)) + head_off;
     };
+    // Its place in the cache in bytes, and which rows of the tile count.
+    int64_t off = 0;
+    uint32_t live = 0;
+    auto locate = [&] {
+      const bool in_cache = page >= 0 && page < a.num_pages;
+      if (!in_cache && page != kNoRow) atomicOr(a.status, kPagerBadPage);
+      off = in_cache ? (page * a.page + in_page) * 2 : 0;
+      live = __ballot_sync(~0u, in_cache);
+    };
+    // Rows of a tile into a stage: 8 lanes copy 128 bytes of a row, chunk c of row r
+    // to place c ^ (r % 8) of its 8.
     const uint64_t policy = read_once_policy();
-    auto issue = [&](int stage, const Row& row) {
-      constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of an instruction
-      const bool in_cache = row.page >= 0 && row.page < a.num_pages;
-      if (!in_cache && row.page != kNoRow) atomicOr(a.status, kPagerBadPage);
-      const int64_t off = in_cache ? row.page * a.page + row.in_page : -1;
-      const uint32_t live = __ballot_sync(~0u, in_cache);
-      if (lane == 0) sh.live[warp][stage] = live;
-      const uint32_t k_at = ring_addr + stage * C::kStageBytes, v_at = k_at + kTile * D * 2;
-      const int c = lane % kLanes;
+    const uint32_t to_even = (lane >> 3) * (D * 2) + (((lane & 7) ^ (lane >> 3)) << 4), to_odd = to_even ^ 64;
+    auto copy = [&](uint32_t stage, const uint16_t* from) {
+      const char* base = reinterpret_cast<const char*>(from) + (lane & 7) * 16;
 #pragma unroll
-      for (int i = 0; i < kTile / kRows; ++i) {
-        const int r = i * kRows + lane / kLanes;
-        const int64_t o = __shfl_sync(~0u, off, r);
-        const bool take = o >= 0;
-        const int64_t src = (take ? o : 0) + c * 8;
-        const uint32_t dst = r * (D * 2) + ((c ^ (r & 7)) << 4);
-        cp_async16(k_at + dst, a.k + src, take, policy);
-        cp_async16(v_at + dst, a.v + src, take, policy);
+      for (int i = 0; i < kTile / 4; ++i) {  // rows 4 i + lane / 8
+        const char* src = base + __shfl_sync(~0u, off, 4 * i + (lane >> 3));
+        const bool take = (live >> (4 * i + (lane >> 3))) & 1;
+        const uint32_t dst = stage + 4 * i * (D * 2) + (i & 1 ? to_odd : to_even);
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) cp_async16(dst + 128 * half, src + 128 * half, take, policy);
       }
     };
 
-    Row ahead[C::kStages];
-    uint32_t have = 0;
-#pragma unroll
-    for (int s = 0; s < C::kStages; ++s) {
-      if (at.u < hi) {
-        have |= 1u << s;
-        ahead[s] = look_up(at);
-        advance(at);
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < C::kStages; ++s) {
-      if (have >> s & 1) issue(s, ahead[s]);
-      cp_async_commit();
-    }
     bool more = at.u < hi;
-    Row next{kNoRow, 0};  // of the tile issued next
-    if (more) next = look_up(at);
+    if (more) look_up();
+    locate();
+    copy(k_stage, a.k);
+    cp_async_commit();
+    copy(v_stage, a.v);
+    cp_async_commit();
+    uint32_t live_now = live;
+    // looks up the tile behind the one asked for, if the share has one
+    auto find_next = [&] {
+      ++at.t;
+      ++at.u;
+      if (at.t >= at.n) {
+        next_row(at);
+        row_of_at();
+      }
+      more = at.u < hi;
+      if (more) look_up();
+    };
+    if (more) find_next();
 
     float o_acc[D / 16][NT][4], m[NT][2], l[NT][2];
     uint32_t qf[D / 16][NT][2];
     const int g = lane >> 2, j = lane & 3;
-    int stage = 0, t0 = 0, first = 0, heads = 0, kv = 0;
+    int t0 = 0, first = 0, heads = 0, kv = 0;
     bool fresh = true;
     const float scale_log2 = a.scale * kLog2e;
+    // ldmatrix: lane's row of the first 16 and its chunk, exclusive or included; what
+    // is added for later chunks touches other bits
+    const uint32_t k_lane = k_stage + (lane & 15) * (D * 2) + (((lane >> 4) ^ (lane & 7)) << 4);
+    const uint32_t v_lane = v_stage + ((lane & 7) + (lane >> 4) * 8) * (D * 2) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
 
     while (now.u < hi) {
       if (fresh) {
@@ -425,38 +436,46 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
             for (int e = 0; e < 4; ++e) o_acc[i][n][e] = 0.f;
         }
       }
-      cp_async_wait<C::kStages - 1>();
+      cp_async_wait<1>();  // K is here, V may be on its way
       __syncwarp();
-      const uint32_t k_at = ring_addr + stage * C::kStageBytes, v_at = k_at + kTile * D * 2;
-      const uint32_t live = sh.live[warp][stage];
 
-      // scores of 16 rows (g, g + 8) and heads (2 j, 2 j + 1)
-      float s[NT][4];
+      // scores of rows 16 x + (g, g + 8) and heads (2 j, 2 j + 1)
+      float s[2][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-      {
-        const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
+          for (int e = 0; e < 4; ++e) s[x][n][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
           uint32_t kf[4];
-          ldmatrix4(kf, k_at + r * (D * 2) + (((2 * ks + c) ^ (r & 7)) << 4));
+          ldmatrix4(kf, (k_lane ^ (ks << 5)) + x * 16 * (D * 2));
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_16816(s[n], kf, qf[ks][n][0], qf[ks][n][1]);
+          for (int n = 0; n < NT; ++n) mma_16816(s[x][n], kf, qf[ks][n][0], qf[ks][n][1]);
         }
       }
-      const bool live0 = (live >> g) & 1, live1 = (live >> (g + 8)) & 1;
-      uint32_t hi_f[NT][2], lo_f[NT][2];
+      __syncwarp();  // K is read
+      if (more) {
+        locate();
+        copy(k_stage, a.k);
+      }
+      cp_async_commit();
+
+      uint32_t hi_f[2][NT][2], lo_f[2][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float top[2];
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          s[n][e] = live0 ? s[n][e] * scale_log2 : -INFINITY;
-          s[n][2 + e] = live1 ? s[n][2 + e] * scale_log2 : -INFINITY;
-          top[e] = fmaxf(s[n][e], s[n][2 + e]);
-        }
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool counts = (live_now >> (16 * x + g + (e >> 1) * 8)) & 1;
+            s[x][n][e] = counts ? s[x][n][e] * scale_log2 : -INFINITY;
+            top[e & 1] = fmaxf(top[e & 1], s[x][n][e]);
+          }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
           top[0] = fmaxf(top[0], __shfl_xor_sync(~0u, top[0], x));
@@ -474,46 +493,49 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
             for (int i = 0; i < D / 16; ++i) o_acc[i][n][e] *= keep, o_acc[i][n][2 + e] *= keep;
           }
         }
-        float p[4];
+        const float ref[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
-          p[e] = fast_exp2(s[n][e] - ref);
-        }
-        l[n][0] += p[0] + p[2];
-        l[n][1] += p[1] + p[3];
+        for (int x = 0; x < 2; ++x) {
+          float p[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t w = pack_bf16x2(p[2 * e], p[2 * e + 1]);
-          const float r0 = p[2 * e] - __uint_as_float(w << 16);
-          const float r1 = p[2 * e + 1] - __uint_as_float(w & 0xffff0000u);
-          hi_f[n][e] = transpose8x8(w);
-          lo_f[n][e] = transpose8x8(pack_bf16x2(r0, r1));
-        }
-      }
-      {
-        const int r = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
+          for (int e = 0; e < 4; ++e) {
+            p[e] = fast_exp2(s[x][n][e] - ref[e & 1]);
+            l[n][e & 1] += p[e];
+          }
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t vf[4];
-          ldmatrix4_trans(vf, v_at + r * (D * 2) + (((2 * i + c) ^ (r & 7)) << 4));
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_16816(o_acc[i][n], vf, hi_f[n][0], hi_f[n][1]);
-            mma_16816(o_acc[i][n], vf, lo_f[n][0], lo_f[n][1]);
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t w = pack_bf16x2(p[2 * e], p[2 * e + 1]);
+            const float r0 = p[2 * e] - __uint_as_float(w << 16);
+            const float r1 = p[2 * e + 1] - __uint_as_float(w & 0xffff0000u);
+            hi_f[x][n][e] = transpose8x8(w);
+            lo_f[x][n][e] = transpose8x8(pack_bf16x2(r0, r1));
           }
         }
       }
-      __syncwarp();  // the stage is read
+      cp_async_wait<1>();  // V is here, the next K may be on its way
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t vf[4];
+          ldmatrix4_trans(vf, (v_lane ^ (i << 5)) + x * 16 * (D * 2));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_16816(o_acc[i][n], vf, hi_f[x][n][0], hi_f[x][n][1]);
+            mma_16816(o_acc[i][n], vf, lo_f[x][n][0], lo_f[x][n][1]);
+          }
+        }
+      }
+      __syncwarp();  // V is read
 
       const bool row_ends = now.t + 1 == now.n;
       const bool share_ends = (row_ends ? now.u + (units_of(now.n) - U(now.t)) : now.u + 1) >= hi;
       if (row_ends || share_ends) {
         const bool whole = row_ends && t0 == 0;
-        // a part of a row: the share's first waits in the park, its last in the ring
+        // a part of a row: the share's first waits in the park, its last where V was
         const bool parked = !whole && !share_ends;
-        if (share_ends) cp_async_wait<0>();
-        float* to = parked ? park : reinterpret_cast<float*>(ring + (share_ends ? 0 : stage * C::kStageBytes));
+        float* to = parked ? park : v_floats;
         const int slot = 2 * warp + (parked ? 0 : 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -549,16 +571,16 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         }
         fresh = true;
       }
-      advance(now);
+      ++now.t;
+      ++now.u;
+      if (now.t >= now.n) next_row(now);
 
       if (more) {
-        issue(stage, next);
-        advance(at);
-        more = at.u < hi;
-        if (more) next = look_up(at);
+        copy(v_stage, a.v);
+        live_now = live;
+        find_next();
       }
       cp_async_commit();
-      stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
     cp_async_wait<0>();
   }
@@ -576,8 +598,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
 
   // ---- parts of a row within this CTA's share
   auto part_o = [&](int slot) -> const float* {
-    const unsigned char* base = smem + (slot >> 1) * C::kWarpBytes;
-    return reinterpret_cast<const float*>(slot & 1 ? base : base + C::kStages * C::kStageBytes);
+    return reinterpret_cast<const float*>(smem + (slot >> 1) * C::kWarpBytes + (slot & 1 ? 1 : 2) * C::kStageBytes);
   };
   constexpr int kQuads = D / 4;
   uint32_t held, heads_at;  // slots that hold a part, and those where a row's first part is

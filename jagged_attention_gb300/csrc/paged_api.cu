@@ -344,6 +344,7 @@ int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, con
   if (!table || !lens || !out || !lse || table_row < pager->max_pages) return JFA_ERR_INVALID_ARG;
   if (int rc = check_rows(q, q_row, pager->H, pager->D, false)) return rc;
   if (int rc = check_pages(pages)) return rc;
+  if (pager->div.d > 1 && pages->row > UINT32_MAX) return JFA_ERR_UNSUPPORTED;
   if (!aligned(out, 16) || !aligned(lse, 16) || !aligned(table, 4) || !aligned(lens, 4)) return JFA_ERR_ALIGNMENT;
   if (int rc = check_device(pager)) return rc;
   jfa::DecodeArgs a{};
