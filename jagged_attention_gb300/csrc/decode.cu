@@ -15,8 +15,11 @@
 // wastes least of the tile and leaves the cache rows in the layout that
 // ldmatrix reads; tcgen05 would want 64 or 128 query rows per product.
 //
-// Split: a tile is 32 cached rows for one key/value head (and, where G > 16, one
-// part of its query heads).  All tiles of all requests in the order (request,
+// More than 16 query heads to a key/value head are taken in 2, 4 or 8 parts by as
+// many warps side by side, which walk over the same tiles at the same pace: memory
+// is read once, for the others the cache is in L2.
+//
+// Split: a tile is 32 cached rows for one key/value head.  All tiles of all requests in the order (request,
 // head, row) are dealt in equal contiguous shares to the CTAs, and a CTA's share
 // to its warps; a warp streams its tiles by cp.async through a stage for K and one
 // for V -- the next K is on its way while V is used, and the other way round --
@@ -37,6 +40,7 @@ namespace {
 
 constexpr int kTile = 32;        // cached rows of a tile
 constexpr int kDecodeWarps = 8;
+constexpr int kMostHeads = 16;   // query heads that a warp holds
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D, int NT>  // NT: tiles of 8 query heads
@@ -50,9 +54,9 @@ struct DecodeCfg {
   static constexpr int kCtasPerSm = D == 64 ? 2 : 1;
 };
 
-// Units of work: a (request, virtual head) of n tiles counts n units for them,
-// and kRowUnits behind them for its beginning and end.
-constexpr int kRowUnits = 1;
+// Units of work: the n tiles of a (request, key/value head) count n units, and
+// kRowUnits behind them stand for its beginning and end.
+constexpr int kRowUnits = 2;
 
 // Parts of a row that one CTA joins at a time, where a row has more than twice as many.
 constexpr int kGroup = 8;
@@ -60,18 +64,19 @@ constexpr int kGroup = 8;
 // Few rows of at most this many tiles get a CTA each.
 constexpr int kApartTiles = 12;
 
-// Where a warp stands: tile t of n of the rows of (request b, virtual head vh),
-// unit u of all.
+// Where a warp stands: tile t of n of (request b, key/value head and pass vh), unit
+// u of all.
 template <typename U>
 struct Cursor {
   U u;
   int b, vh, t, n, len;
 };
 
-// A stretch that does not hold all tiles of its (b, vh): tiles [t0, t1) of n.
+// A stretch that does not hold all tiles of its (request b, part x of the query
+// heads): tiles [t0, t1) of n.
 struct Stretch {
   int64_t u0;  // unit of its tile 0
-  int b, vh, t0, t1, n;  // n 0: none
+  int b, x, t0, t1, n;  // n 0: none
 };
 
 // Sum of stretches of one row for 4 values of a head, taken up in batches.
@@ -171,19 +176,12 @@ __device__ __forceinline__ int taker(U total, int n, U u) {
   const U big = more * (per + 1);
   return static_cast<int>(u < big ? u / (per + 1) : more + (u - big) / per);
 }
-// CTAs that take part: fewer than `most` where each warp would not have a unit.
-template <typename U>
-__device__ __forceinline__ int ctas_of(U total, int most) {
-  return total >= U(most) * kDecodeWarps ? most : max(1, static_cast<int>(total) / kDecodeWarps);
-}
-
-// Query heads [first, first + count) of virtual head vh, and its key/value head.
-__device__ __forceinline__ void heads_of(const DecodeArgs& a, int vh, int* kv, int* first, int* count) {
-  const int group = a.H / a.Hkv;
-  *kv = vh / a.parts;
-  const int g0 = (vh - *kv * a.parts) * a.part_heads;
-  *first = *kv * group + g0;
-  *count = min(a.part_heads, group - g0);  // >= 1: part_heads is the least that does
+// Query heads [first, first + count) of part x of all, a.parts to a key/value head.
+__device__ __forceinline__ void heads_of(const DecodeArgs& a, int x, int* first, int* count) {
+  const int group = a.H / a.Hkv, kv = x / a.parts;
+  const int g0 = (x - kv * a.parts) * a.part_heads;
+  *first = kv * group + g0;
+  *count = max(0, min(a.part_heads, group - g0));  // 0: more parts than heads fill
 }
 
 // 4 values of out, normalised already.
@@ -216,15 +214,21 @@ __device__ __forceinline__ void store_joined(const DecodeArgs& a, int D, int b, 
 
 // U: unsigned type that counts all units.  32 bits hold them unless the table is
 // wide enough for more; divisions and scans in 64 bits cost a short call 1 us.
-template <int D, int NT, typename U>
+// kSide: parts of query heads side by side.
+template <int D, int NT, bool kSide, typename U>
 __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeCfg<D, NT>::kCtasPerSm)
 decode_kernel(const __grid_constant__ DecodeArgs a) {
   using C = DecodeCfg<D, NT>;
   extern __shared__ __align__(256) unsigned char smem[];
   __shared__ DecodeShared<D, NT> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int vheads = a.Hkv * a.parts;
   wait_for_launch_before();
+  // A CTA's share is dealt to `subs` sets of `together` warps, one for each part of
+  // the query heads; a line is a warp's place with those of its part in a row.
+  const int vheads = a.Hkv * a.passes, together = kSide ? a.together : 1;
+  const int sub_bits = kSide ? __ffs(kDecodeWarps / together) - 1 : __builtin_ctz(kDecodeWarps), subs = 1 << sub_bits;
+  const int part = kSide ? warp & (together - 1) : 0, sub = kSide ? warp / together : warp;
+  const int line = (part << sub_bits) + sub;
 
   // ---- tiles of all requests, and where this CTA's warps begin
   const int slab = (a.B + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
@@ -265,7 +269,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     most = max(most, sh.scan_most[w]);
   }
   // few and short rows: a CTA for each, so that nothing is left to be joined between CTAs
-  const bool apart = most <= kApartTiles && int64_t(all_rows) * vheads <= gridDim.x;
+  const bool apart = most <= kApartTiles / together && int64_t(all_rows) * vheads <= gridDim.x;
   if (apart) {
     units = U(rows) * U(most);
     units_to = U(rows_to) * U(most);
@@ -273,19 +277,25 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   }
   auto units_of = [&](int n) -> U { return n == 0 ? 0 : apart ? most : n + kRowUnits; };
   total *= vheads;
-  const int ctas = apart ? max(1, all_rows * vheads) : ctas_of(total, static_cast<int>(gridDim.x));
+  // fewer CTAs than there are where each warp would not have a unit
+  int ctas = static_cast<int>(gridDim.x);
+  if (apart)
+    ctas = max(1, all_rows * vheads);
+  else if (total < U(ctas) << sub_bits)
+    ctas = max(1, static_cast<int>(total >> sub_bits));
   const int cta = blockIdx.x;
   U cta_lo = 0, cta_n = 0;
   if (cta < ctas) {
     cta_lo = share(total, ctas, cta);
     cta_n = share(total, ctas, cta + 1) - cta_lo;
   }
+  auto sub_from = [&](int i) -> U { return cta_lo + (cta_n >> sub_bits) * U(i) + min(U(i), cta_n & U(subs - 1)); };
   {
     // the thread in whose requests a warp's share begins says where
     const U first = (units_to - units) * vheads, end = units_to * vheads;
     if (first < cta_lo + cta_n && end > cta_lo) {
-      for (int w = 0; w < kDecodeWarps; ++w) {
-        const U u = cta_lo + share(cta_n, kDecodeWarps, w);
+      for (int w = 0; w < subs; ++w) {
+        const U u = sub_from(w);
         if (u < first || u >= end) continue;
         U at = first;
         int b = b_lo, len = length_of(a, b);
@@ -301,9 +311,9 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   }
   __syncthreads();
 
-  const U lo = cta_lo + share(cta_n, kDecodeWarps, warp), hi = cta_lo + share(cta_n, kDecodeWarps, warp + 1);
+  const U lo = sub_from(sub), hi = sub_from(sub + 1);
 
-  unsigned char* mine_smem = smem + warp * C::kWarpBytes;
+  unsigned char* mine_smem = smem + line * C::kWarpBytes;
   const uint32_t k_stage = smem_u32(mine_smem), v_stage = k_stage + C::kStageBytes;
   float* v_floats = reinterpret_cast<float*>(mine_smem + C::kStageBytes);
   float* park = reinterpret_cast<float*>(mine_smem + 2 * C::kStageBytes);
@@ -324,11 +334,11 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     };
     Cursor<U> at;  // of the tile whose rows are looked up next
     at.u = lo;
-    at.b = sh.start_b[warp];
-    at.len = sh.start_len[warp];
+    at.b = sh.start_b[sub];
+    at.len = sh.start_len[sub];
     at.n = tiles_of(at.len);
     {
-      const U r = lo - static_cast<U>(sh.start_unit[warp]), per = units_of(at.n);
+      const U r = lo - static_cast<U>(sh.start_unit[sub]), per = units_of(at.n);
       at.vh = static_cast<int>(r / per);
       at.t = static_cast<int>(r - U(at.vh) * per);
     }
@@ -338,7 +348,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     int64_t head_off = 0;
     auto row_of_at = [&] {
       table = a.table + at.b * a.table_row;
-      head_off = (at.vh / a.parts) * a.head;
+      head_off = (at.vh / a.passes) * a.head;
     };
     row_of_at();
 
@@ -406,7 +416,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     float o_acc[D / 16][NT][4], m[NT][2], l[NT][2];
     uint32_t qf[D / 16][NT][2];
     const int g = lane >> 2, j = lane & 3;
-    int t0 = 0, first = 0, heads = 0, kv = 0;
+    int t0 = 0, first = 0, heads = 0;
     bool fresh = true;
     const float scale_log2 = a.scale * kLog2e;
     // ldmatrix: lane's row of the first 16 and its chunk, exclusive or included; what
@@ -418,7 +428,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       if (fresh) {
         fresh = false;
         t0 = now.t;
-        heads_of(a, now.vh, &kv, &first, &heads);
+        heads_of(a, now.vh * together + part, &first, &heads);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const bool have = 8 * n + g < heads;
@@ -536,7 +546,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         // a part of a row: the share's first waits in the park, its last where V was
         const bool parked = !whole && !share_ends;
         float* to = parked ? park : v_floats;
-        const int slot = 2 * warp + (parked ? 0 : 1);
+        const int slot = 2 * line + (parked ? 0 : 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -567,7 +577,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
           }
           __syncwarp();
         } else if (lane == 0) {
-          sh.part[slot] = {int64_t(now.u - U(now.t)), now.b, now.vh, t0, now.t + 1, now.n};
+          sh.part[slot] = {int64_t(now.u - U(now.t)), now.b, now.vh * together + part, t0, now.t + 1, now.n};
         }
         fresh = true;
       }
@@ -608,14 +618,16 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     held = __ballot_sync(~0u, have);
     const uint32_t below = held & ((1u << lane) - 1);
     const int prev = below ? 31 - __clz(below) : lane;
-    const int prev_b = __shfl_sync(~0u, p.b, prev), prev_vh = __shfl_sync(~0u, p.vh, prev);
-    heads_at = __ballot_sync(~0u, have && (!below || prev_b != p.b || prev_vh != p.vh));
+    const int prev_b = __shfl_sync(~0u, p.b, prev), prev_x = __shfl_sync(~0u, p.x, prev);
+    heads_at = __ballot_sync(~0u, have && (!below || prev_b != p.b || prev_x != p.x));
   }
   // as many rows at once as have threads for their heads
   int row_threads = 32;
   while (row_threads < a.part_heads * kQuads && row_threads < kDecodeWarps * 32) row_threads *= 2;
   const int row_tid = tid & (row_threads - 1), my_turn = tid / row_threads, turns = kDecodeWarps * 32 / row_threads;
-  int open[2] = {-1, -1};  // slots of parts that go on in other CTAs, by their place in global memory
+  // a slot of what goes on in other CTAs, by its place in global memory: 0 begun
+  // before, 1 begun here (all parts of its query heads alike)
+  int open[2] = {-1, -1};
   for (int turn = 0; heads_at; ++turn) {
     const int s = __ffs(heads_at) - 1;
     heads_at &= heads_at - 1;
@@ -626,8 +638,8 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     const int place = p.t0 == 0 ? 1 : 0;
     if (!whole) (place == 0 ? open[0] : open[1]) = s;
     if ((turn & (turns - 1)) != my_turn) continue;
-    int kv, first, heads;
-    heads_of(a, p.vh, &kv, &first, &heads);
+    int first, heads;
+    heads_of(a, p.x, &first, &heads);
     for (int i = row_tid; i < heads * kQuads; i += row_threads) {
       const int h = i / kQuads, d = 4 * (i % kQuads);
       Joined sum;
@@ -651,7 +663,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       if (whole) {
         store_joined(a, D, p.b, first + h, d, sum);
       } else {
-        const int64_t at = int64_t(cta) * 2 + place;
+        const int64_t at = (int64_t(cta) * 2 + place) * together + (p.x & (together - 1));
         __stcg(reinterpret_cast<float4*>(a.part_o + at * (C::kHeads * D) + h * D + d), sum.o);
         if (d == 0)
           __stcg(reinterpret_cast<float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h), make_float2(sum.top, sum.sum));
@@ -684,56 +696,57 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     if (!sh.last[place]) continue;
     const Stretch& p = sh.part[place == 0 ? open[0] : open[1]];
     const int from = sh.from[place], to = sh.to[place];
-    int kv, first, heads;
-    heads_of(a, p.vh, &kv, &first, &heads);
     bool grouped = to - from + 1 > 2 * kGroup;
     int base = grouped ? from + (cta - from) / kGroup * kGroup : from, step = 1;
     int count = grouped ? min(kGroup, to + 1 - base) : to - from + 1;
     for (;;) {
-      // the parts of CTAs base, base + step ... : a CTA's last share (place 1) where
-      // the row begins, else its first
-      // 4 values of kItems heads to a thread, their loads under way together
-      constexpr int kThreads = kDecodeWarps * 32;
-      constexpr int kItems = C::kHeads * kQuads > kThreads ? C::kHeads * kQuads / kThreads : 1;
-      constexpr int kBatch = D == 128 ? 16 / kItems : 8;
-      static_assert(kItems * kThreads >= C::kHeads * kQuads, "one round for all heads");
-      Joined sum[kItems];
-      for (int x0 = 0; x0 < count; x0 += kBatch) {
-        float2 ml[kItems][kBatch];
-        float4 v[kItems][kBatch];
+      for (int y = 0; y < together; ++y) {
+        int first, heads;
+        heads_of(a, (p.x & -together) + y, &first, &heads);
+        // what CTA c has: in its last place where the row begins, else in its first
+        auto place_of = [&](int c) { return (int64_t(c) * 2 + (c == from ? 1 : 0)) * together + y; };
+        // 4 values of kItems heads to a thread, their loads under way together
+        constexpr int kThreads = kDecodeWarps * 32;
+        constexpr int kItems = C::kHeads * kQuads > kThreads ? C::kHeads * kQuads / kThreads : 1;
+        constexpr int kBatch = D == 128 ? 16 / kItems : 8;
+        static_assert(kItems * kThreads >= C::kHeads * kQuads, "one round for all heads");
+        Joined sum[kItems];
+        for (int x0 = 0; x0 < count; x0 += kBatch) {
+          float2 ml[kItems][kBatch];
+          float4 v[kItems][kBatch];
+#pragma unroll
+          for (int z = 0; z < kItems; ++z) {
+            const int i = tid + z * kThreads, h = i / kQuads, d = 4 * (i % kQuads);
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+              ml[z][x] = make_float2(-INFINITY, 0.f);
+              v[z][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (x0 + x < count && h < heads) {
+                const int64_t at = place_of(base + (x0 + x) * step);
+                ml[z][x] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h));
+                v[z][x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * (C::kHeads * D) + h * D + d));
+              }
+            }
+          }
+#pragma unroll
+          for (int z = 0; z < kItems; ++z) sum[z].add(ml[z], v[z]);
+        }
+        // a group's sum takes the place of its first part, which a head's warp alone reads
+        static_assert(32 % kQuads == 0, "a head's values lie in one warp");
+        __syncwarp();
 #pragma unroll
         for (int z = 0; z < kItems; ++z) {
           const int i = tid + z * kThreads, h = i / kQuads, d = 4 * (i % kQuads);
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            ml[z][x] = make_float2(-INFINITY, 0.f);
-            v[z][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x0 + x < count && h < heads) {
-              const int c = base + (x0 + x) * step;
-              const int64_t at = int64_t(c) * 2 + (c == from ? 1 : 0);
-              ml[z][x] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h));
-              v[z][x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * (C::kHeads * D) + h * D + d));
-            }
+          if (h >= heads) continue;
+          if (grouped) {
+            const int64_t at = place_of(base);
+            __stcg(reinterpret_cast<float4*>(a.part_o + at * (C::kHeads * D) + h * D + d), sum[z].o);
+            if (d == 0)
+              __stcg(reinterpret_cast<float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h),
+                     make_float2(sum[z].top, sum[z].sum));
+          } else {
+            store_joined(a, D, p.b, first + h, d, sum[z]);
           }
-        }
-#pragma unroll
-        for (int z = 0; z < kItems; ++z) sum[z].add(ml[z], v[z]);
-      }
-      // a group's sum takes the place of its first part, which a head's warp alone reads
-      static_assert(32 % kQuads == 0, "a head's values lie in one warp");
-      __syncwarp();
-#pragma unroll
-      for (int z = 0; z < kItems; ++z) {
-        const int i = tid + z * kThreads, h = i / kQuads, d = 4 * (i % kQuads);
-        if (h >= heads) continue;
-        if (grouped) {
-          const int64_t at = int64_t(base) * 2 + (base == from ? 1 : 0);
-          __stcg(reinterpret_cast<float4*>(a.part_o + at * (C::kHeads * D) + h * D + d), sum[z].o);
-          if (d == 0)
-            __stcg(reinterpret_cast<float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h),
-                   make_float2(sum[z].top, sum[z].sum));
-        } else {
-          store_joined(a, D, p.b, first + h, d, sum[z]);
         }
       }
       if (!grouped) break;
@@ -749,34 +762,50 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   }
 }
 
-template <int D, int NT, typename U>
+template <int D, int NT, bool kSide, typename U>
 cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
   using C = DecodeCfg<D, NT>;
   static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<D, NT>) + 1024) <= 233472, "shared memory of an SM");
-  cudaError_t e = set_smem_limit_once<decode_kernel<D, NT, U>>(C::kSmemBytes);
+  cudaError_t e = set_smem_limit_once<decode_kernel<D, NT, kSide, U>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(decode_kernel<D, NT, U>, dim3(sms * C::kCtasPerSm), kDecodeWarps * 32, C::kSmemBytes, 1, stream, a);
+  return launch_overlapped(decode_kernel<D, NT, kSide, U>, dim3(sms * C::kCtasPerSm), kDecodeWarps * 32, C::kSmemBytes, 1,
+                           stream, a);
+}
+
+template <int D, typename U>
+cudaError_t launch_by_heads(const DecodeArgs& a, int sms, cudaStream_t stream) {
+  if (a.together > 1) return launch<D, 2, true, U>(a, sms, stream);
+  return a.part_heads <= 8 ? launch<D, 1, false, U>(a, sms, stream) : launch<D, 2, false, U>(a, sms, stream);
 }
 
 }  // namespace
 
-DecodeSpace decode_space(int D, int part_heads, int sms) {
-  const int heads = part_heads <= 8 ? 8 : 16;
+DecodeSpace decode_space(int D, const QueryParts& parts, int sms) {
+  const int heads = parts.part_heads <= 8 ? 8 : 16;
   const int ctas = sms * (D == 64 ? DecodeCfg<64, 1>::kCtasPerSm : DecodeCfg<128, 1>::kCtasPerSm);
   static_assert(DecodeCfg<64, 1>::kCtasPerSm == DecodeCfg<64, 2>::kCtasPerSm &&
                     DecodeCfg<128, 1>::kCtasPerSm == DecodeCfg<128, 2>::kCtasPerSm, "one grid for each D");
-  // a counter for the row that begins in a CTA's share, two for groups that a CTA leads
-  return {3 * ctas, int64_t(ctas) * 2 * heads * 2, int64_t(ctas) * 2 * heads * D};
+  // a counter for the row that begins in a CTA's share, two for groups that a CTA
+  // leads; two places for each CTA and part
+  const int64_t places = int64_t(ctas) * 2 * parts.together;
+  return {3 * ctas, places * heads * 2, places * heads * D};
+}
+
+QueryParts query_parts(int group) {
+  QueryParts k{1, 1, 1, group};
+  while (k.together < kDecodeWarps && k.together * kMostHeads < group) k.together *= 2;
+  k.passes = (group + kMostHeads * k.together - 1) / (kMostHeads * k.together);
+  k.parts = k.passes * k.together;
+  k.part_heads = (group + k.parts - 1) / k.parts;  // above 8 where there are parts
+  return k;
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t stream) {
   // the units of B full table rows
   const int64_t most = int64_t(a.B) * (int64_t(a.max_pages) * a.div.d / kTile + 1 + kRowUnits);
-  const bool wide = most > UINT32_MAX / (a.Hkv * a.parts);
-#define JFA_DECODE(D, NT) (wide ? launch<D, NT, uint64_t>(a, sms, stream) : launch<D, NT, uint32_t>(a, sms, stream))
-  if (a.part_heads <= 8) return a.D == 128 ? JFA_DECODE(128, 1) : JFA_DECODE(64, 1);
-  return a.D == 128 ? JFA_DECODE(128, 2) : JFA_DECODE(64, 2);
-#undef JFA_DECODE
+  if (most > UINT32_MAX / (a.Hkv * a.passes))
+    return a.D == 128 ? launch_by_heads<128, uint64_t>(a, sms, stream) : launch_by_heads<64, uint64_t>(a, sms, stream);
+  return a.D == 128 ? launch_by_heads<128, uint32_t>(a, sms, stream) : launch_by_heads<64, uint32_t>(a, sms, stream);
 }
 
 }  // namespace jfa

@@ -105,7 +105,7 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream);
 
 struct DecodeArgs {
   int B, H, Hkv, D;
-  int parts, part_heads;  // a key/value head's query heads in parts of at most 16
+  int parts, together, passes, part_heads;  // QueryParts
   int64_t num_pages;
   int max_pages;
   PageDiv div;
@@ -122,12 +122,19 @@ struct DecodeArgs {
   int* counters;             // arrivals at the parts of split rows; zero between launches
   float *part_ml, *part_o;   // what CTAs leave of split rows
 };
+// A key/value head's query heads in parts of at most 16: `together` of them (1, 2,
+// 4 or 8) side by side in a CTA, in `passes` over the cache.
+struct QueryParts {
+  int parts, together, passes, part_heads;
+};
+QueryParts query_parts(int group);
+
 // Workspace of a decode launch: counters (int), part_ml and part_o (float).
 struct DecodeSpace {
   int counters;
   int64_t part_ml, part_o;
 };
-DecodeSpace decode_space(int D, int part_heads, int sms);
+DecodeSpace decode_space(int D, const QueryParts& parts, int sms);
 cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace jfa

@@ -17,7 +17,7 @@ struct jfa_rotary {
 
 struct jfa_pager {
   int max_seqs, max_pages, H, Hkv, D, device, sms;
-  int parts, part_heads;
+  jfa::QueryParts parts;
   int64_t num_pages;
   jfa::PageDiv div;
   int *d_status, *d_counters;  // in the caller's block, as the rest
@@ -103,14 +103,12 @@ int check_pages(const jfa_pages* g) {
 // A pager's block: status word, counters, then what split rows leave.
 struct Block {
   size_t counters, part_ml, part_o, bytes;
-  int parts, part_heads;
+  jfa::QueryParts parts;
 };
 Block block_of(int H, int Hkv, int D, int sms) {
   Block k;
-  const int group = H / Hkv;
-  k.parts = (group + 15) / 16;
-  k.part_heads = (group + k.parts - 1) / k.parts;
-  const jfa::DecodeSpace n = jfa::decode_space(D, k.part_heads, sms);
+  k.parts = jfa::query_parts(H / Hkv);
+  const jfa::DecodeSpace n = jfa::decode_space(D, k.parts, sms);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   k.counters = 256;
   k.part_ml = up(k.counters + n.counters * sizeof(int));
@@ -235,7 +233,6 @@ int jfa_pager_create(int max_seqs, int max_pages, int64_t num_pages, int page_si
   p->device = dev;
   p->sms = sms;
   p->parts = k.parts;
-  p->part_heads = k.part_heads;
   p->num_pages = num_pages;
   p->div = jfa::make_page_div(page_size);
   p->d_status = reinterpret_cast<int*>(base);
@@ -352,8 +349,10 @@ int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, con
   a.H = pager->H;
   a.Hkv = pager->Hkv;
   a.D = pager->D;
-  a.parts = pager->parts;
-  a.part_heads = pager->part_heads;
+  a.parts = pager->parts.parts;
+  a.together = pager->parts.together;
+  a.passes = pager->parts.passes;
+  a.part_heads = pager->parts.part_heads;
   a.num_pages = pager->num_pages;
   a.max_pages = pager->max_pages;
   a.div = pager->div;
