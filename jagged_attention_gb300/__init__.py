@@ -669,7 +669,7 @@ class Pager:
         self.block = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
         h = _vp()
         _check(lib().jfa_pager_create(max_seqs, max_pages, num_pages, page_size, H, Hkv, D, self.block.data_ptr(), n,
-                                      _stream(None), ctypes.byref(h)), "jfa_pager_create")
+                                      _raw_stream(self.index), ctypes.byref(h)), "jfa_pager_create")
         self._h = h
 
     @property

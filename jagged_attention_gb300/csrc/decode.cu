@@ -6,29 +6,40 @@
 // Everything but the operands of the tensor cores is fp32.  A weight goes into
 // the product with V as the sum of two bf16 values (its rounding and what that
 // leaves), 16 bits in all: one bf16 alone would add as much error to the output
-// as its own rounding to bf16 does.
+// as its own rounding to bf16 does, and saves 0 to 2% of the time.
 //
 // Bound: every cached row is read once, 4 D bytes for 4 D G flops (G query heads
-// to a key/value head), so memory bandwidth bounds it for G up to the hundreds.
-// The products use mma.sync, transposed -- rows of the cache are the long side
-// of the 16 x 8 tile, up to 8 query heads (16: two tiles) the short one -- which
-// wastes least of the tile and leaves the cache rows in the layout that
-// ldmatrix reads; tcgen05 would want 64 or 128 query rows per product.
+// to a key/value head), so memory bandwidth bounds it while G is small.  The
+// products use mma.sync, transposed -- rows of the cache are the long side of the
+// 16 x 8 tile, up to 8 query heads (16: two tiles) the short one -- which wastes
+// least of the tile and leaves the cache rows in the layout that ldmatrix reads;
+// tcgen05 would want 64 or 128 query rows per product.  The tensor pipe is 12%
+// busy at G = 8.
+//
+// Split: a tile is 32 cached rows for one key/value head.  All tiles of all
+// requests in the order (request, head, row) are dealt in equal contiguous shares
+// to the CTAs, and a CTA's share to its warps; a warp streams its tiles by
+// cp.async through a stage for K and one for V -- the next K is on its way while V
+// is used, and the other way round -- over the ends of rows and requests, and
+// meets no barrier on the way.  What is left at the ends of the warps' shares is
+// joined in shared memory, what is left at the ends of the CTAs' shares in global
+// memory by the CTA that arrives last, in the order of the shares: the same
+// arguments give the same bits.  So one row of any length and thousands of short
+// ones spread alike, without a schedule from the host.
 //
 // More than 16 query heads to a key/value head are taken in 2, 4 or 8 parts by as
 // many warps side by side, which walk over the same tiles at the same pace: memory
-// is read once, for the others the cache is in L2.
+// is read once, for the others the cache is in L2 (64 requests, 1.1 GB, 24 heads on
+// each of 2: 226 us, one part after the other 340 us).
 //
-// Split: a tile is 32 cached rows for one key/value head.  All tiles of all requests in the order (request,
-// head, row) are dealt in equal contiguous shares to the CTAs, and a CTA's share
-// to its warps; a warp streams its tiles by cp.async through a stage for K and one
-// for V -- the next K is on its way while V is used, and the other way round --
-// over the ends of rows and requests, and meets no barrier on the way.
-// What is left at the ends of the warps' shares is joined in shared memory, what
-// is left at the ends of the CTAs' shares in global memory by the CTA that
-// arrives last, in the order of the shares: the same arguments give the same
-// bits.  So one row of any length and thousands of short ones spread alike,
-// without a schedule from the host.
+// Measured (GB300, 6.67 TB/s copied): 96 requests up to 32768 rows, 64 heads on 8,
+// 7.2 GB in 1051 us, 6.8 TB/s; 128 requests of 16 to 8192 rows, 443 MB in 75 us,
+// 5.9 TB/s; one request of 131072, 268 MB in 51 us, 5.2 TB/s; one of 300 rows in
+// 7.4 us.  What is left of the middle sizes is about 3 us until the first rows
+// arrive (lengths, table, rows: three dependent trips to memory), 3 to 6 us of
+// joining, and SMs whose memory is 7% slower than others'.  64 KB of K and V in
+// flight in the two stages of 8 warps measured best: with three stages the full
+// cache took 1126 us for 1070, with 6 warps 1094 for 1064.
 #include <climits>
 
 #include "kernels.h"
@@ -55,13 +66,17 @@ struct DecodeCfg {
 };
 
 // Units of work: the n tiles of a (request, key/value head) count n units, and
-// kRowUnits behind them stand for its beginning and end.
+// kRowUnits behind them stand for its beginning and end (256 requests up to 300
+// rows: 35.5 us without, 33.7 with; one long row 51.7 and 51.4).
 constexpr int kRowUnits = 2;
 
-// Parts of a row that one CTA joins at a time, where a row has more than twice as many.
+// Parts of a row that one CTA joins at a time, where a row has more than three times
+// as many (38 parts of 16 heads: 24.1 us, all at once 29.9; 18 parts of 12 heads:
+// 12.8 and 12.5).
 constexpr int kGroup = 8;
 
-// Few rows of at most this many tiles get a CTA each.
+// Few rows of at most this many tiles get a CTA each (4 rows of 300: 7.4 us, spread
+// over 9 CTAs and joined 8.7).
 constexpr int kApartTiles = 12;
 
 // Where a warp stands: tile t of n of (request b, key/value head and pass vh), unit
@@ -121,7 +136,7 @@ __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
 __device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
 
 // The cache is read once a launch: its lines are the first to leave L2, before the
-// lengths, tables and queries.
+// lengths, tables and queries (1 to 5% of a call of 30 to 75 us).
 __device__ __forceinline__ uint64_t read_once_policy() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -163,19 +178,18 @@ __device__ __forceinline__ int o_at(int head, int d) {
   return head * D + (d ^ (((head >> 1) & 3) << 3));
 }
 
-// Shares of `total` items dealt to n takers: taker i's first.
+// Items dealt to takers in equal contiguous shares, the first `more` of them with one more.
 template <typename U>
-__device__ __forceinline__ U share(U total, int n, int i) {
-  const U per = total / U(n), more = total - per * U(n);
-  return per * U(i) + min(U(i), more);
-}
-// The taker of item u.
-template <typename U>
-__device__ __forceinline__ int taker(U total, int n, U u) {
-  const U per = total / U(n), more = total - per * U(n);
-  const U big = more * (per + 1);
-  return static_cast<int>(u < big ? u / (per + 1) : more + (u - big) / per);
-}
+struct Deal {
+  U per, more;
+  __device__ __forceinline__ Deal(U items, int takers) : per(items / U(takers)), more(items - per * U(takers)) {}
+  __device__ __forceinline__ U from(int i) const { return per * U(i) + min(U(i), more); }
+  __device__ __forceinline__ int taker(U item) const {
+    const U big = more * (per + 1);
+    return static_cast<int>(item < big ? item / (per + 1) : more + (item - big) / per);
+  }
+};
+
 // Query heads [first, first + count) of part x of all, a.parts to a key/value head.
 __device__ __forceinline__ void heads_of(const DecodeArgs& a, int x, int* first, int* count) {
   const int group = a.H / a.Hkv, kv = x / a.parts;
@@ -213,7 +227,7 @@ __device__ __forceinline__ void store_joined(const DecodeArgs& a, int D, int b, 
 }
 
 // U: unsigned type that counts all units.  32 bits hold them unless the table is
-// wide enough for more; divisions and scans in 64 bits cost a short call 1 us.
+// wide enough for more; 64 bits cost 0.2 to 0.4 us.
 // kSide: parts of query heads side by side.
 template <int D, int NT, bool kSide, typename U>
 __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeCfg<D, NT>::kCtasPerSm)
@@ -284,28 +298,23 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   else if (total < U(ctas) << sub_bits)
     ctas = max(1, static_cast<int>(total >> sub_bits));
   const int cta = blockIdx.x;
-  U cta_lo = 0, cta_n = 0;
-  if (cta < ctas) {
-    cta_lo = share(total, ctas, cta);
-    cta_n = share(total, ctas, cta + 1) - cta_lo;
-  }
+  const Deal<U> deal(total, ctas);
+  const U cta_lo = cta < ctas ? deal.from(cta) : 0, cta_n = cta < ctas ? deal.from(cta + 1) - cta_lo : 0;
   auto sub_from = [&](int i) -> U { return cta_lo + (cta_n >> sub_bits) * U(i) + min(U(i), cta_n & U(subs - 1)); };
   {
     // the thread in whose requests a warp's share begins says where
-    const U first = (units_to - units) * vheads, end = units_to * vheads;
+    const U end = units_to * vheads;
+    U first = (units_to - units) * vheads;
     if (first < cta_lo + cta_n && end > cta_lo) {
+      int b = b_lo, len = length_of(a, b);
       for (int w = 0; w < subs; ++w) {
         const U u = sub_from(w);
-        if (u < first || u >= end) continue;
-        U at = first;
-        int b = b_lo, len = length_of(a, b);
-        while (b + 1 < b_hi && u >= at + units_of(tiles_of(len)) * vheads) {
-          at += units_of(tiles_of(len)) * vheads;
-          len = length_of(a, ++b);
-        }
+        if (u < first) continue;
+        if (u >= end) break;
+        for (U n; b + 1 < b_hi && u >= first + (n = units_of(tiles_of(len)) * vheads); len = length_of(a, ++b)) first += n;
         sh.start_b[w] = b;
         sh.start_len[w] = len;
-        sh.start_unit[w] = at;
+        sh.start_unit[w] = first;
       }
     }
   }
@@ -681,8 +690,8 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     sh.last[tid] = 0;
     if (slot >= 0) {
       const Stretch& p = sh.part[slot];
-      const int from = taker(total, ctas, static_cast<U>(p.u0)), to = taker(total, ctas, static_cast<U>(p.u0) + p.n - 1);
-      const bool grouped = to - from + 1 > 2 * kGroup;
+      const int from = deal.taker(static_cast<U>(p.u0)), to = deal.taker(static_cast<U>(p.u0) + p.n - 1);
+      const bool grouped = to - from + 1 > 3 * kGroup;
       const int lead = grouped ? from + (cta - from) / kGroup * kGroup : from;
       sh.from[tid] = from;
       sh.to[tid] = to;
@@ -696,7 +705,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     if (!sh.last[place]) continue;
     const Stretch& p = sh.part[place == 0 ? open[0] : open[1]];
     const int from = sh.from[place], to = sh.to[place];
-    bool grouped = to - from + 1 > 2 * kGroup;
+    bool grouped = to - from + 1 > 3 * kGroup;
     int base = grouped ? from + (cta - from) / kGroup * kGroup : from, step = 1;
     int count = grouped ? min(kGroup, to + 1 - base) : to - from + 1;
     for (;;) {

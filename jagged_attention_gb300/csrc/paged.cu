@@ -21,6 +21,8 @@ namespace {
 // many rows a cluster of 8 that each form the sums for themselves -- cheaper than
 // a second launch -- and share out pages and rows; the cluster's barrier stands
 // between giving and taking, and before lengths are overwritten in place.
+// Measured on GB300: 256 requests and tokens 6.0 us, 96 requests and 50141 rows
+// 10.5 us (one CTA: 52 us).
 // ---------------------------------------------------------------------------
 constexpr int kTableThreads = 1024, kTableCluster = 8;
 

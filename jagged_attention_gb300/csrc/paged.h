@@ -8,10 +8,10 @@ namespace jfa {
 
 // These kernels are launched before the one ahead of them in the stream has quite
 // ended: they are set up while its last writes settle, and wait for those before
-// they touch memory.  Back to back that takes 0.2 to 0.5 us off a call of 3 to 8 us
-// (letting go of the next kernel earlier, while this one still runs, gains nothing
-// more).  As a kernel so begins before its inputs are final, nothing is read
-// through the non-coherent cache.
+// they touch memory.  Back to back that takes 0.2 to 0.5 us off a call (letting go
+// of the next kernel earlier, while this one still runs, gains nothing more).  As a
+// kernel so begins before its inputs are final, nothing is read through the
+// non-coherent cache.
 #ifdef __CUDACC__
 __device__ __forceinline__ void wait_for_launch_before() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

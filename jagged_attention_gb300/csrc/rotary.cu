@@ -13,6 +13,11 @@
 // With (x[i], x[i + pairs]) lo and hi are the two members; interleaved, each run
 // holds four whole pairs.  Either way the D/16 threads of a row read whole
 // 128-byte lines per run.
+//
+// Measured (GB300, 6.67 TB/s copied): 786432 rows of 8 heads, 3.2 GB in 471 us,
+// 6.85 TB/s; 17311 rows of 4 fp32 and 4 bf16 heads, 106 MB in 18.8 us, 5.7 TB/s;
+// 32769 rows into pages, 268 MB in 44.5 us, 6.0 TB/s; 256 rows of 4 heads in 2.8
+// us, 64 rows of 48 in 3.2 us, of which 2 us are the launch.
 #include <algorithm>
 
 #include "paged.h"
