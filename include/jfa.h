@@ -568,8 +568,9 @@ int jfa_pager_status(jfa_pager_t pager, void* stream, int* raw);
  *   positions     int32 [rows]: lens[b] + i for the i-th new row; 0 behind
  *   row_offsets   int32 [B + 1]: the first new row of each request (delta > 0
  *                 counts whether the request was left as it was or not)
- * `rows` is the capacity of slots and positions.  Distinct outputs must not
- * overlap.  A call whose lens_out and n_free_out are not its lens and n_free
+ * A page belongs to one request: giving back a page that another table shares
+ * puts it onto the free list twice.  `rows` is the capacity of slots and
+ * positions.  Distinct outputs must not overlap.  A call whose lens_out and n_free_out are not its lens and n_free
  * can be repeated with the same result.
  */
 int jfa_paged_tables(jfa_pager_t pager, int B, const int32_t* lens, const int32_t* delta,

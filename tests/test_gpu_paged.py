@@ -562,16 +562,23 @@ def test_serving_run(captured):
         assert [len(x) for x in kept] == lens_now.tolist()
 
 
-def test_decode_tables_wide_enough_for_64_bit_counts():
-    """A table of which full rows would hold more than 2^32 tiles."""
-    pager, q, kp, vp, table, lens = _decode_case([300, 5000, 0, 17], 16, 8, 64, 1024, False, 12)
-    wide = torch.full((4, 1 << 20), -1, dtype=I32, device="cuda")
-    wide[:, :table.shape[1]] = table
-    big = jfa.Pager(max_seqs=4, max_pages=1 << 20, num_pages=kp.shape[0], page_size=1024, H=16, Hkv=8, D=64)
-    assert 4 * ((1 << 20) * 1024 // 16 + 1) * 8 > 2**32 - 1 - 2**31
-    out, lse = _check_decode(big, q, kp, vp, wide, lens)
-    narrow = jfa.paged_decode(pager, q, kp, vp, table, lens, 0.125)
-    assert torch.equal(out, narrow[0]) and torch.equal(lse, narrow[1])
+@pytest.mark.parametrize("hq,hk,D", [(16, 8, 64), (32, 2, 64), (40, 2, 64), (10, 2, 128), (32, 2, 128), (70, 2, 128)])
+def test_decode_tables_wide_enough_for_64_bit_counts(hq, hk, D):
+    """A table of which full rows would hold more tiles than 32 bits count."""
+    pager, q, kp, vp, table, lens = _decode_case([300, 5000, 0, 17], hq, hk, D, 1024, False, 12)
+    pages = (1 << 21) - 2
+    wide = torch.full((64, pages), -1, dtype=I32, device="cuda")  # 0.5 GB; only the rows of 64 requests count
+    wide[:4, :table.shape[1]] = table
+    big = jfa.Pager(max_seqs=64, max_pages=pages, num_pages=kp.shape[0], page_size=1024, H=hq, Hkv=hk, D=D)
+    assert 64 * (pages * 1024 // 32) > 2**32 // hk
+    many = torch.zeros((64, hq, D), dtype=BF16, device="cuda")
+    many[:4] = q
+    some = torch.zeros(64, dtype=I32, device="cuda")
+    some[:4] = lens
+    out, lse = _check_decode(big, many, kp, vp, wide, some)
+    narrow = jfa.paged_decode(pager, q, kp, vp, table, lens, 1 / math.sqrt(D))
+    assert torch.equal(out[:4], narrow[0]) and torch.equal(lse[:, :4], narrow[1])
+    assert not out[4:].any() and torch.isinf(lse[:, 4:]).all()
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -605,3 +612,49 @@ def test_a_stream_of_its_own():
                            stream=side.cuda_stream)
     side.synchronize()
     assert got[0].tolist() == [3, 5]
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (6, 2)])
+def test_decode_the_most_requests(hq, hk):
+    """16384 requests of 0 to 40 rows, a page of 40 each, against a batched 64-bit softmax."""
+    B, page, D = 16384, 40, 64
+    rng = np.random.default_rng(1)
+    lens, order = rng.integers(0, page + 1, B), rng.permutation(B)
+    pager = jfa.Pager(max_seqs=B, max_pages=1, num_pages=B, page_size=page, H=hq, Hkv=hk, D=D)
+    kp, vp, q = _draw((B, page, hk, D), 1), _draw((B, page, hk, D), 2), _draw((B, hq, D), 3)
+    table, dl = _ints(order[:, None]), _ints(lens)
+    out, lse = jfa.paged_decode(pager, q, kp, vp, table, dl, 0.125)
+    assert pager.status() == 0
+    k, v = (x[table[:, 0].long()].double().repeat_interleave(hq // hk, 2) for x in (kp, vp))
+    s = 0.125 * torch.einsum("bhd,bthd->bht", q.double(), k)
+    size = 0.125 * torch.einsum("bhd,bthd->bht", q.double().abs(), k.abs()).amax(-1)
+    dead = torch.arange(page, device="cuda")[None, None] >= dl[:, None, None]
+    w = torch.softmax(s.masked_fill(dead, -math.inf), -1).nan_to_num(0.0)
+    want, mass = torch.einsum("bht,bthd->bhd", w, v), torch.einsum("bht,bthd->bhd", w, v.abs())
+    # the bounds of paged_ref.decode
+    delta = 2 * D * 2.0 ** -24 * size + 2.0 ** -15 + 2 * page * 2.0 ** -24
+    step = torch.finfo(BF16).eps / 2
+    assert ((out.double() - want).abs() <= 2 * delta[..., None] * mass * (1 + step) + step * want.abs()).all()
+    ref = torch.logsumexp(s.masked_fill(dead, -math.inf), -1)
+    some = (dl > 0)[:, None].expand_as(ref)
+    assert ((lse.T.double() - ref).abs()[some] <= (delta + 2.0 ** -23 * ref.abs())[some]).all()
+    assert (lse.T[~some] == -math.inf).all()
+
+
+def test_tables_of_the_most_requests():
+    B, page, width = 16384, 4, 3
+    rng, lens, table, free, n_free = _tables_case(B, page, width, B * width, page * width - 3, 21)
+    delta = np.where(rng.random(B) < 0.4, -rng.integers(0, lens + 1), rng.integers(0, 4, B))
+    _run_tables(lens, delta, table, free, n_free, int(np.maximum(delta, 0).sum()) + 5, page, B * width, in_place=True)
+
+
+def test_tables_down_to_the_last_page():
+    """A step that takes every free page, and one that wants one more."""
+    table = np.array([[0, -1, -1], [1, -1, -1], [2, -1, -1]])
+    free = np.array([5, 4, 3, 0, 0, 0])
+    want = _run_tables([4, 4, 4], [1, 1, 1], table, free, 3, 3, 4, 6)
+    assert want[1] == 0 and want[-1] == 0
+    want = _run_tables([4, 4, 4], [1, 5, 1], table, free, 3, 7, 4, 6)
+    assert want[-1] == paged_ref.NO_PAGES and want[1] == 0
+    want = _run_tables([4, 4, 4], [1, -4, 5], table, free, 2, 6, 4, 6)  # served from what the second gives back
+    assert want[-1] == 0 and want[1] == 0
