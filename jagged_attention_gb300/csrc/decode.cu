@@ -123,8 +123,7 @@ struct DecodeShared {
   float m[2 * kDecodeWarps][8 * NT], l[2 * kDecodeWarps][8 * NT];
   int64_t scan_units[kDecodeWarps];
   int scan_rows[kDecodeWarps], scan_most[kDecodeWarps];
-  int64_t start_unit[kDecodeWarps];  // where the request begins in which a warp's share does
-  int start_b[kDecodeWarps], start_len[kDecodeWarps];
+  int64_t first_unit[kDecodeWarps * 32];  // of the requests that a thread adds up
   int from[2], to[2], last[2];
 };
 
@@ -190,12 +189,13 @@ struct Deal {
   }
 };
 
-// Query heads [first, first + count) of part x of all, a.parts to a key/value head.
+// Query heads [first, first + count) of part x of all, a.parts to a key/value head:
+// one where the parts are not side by side.
+template <bool kSide>
 __device__ __forceinline__ void heads_of(const DecodeArgs& a, int x, int* first, int* count) {
-  const int group = a.H / a.Hkv, kv = x / a.parts;
-  const int g0 = (x - kv * a.parts) * a.part_heads;
-  *first = kv * group + g0;
-  *count = max(0, min(a.part_heads, group - g0));  // 0: more parts than heads fill
+  const int kv = kSide ? x / a.parts : x, g0 = kSide ? (x - kv * a.parts) * a.part_heads : 0;
+  *first = kv * a.group + g0;
+  *count = kSide ? max(0, min(a.part_heads, a.group - g0)) : a.group;  // 0: more parts than heads fill
 }
 
 // 4 values of out, normalised already.
@@ -239,7 +239,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   wait_for_launch_before();
   // A CTA's share is dealt to `subs` sets of `together` warps, one for each part of
   // the query heads; a line is a warp's place with those of its part in a row.
-  const int vheads = a.Hkv * a.passes, together = kSide ? a.together : 1;
+  const int passes = kSide ? a.passes : 1, vheads = a.Hkv * passes, together = kSide ? a.together : 1;
   const int sub_bits = kSide ? __ffs(kDecodeWarps / together) - 1 : __builtin_ctz(kDecodeWarps), subs = 1 << sub_bits;
   const int part = kSide ? warp & (together - 1) : 0, sub = kSide ? warp / together : warp;
   const int line = (part << sub_bits) + sub;
@@ -301,23 +301,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   const Deal<U> deal(total, ctas);
   const U cta_lo = cta < ctas ? deal.from(cta) : 0, cta_n = cta < ctas ? deal.from(cta + 1) - cta_lo : 0;
   auto sub_from = [&](int i) -> U { return cta_lo + (cta_n >> sub_bits) * U(i) + min(U(i), cta_n & U(subs - 1)); };
-  {
-    // the thread in whose requests a warp's share begins says where
-    const U end = units_to * vheads;
-    U first = (units_to - units) * vheads;
-    if (first < cta_lo + cta_n && end > cta_lo) {
-      int b = b_lo, len = length_of(a, b);
-      for (int w = 0; w < subs; ++w) {
-        const U u = sub_from(w);
-        if (u < first) continue;
-        if (u >= end) break;
-        for (U n; b + 1 < b_hi && u >= first + (n = units_of(tiles_of(len)) * vheads); len = length_of(a, ++b)) first += n;
-        sh.start_b[w] = b;
-        sh.start_len[w] = len;
-        sh.start_unit[w] = first;
-      }
-    }
-  }
+  sh.first_unit[tid] = (units_to - units) * vheads;
   __syncthreads();
 
   const U lo = sub_from(sub), hi = sub_from(sub + 1);
@@ -342,12 +326,24 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       } while (c.n == 0 && c.b + 1 < a.B);
     };
     Cursor<U> at;  // of the tile whose rows are looked up next
-    at.u = lo;
-    at.b = sh.start_b[sub];
-    at.len = sh.start_len[sub];
-    at.n = tiles_of(at.len);
     {
-      const U r = lo - static_cast<U>(sh.start_unit[sub]), per = units_of(at.n);
+      // the last thread whose requests begin at or before the share, by groups of
+      // kDecodeWarps threads and then within the group
+      auto begins = [&](int t) { return static_cast<U>(sh.first_unit[t]) <= lo; };
+      static_assert(kDecodeWarps <= 32, "a group's threads have a lane each");
+      const int t0 = (__popc(__ballot_sync(~0u, begins(lane * kDecodeWarps))) - 1) * kDecodeWarps;
+      const int t = t0 + __popc(__ballot_sync(~0u, lane < kDecodeWarps && begins(t0 + (lane % kDecodeWarps)))) - 1;
+      U r = lo - static_cast<U>(sh.first_unit[t]);
+      at.u = lo;
+      at.b = t * slab;
+      for (;; ++at.b) {
+        at.len = length_of(a, at.b);
+        at.n = tiles_of(at.len);
+        const U all = units_of(at.n) * vheads;
+        if (r < all || at.b + 1 >= a.B) break;
+        r -= all;
+      }
+      const U per = units_of(at.n);
       at.vh = static_cast<int>(r / per);
       at.t = static_cast<int>(r - U(at.vh) * per);
     }
@@ -357,7 +353,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     int64_t head_off = 0;
     auto row_of_at = [&] {
       table = a.table + at.b * a.table_row;
-      head_off = (at.vh / a.passes) * a.head;
+      head_off = (at.vh / passes) * a.head;
     };
     row_of_at();
 
@@ -437,7 +433,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       if (fresh) {
         fresh = false;
         t0 = now.t;
-        heads_of(a, now.vh * together + part, &first, &heads);
+        heads_of<kSide>(a, now.vh * together + part, &first, &heads);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const bool have = 8 * n + g < heads;
@@ -648,7 +644,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     if (!whole) (place == 0 ? open[0] : open[1]) = s;
     if ((turn & (turns - 1)) != my_turn) continue;
     int first, heads;
-    heads_of(a, p.x, &first, &heads);
+    heads_of<kSide>(a, p.x, &first, &heads);
     for (int i = row_tid; i < heads * kQuads; i += row_threads) {
       const int h = i / kQuads, d = 4 * (i % kQuads);
       Joined sum;
@@ -711,7 +707,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     for (;;) {
       for (int y = 0; y < together; ++y) {
         int first, heads;
-        heads_of(a, (p.x & -together) + y, &first, &heads);
+        heads_of<kSide>(a, (p.x & -together) + y, &first, &heads);
         // what CTA c has: in its last place where the row begins, else in its first
         auto place_of = [&](int c) { return (int64_t(c) * 2 + (c == from ? 1 : 0)) * together + y; };
         // 4 values of kItems heads to a thread, their loads under way together

@@ -105,6 +105,7 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream);
 
 struct DecodeArgs {
   int B, H, Hkv, D;
+  int group;                                // H / Hkv
   int parts, together, passes, part_heads;  // QueryParts
   int64_t num_pages;
   int max_pages;

@@ -349,6 +349,7 @@ int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, con
   a.H = pager->H;
   a.Hkv = pager->Hkv;
   a.D = pager->D;
+  a.group = pager->H / pager->Hkv;
   a.parts = pager->parts.parts;
   a.together = pager->parts.together;
   a.passes = pager->parts.passes;
