@@ -6,7 +6,7 @@
 // Everything but the operands of the tensor cores is fp32.  A weight goes into
 // the product with V as the sum of two bf16 values (its rounding and what that
 // leaves), 16 bits in all: one bf16 alone would add as much error to the output
-// as its own rounding to bf16 does, and saves 0 to 2% of the time.
+// as its own rounding to bf16 does, and saves 0.5% of the time (9% at G = 24).
 //
 // Bound: every cached row is read once, 4 D bytes for 4 D G flops (G query heads
 // to a key/value head), so memory bandwidth bounds it while G is small.  The
@@ -30,16 +30,16 @@
 // More than 16 query heads to a key/value head are taken in 2, 4 or 8 parts by as
 // many warps side by side, which walk over the same tiles at the same pace: memory
 // is read once, for the others the cache is in L2 (64 requests, 1.1 GB, 24 heads on
-// each of 2: 226 us, one part after the other 340 us).
+// each of 2: 225 us, one part after the other 340 us).
 //
 // Measured (GB300, 6.67 TB/s copied): 96 requests up to 32768 rows, 64 heads on 8,
-// 7.2 GB in 1051 us, 6.8 TB/s; 128 requests of 16 to 8192 rows, 443 MB in 75 us,
-// 5.9 TB/s; one request of 131072, 268 MB in 51 us, 5.2 TB/s; one of 300 rows in
-// 7.4 us.  What is left of the middle sizes is about 3 us until the first rows
+// 7.2 GB in 1049 us, 6.8 TB/s; 128 requests of 0 to 8192 rows, 443 MB in 74 us,
+// 6.0 TB/s; one request of 131072, 268 MB in 50 us, 5.3 TB/s; one of 300 rows in
+// 6.4 us.  What is left of the middle sizes is about 2.5 us until the first rows
 // arrive (lengths, table, rows: three dependent trips to memory), 3 to 6 us of
-// joining, and SMs whose memory is 7% slower than others'.  64 KB of K and V in
-// flight in the two stages of 8 warps measured best: with three stages the full
-// cache took 1126 us for 1070, with 6 warps 1094 for 1064.
+// joining, and SMs whose memory is 7% slower than others'.  128 KB of K and V in
+// the stages of 8 warps measured best: with 192 KB the full cache took 1126 us for
+// 1070, with 6 warps 1094 for 1064.
 #include <climits>
 
 #include "kernels.h"
@@ -67,16 +67,16 @@ struct DecodeCfg {
 
 // Units of work: the n tiles of a (request, key/value head) count n units, and
 // kRowUnits behind them stand for its beginning and end (256 requests up to 300
-// rows: 35.5 us without, 33.7 with; one long row 51.7 and 51.4).
+// rows: 34.6 us without, 32.5 with; 128 mixed ones 74.7 and 74.2).
 constexpr int kRowUnits = 2;
 
 // Parts of a row that one CTA joins at a time, where a row has more than three times
-// as many (38 parts of 16 heads: 24.1 us, all at once 29.9; 18 parts of 12 heads:
-// 12.8 and 12.5).
+// as many (38 parts of 16 heads: 22.9 us, all at once 28.7; up to 24 parts it makes
+// no difference).
 constexpr int kGroup = 8;
 
-// Few rows of at most this many tiles get a CTA each (4 rows of 300: 7.4 us, spread
-// over 9 CTAs and joined 8.7).
+// Few rows of at most this many tiles get a CTA each (4 rows of 300: 6.4 us, spread
+// over more CTAs and joined 7.8).
 constexpr int kApartTiles = 12;
 
 // Where a warp stands: tile t of n of (request b, key/value head and pass vh), unit
@@ -135,7 +135,7 @@ __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
 __device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
 
 // The cache is read once a launch: its lines are the first to leave L2, before the
-// lengths, tables and queries (1 to 5% of a call of 30 to 75 us).
+// lengths, tables and queries (1 to 6% of a call of 23 to 75 us).
 __device__ __forceinline__ uint64_t read_once_policy() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -203,20 +203,6 @@ __device__ __forceinline__ void store_out4(const DecodeArgs& a, int D, int b, in
   *reinterpret_cast<uint2*>(a.out + (int64_t(b) * a.H + head) * D + d) =
       make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
-// Adds one to a counter, releasing this thread's view of memory and acquiring the
-// others': what was there before.
-__device__ __forceinline__ int arrive(int* counter) {
-  int was;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(was) : "l"(counter) : "memory");
-  return was;
-}
-// Whether the caller is the last of `count` at a counter, which starts again then.
-// A barrier before orders the other threads' writes, one behind their reads.
-__device__ __forceinline__ bool last_of(int* counter, int count) {
-  if (arrive(counter) != count - 1) return false;
-  *counter = 0;
-  return true;
-}
 __device__ __forceinline__ float lse_of(float m, float l) { return m * kLn2 + logf(l); }
 
 // A finished row: normalised, with its log-sum-exp.
@@ -227,7 +213,7 @@ __device__ __forceinline__ void store_joined(const DecodeArgs& a, int D, int b, 
 }
 
 // U: unsigned type that counts all units.  32 bits hold them unless the table is
-// wide enough for more; 64 bits cost 0.2 to 0.4 us.
+// wide enough for more; 64 bits cost 0.3 to 0.6 us.
 // kSide: parts of query heads side by side.
 template <int D, int NT, bool kSide, typename U>
 __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeCfg<D, NT>::kCtasPerSm)
@@ -773,7 +759,7 @@ cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
   static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<D, NT>) + 1024) <= 233472, "shared memory of an SM");
   cudaError_t e = set_smem_limit_once<decode_kernel<D, NT, kSide, U>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(decode_kernel<D, NT, kSide, U>, dim3(sms * C::kCtasPerSm), kDecodeWarps * 32, C::kSmemBytes, 1,
+  return launch_overlapped(decode_kernel<D, NT, kSide, U>, dim3(sms * C::kCtasPerSm), kDecodeWarps * 32, C::kSmemBytes,
                            stream, a);
 }
 

@@ -1,4 +1,5 @@
 // paged.cu -- block tables and slots from request lengths.
+#include <algorithm>
 #include <climits>
 
 #include "kernels.h"
@@ -17,14 +18,17 @@ namespace {
 // free_list[top - 1 - p] with top = n_free + all pages given back.  A page or row
 // finds its request by a search in the sums.
 //
-// Bound: a handful of dependent loads.  One launch does it all: one CTA, or for
-// many rows a cluster of 8 that each form the sums for themselves -- cheaper than
-// a second launch -- and share out pages and rows; the cluster's barrier stands
-// between giving and taking, and before lengths are overwritten in place.
-// Measured on GB300: 256 requests and tokens 6.0 us, 96 requests and 50141 rows
-// 10.5 us (one CTA: 52 us).
+// Bound: a handful of dependent loads.  One launch does it all: each CTA forms the
+// sums for itself -- cheaper than a second launch -- and pages and rows are shared
+// out.  No CTA waits for another: a page that is given back and taken again in the
+// same call is read where it comes from, the table of the request that gives it
+// back, and where lengths are overwritten in place, the CTA that is done last does
+// it.
+// Measured on GB300: 256 requests and tokens 6.5 us; 96 requests and 50141 rows 8.2
+// us (a CTA for 8192 pages or rows: 11.9); 157,000 pages given back 9.6 us.
 // ---------------------------------------------------------------------------
-constexpr int kTableThreads = 1024, kTableCluster = 8;
+constexpr int kTableThreads = 1024;
+constexpr int64_t kTableWork = 2048;  // pages and rows that a CTA is started for
 
 // Sums that stop at 2^32 - 1: what goes beyond is refused whatever its size.
 struct Need {
@@ -76,25 +80,17 @@ __device__ __forceinline__ int owner_of(const int* at, int lo, int n, int p) {
   return lo;
 }
 
-__device__ __forceinline__ void all_arrive(bool cluster) {
-  if (cluster) {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  } else {
-    __syncthreads();
-  }
-}
-
 // No pointer is __restrict__ and nothing goes through the read-only cache: lens
 // and n_free may be overwritten in place.
-__global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_constant__ TablesArgs a) {
+__global__ void __launch_bounds__(kTableThreads, 1) tables_kernel(const __grid_constant__ TablesArgs a) {
   wait_for_launch_before();
   extern __shared__ int sm[];
   int* row_at = sm;              // [B + 1] new rows before each request
-  int* give_at = sm + a.B + 1;   // [B] pages given back before it; later: whether it is served
+  int* give_at = sm + a.B + 1;   // [B] pages given back before it
   int* take_at = give_at + a.B;  // [B] pages taken before it
+  auto* served = reinterpret_cast<unsigned char*>(take_at + a.B);  // [B] whether it is served
   __shared__ Need warp_sum[32];
-  __shared__ int problem, taken;
+  __shared__ int problem, taken, last;
   const int capacity = a.max_pages * a.div.d;
   const int tid = threadIdx.x, rank = blockIdx.x, ranks = gridDim.x;
   const int all = tid + rank * kTableThreads, stride = ranks * kTableThreads;
@@ -141,16 +137,7 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
   const bool sound = n_free >= 0 && top <= a.num_pages;
   __syncthreads();
 
-  if (sound && carry.give > 0) {
-    const int give = static_cast<int>(carry.give);
-    for (int p = all; p < give; p += stride) {
-      const int b = owner_of(give_at, 0, a.B, p);
-      a.free_list[n_free + p] = a.table[b * a.table_row + pages(a.lens[b] + a.delta[b]) + (p - give_at[b])];
-    }
-    all_arrive(ranks > 1);  // what is given back may be taken again; give_at is read
-  }
-
-  // who is served: give_at becomes that flag
+  // who is served
   for (int b = tid; b < a.B; b += kTableThreads) {
     const int64_t len = a.lens[b], delta = a.delta[b], after = len + delta;
     bool ok = sound_length(len, after) && (fits || delta <= 0 || row_at[b] + delta <= a.rows);
@@ -166,12 +153,19 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
         if (rank == 0) atomicOr(&problem, kPagerNoPages);
       }
     }
-    give_at[b] = ok;
+    served[b] = ok;
   }
   __syncthreads();
 
-  // The p-th page taken, loaded now and stored behind the rows.
-  const int page_taken = all < taken ? a.free_list[top - 1 - all] : 0;
+  // the p-th page given back, and the p-th page taken
+  auto given = [&](int p) {
+    const int b = owner_of(give_at, 0, a.B, p);
+    return a.table[b * a.table_row + pages(a.lens[b] + a.delta[b]) + (p - give_at[b])];
+  };
+  auto page_taken = [&](int p) {
+    const int64_t at = top - 1 - p;
+    return at < n_free ? a.free_list[at] : given(static_cast<int>(at - n_free));
+  };
 
   // A warp has stretches of 32 * run rows, a lane every 32nd of them: it searches
   // for the first one's request and walks on from there, the pages of kTogether
@@ -184,23 +178,23 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
     int b = -1;
     for (int k0 = 0; k0 < run; k0 += kTogether) {
       int position[kTogether], page[kTogether];
-      bool served[kTogether];
+      bool live[kTogether];
 #pragma unroll
       for (int k = 0; k < kTogether; ++k) {
         const int64_t r = base + 32 * (k0 + k) + lane;
         position[k] = page[k] = 0;
-        served[k] = false;
+        live[k] = false;
         if (k0 + k < run && r < new_rows) {
           const int row = static_cast<int>(r);
           if (b < 0) b = owner_of(row_at, 0, a.B, row);
           while (row_at[b + 1] <= row) ++b;
           const int len = a.lens[b];
           position[k] = static_cast<int>(int64_t(len) + (row - row_at[b]));
-          served[k] = give_at[b];
-          if (served[k]) {
+          live[k] = served[b];
+          if (live[k]) {
             const int i = a.div.quot(position[k]), held = pages(len);
             // entries of new pages are on their way into the table: take them where they come from
-            page[k] = i < held ? a.table[b * a.table_row + i] : a.free_list[top - 1 - take_at[b] - (i - held)];
+            page[k] = i < held ? a.table[b * a.table_row + i] : page_taken(take_at[b] + (i - held));
           }
         }
       }
@@ -209,7 +203,7 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
         const int64_t r = base + 32 * (k0 + k) + lane;
         if (k0 + k >= run || r >= a.rows) continue;
         int slot = -1;
-        if (served[k]) {
+        if (live[k]) {
           if (page[k] >= 0 && page[k] < a.num_pages)
             slot = page[k] * a.div.d + (position[k] - a.div.quot(position[k]) * a.div.d);
           else
@@ -222,28 +216,45 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
   }
   for (int p = all; p < taken; p += stride) {
     const int b = owner_of(take_at, 0, a.B, p);
-    a.table[b * a.table_row + pages(a.lens[b]) + (p - take_at[b])] = p == all ? page_taken : a.free_list[top - 1 - p];
+    a.table[b * a.table_row + pages(a.lens[b]) + (p - take_at[b])] = page_taken(p);
   }
+  const int give = sound ? static_cast<int>(carry.give) : 0;
+  for (int p = all; p < give; p += stride) a.free_list[n_free + p] = given(p);
   for (int b = all; b <= a.B; b += stride) a.row_offsets[b] = row_at[b];
-  all_arrive(ranks > 1);  // lens and n_free are read
-  for (int b = all; b < a.B; b += stride)
-    a.lens_out[b] = give_at[b] ? a.lens[b] + a.delta[b] : a.lens[b];
+
+  int from = all, step = stride;
+  bool writes = true;
+  if (a.lens_out == a.lens || a.n_free_out == a.n_free) {  // nobody may read them any more
+    __syncthreads();
+    if (ranks > 1) {
+      if (tid == 0) last = last_of(a.counter, ranks);
+      __syncthreads();
+      writes = last;
+      from = tid;
+      step = kTableThreads;
+    }
+  }
+  if (writes) {
+    for (int b = from; b < a.B; b += step) a.lens_out[b] = served[b] ? a.lens[b] + a.delta[b] : a.lens[b];
+    if (from == 0) a.n_free_out[0] = static_cast<int>(sound ? top - taken : n_free);
+  }
+  __syncthreads();
   if (tid == 0) {
     const int bits = problem | (sound ? 0 : kPagerBadPage);
-    if (rank == 0) a.n_free_out[0] = static_cast<int>(sound ? top - taken : n_free);
     if (bits) atomicOr(a.status, bits);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
-  cudaError_t e = set_smem_limit_once<tables_kernel>((3 * 16384 + 1) * 4);
+cudaError_t launch_tables(const TablesArgs& a, int sms, cudaStream_t stream) {
+  constexpr int kMostSeqs = 16384;
+  cudaError_t e = set_smem_limit_once<tables_kernel>((3 * kMostSeqs + 1) * 4 + kMostSeqs);
   if (e != cudaSuccess) return e;
-  // one CTA while its threads have no more than one run of rows each
-  const bool many = a.rows > 4 * kTableThreads;
-  const int ctas = many ? kTableCluster : 1;
-  return launch_overlapped(tables_kernel, dim3(ctas), kTableThreads, (3 * a.B + 1) * 4, ctas, stream, a);
+  // how many pages change hands only the device knows: at most all of the table
+  const int64_t most = a.rows + std::min(int64_t(a.B) * a.max_pages, 2 * a.num_pages);
+  const int ctas = static_cast<int>(std::min<int64_t>(sms, 1 + most / kTableWork));
+  return launch_overlapped(tables_kernel, dim3(ctas), kTableThreads, (3 * a.B + 1) * 4 + a.B, stream, a);
 }
 
 }  // namespace jfa

@@ -16,22 +16,32 @@ namespace jfa {
 __device__ __forceinline__ void wait_for_launch_before() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+// Adds one to a counter, releasing this thread's view of memory and acquiring the
+// others': what was there before.
+__device__ __forceinline__ int arrive(int* counter) {
+  int was;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(was) : "l"(counter) : "memory");
+  return was;
+}
+// Whether the caller is the last of `count` at a counter, which starts again then.
+// A barrier before orders the other threads' writes, one behind their reads.
+__device__ __forceinline__ bool last_of(int* counter, int count) {
+  if (arrive(counter) != count - 1) return false;
+  *counter = 0;
+  return true;
+}
 template <typename K, typename... A>
-cudaError_t launch_overlapped(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
-                              const A&... args) {
+cudaError_t launch_overlapped(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 #endif
@@ -100,8 +110,9 @@ struct TablesArgs {
   int32_t *lens_out, *table, *free_list, *n_free_out, *slots, *positions, *row_offsets;
   int64_t table_row;
   int* status;
+  int* counter;  // CTAs that are done; zero between launches
 };
-cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream);
+cudaError_t launch_tables(const TablesArgs& a, int sms, cudaStream_t stream);
 
 struct DecodeArgs {
   int B, H, Hkv, D;

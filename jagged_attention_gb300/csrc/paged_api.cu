@@ -271,6 +271,7 @@ int jfa_paged_tables(jfa_pager_t pager, int B, const int32_t* lens, const int32_
   if (!lens || !delta || !lens_out || !table || !free_list || !n_free || !n_free_out || !row_offsets ||
       (rows > 0 && (!slots || !positions)) || table_row < pager->max_pages)
     return JFA_ERR_INVALID_ARG;
+  if (lens_out == delta || n_free_out == lens_out) return JFA_ERR_INVALID_ARG;  // read or written by others meanwhile
   const void* ptrs[] = {lens, delta, lens_out, table, free_list, n_free, n_free_out, slots, positions, row_offsets};
   for (const void* p : ptrs)
     if (!aligned(p, 4)) return JFA_ERR_ALIGNMENT;
@@ -293,7 +294,8 @@ int jfa_paged_tables(jfa_pager_t pager, int B, const int32_t* lens, const int32_
   a.row_offsets = row_offsets;
   a.table_row = table_row;
   a.status = pager->d_status;
-  return jfa::launch_tables(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+  a.counter = pager->d_status + 16;  // in the block's first 256 bytes, as the status word
+  return jfa::launch_tables(a, pager->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
 int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_row, const void* v,

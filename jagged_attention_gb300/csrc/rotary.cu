@@ -16,7 +16,7 @@
 //
 // Measured (GB300, 6.67 TB/s copied): 786432 rows of 8 heads, 3.2 GB in 471 us,
 // 6.85 TB/s; 17311 rows of 4 fp32 and 4 bf16 heads, 106 MB in 18.8 us, 5.7 TB/s;
-// 32769 rows into pages, 268 MB in 44.5 us, 6.0 TB/s; 256 rows of 4 heads in 2.8
+// 32769 rows into pages, 268 MB in 43.6 us, 6.1 TB/s; 256 rows of 4 heads in 2.8
 // us, 64 rows of 48 in 3.2 us, of which 2 us are the launch.
 #include <algorithm>
 
@@ -30,6 +30,9 @@ namespace {
 // in each: 64 KB an SM.  786432 rows of 8 heads take 470 us so; with four heads at
 // once in half the threads 514 us, with fewer registers (1280 threads) 529 us.
 constexpr int kRowThreads = 64, kBlocksPerSm = 16;
+// 8980 rows of 32 fp32 and 8 bf16 heads: 57 us, all heads in a thread 65; 17311 rows
+// of 4 and 4: 18.8 us, 8 in a thread 19.7.
+constexpr int kHeadsAThread = 12;
 
 // 8 values as they lie in memory.
 template <bool kF32>
@@ -177,15 +180,18 @@ cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   if (a.rows == 0 || a.heads == 0) return cudaSuccess;
   const int64_t per_block = kRowThreads / (a.D / 16);
   const int64_t blocks = (a.rows + per_block - 1) / per_block;
-  // A thread walks over all heads of its row where the rows alone fill the SMs
-  // (1024 threads each); of fewer rows the heads are dealt to more threads, which
-  // form their sines again.
+  // A thread walks over at most kHeadsAThread heads of its row (fp32 ones count
+  // double): more even out less over the SMs, fewer form their sines too often.  Of
+  // rows too few to fill the SMs (1024 threads each) the heads are dealt to more.
+  int64_t weight = 0;
+  for (const RowJob& job : a.job) weight += int64_t(job.heads) * (job.f32 ? 2 : 1);
   const int64_t fill = int64_t(sms) * 1024 / kRowThreads;
-  const int split = static_cast<int>(std::min<int64_t>(a.heads, std::max<int64_t>(1, fill / blocks)));
+  const int split = static_cast<int>(
+      std::min<int64_t>(a.heads, std::max({fill / blocks, (weight + kHeadsAThread - 1) / kHeadsAThread, int64_t(1)})));
   const int per = (a.heads + split - 1) / split;
   const dim3 grid(static_cast<unsigned>(blocks), (a.heads + per - 1) / per);
-  return launch_overlapped(a.turns.interleaved ? rows_kernel<true> : rows_kernel<false>, grid, kRowThreads, 0, 1, stream,
-                           a, per);
+  return launch_overlapped(a.turns.interleaved ? rows_kernel<true> : rows_kernel<false>, grid, kRowThreads, 0, stream, a,
+                           per);
 }
 
 }  // namespace jfa

@@ -470,11 +470,11 @@ def test_host_refusals_with_a_pager():
         assert L.jfa_paged_append(*args) == code, (at, value)
     free = _ints(np.zeros(pager.num_pages))
     one, off = _ints([0]), _ints([0, 0, 0])
-    good = [h, 2, lens.data_ptr(), lens.data_ptr(), lens.data_ptr(), table.data_ptr(), table.stride(0), free.data_ptr(),
+    good = [h, 2, lens.data_ptr(), s.data_ptr(), lens.data_ptr(), table.data_ptr(), table.stride(0), free.data_ptr(),
             one.data_ptr(), one.data_ptr(), 2, s.data_ptr(), s.data_ptr(), off.data_ptr(), None]
     for at, value, code in [(1, 0, 1), (1, 3, 1), (2, None, 1), (3, None, 1), (4, None, 1), (5, None, 1),
                             (5, table.data_ptr() + 2, 4), (6, pager.max_pages - 1, 1), (7, None, 1), (8, None, 1),
-                            (9, None, 1), (10, -1, 1), (10, 2**31, 1), (11, None, 1), (12, None, 1), (13, None, 1)]:
+                            (3, lens.data_ptr(), 1), (9, None, 1), (9, lens.data_ptr(), 1), (10, -1, 1), (10, 2**31, 1), (11, None, 1), (12, None, 1), (13, None, 1)]:
         args = list(good)
         args[at] = value
         assert L.jfa_paged_tables(*args) == code, (at, value)
