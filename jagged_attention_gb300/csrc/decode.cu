@@ -41,6 +41,7 @@
 // the stages of 8 warps measured best: with 192 KB the full cache took 1126 us for
 // 1070, with 6 warps 1094 for 1064.
 #include <climits>
+#include <type_traits>
 
 #include "kernels.h"
 #include "paged.h"
@@ -654,10 +655,10 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       if (whole) {
         store_joined(a, D, p.b, first + h, d, sum);
       } else {
-        const int64_t at = (int64_t(cta) * 2 + place) * together + (p.x & (together - 1));
-        __stcg(reinterpret_cast<float4*>(a.part_o + at * (C::kHeads * D) + h * D + d), sum.o);
+        const int at = (2 * cta + place) * together + (p.x & (together - 1));
+        __stcg(reinterpret_cast<float4*>(a.part_o + (at * C::kHeads + h) * D + d), sum.o);
         if (d == 0)
-          __stcg(reinterpret_cast<float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h), make_float2(sum.top, sum.sum));
+          __stcg(reinterpret_cast<float2*>(a.part_ml + (at * C::kHeads + h) * 2), make_float2(sum.top, sum.sum));
       }
     }
   }
@@ -694,15 +695,17 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       for (int y = 0; y < together; ++y) {
         int first, heads;
         heads_of<kSide>(a, (p.x & -together) + y, &first, &heads);
-        // what CTA c has: in its last place where the row begins, else in its first
-        auto place_of = [&](int c) { return (int64_t(c) * 2 + (c == from ? 1 : 0)) * together + y; };
-        // 4 values of kItems heads to a thread, their loads under way together
+        // Where the parts are: a CTA's last place if the row begins in it, else its
+        // first.  32 bits hold the whole workspace.
+        const int first_at = (2 * base + (base == from ? 1 : 0)) * together + y;
+        const int next_at = 2 * base * together + y, step_at = 2 * step * together;
+        // 4 values of kItems heads to a thread, the loads of a batch of parts under way together
         constexpr int kThreads = kDecodeWarps * 32;
         constexpr int kItems = C::kHeads * kQuads > kThreads ? C::kHeads * kQuads / kThreads : 1;
-        constexpr int kBatch = D == 128 ? 16 / kItems : 8;
         static_assert(kItems * kThreads >= C::kHeads * kQuads, "one round for all heads");
         Joined sum[kItems];
-        for (int x0 = 0; x0 < count; x0 += kBatch) {
+        auto add_batch = [&](auto size, int x0) {
+          constexpr int kBatch = decltype(size)::value;
           float2 ml[kItems][kBatch];
           float4 v[kItems][kBatch];
 #pragma unroll
@@ -713,14 +716,22 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
               ml[z][x] = make_float2(-INFINITY, 0.f);
               v[z][x] = make_float4(0.f, 0.f, 0.f, 0.f);
               if (x0 + x < count && h < heads) {
-                const int64_t at = place_of(base + (x0 + x) * step);
-                ml[z][x] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h));
-                v[z][x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * (C::kHeads * D) + h * D + d));
+                const int at = x0 + x == 0 ? first_at : next_at + (x0 + x) * step_at;
+                ml[z][x] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (at * C::kHeads + h) * 2));
+                v[z][x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (at * C::kHeads + h) * D + d));
               }
             }
           }
 #pragma unroll
           for (int z = 0; z < kItems; ++z) sum[z].add(ml[z], v[z]);
+        };
+        // a batch costs its size, and most rows have two parts: 128 mixed requests take 1
+        // us more with batches of 16 for all, long rows 1 us with batches of 4
+        constexpr int kFew = 2, kMany = 8;
+        if (count <= kFew) {
+          add_batch(std::integral_constant<int, kFew>(), 0);
+        } else {
+          for (int x0 = 0; x0 < count; x0 += kMany) add_batch(std::integral_constant<int, kMany>(), x0);
         }
         // a group's sum takes the place of its first part, which a head's warp alone reads
         static_assert(32 % kQuads == 0, "a head's values lie in one warp");
@@ -730,10 +741,9 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
           const int i = tid + z * kThreads, h = i / kQuads, d = 4 * (i % kQuads);
           if (h >= heads) continue;
           if (grouped) {
-            const int64_t at = place_of(base);
-            __stcg(reinterpret_cast<float4*>(a.part_o + at * (C::kHeads * D) + h * D + d), sum[z].o);
+            __stcg(reinterpret_cast<float4*>(a.part_o + (first_at * C::kHeads + h) * D + d), sum[z].o);
             if (d == 0)
-              __stcg(reinterpret_cast<float2*>(a.part_ml + at * (C::kHeads * 2) + 2 * h),
+              __stcg(reinterpret_cast<float2*>(a.part_ml + (first_at * C::kHeads + h) * 2),
                      make_float2(sum[z].top, sum[z].sum));
           } else {
             store_joined(a, D, p.b, first + h, d, sum[z]);
