@@ -204,11 +204,15 @@ __device__ __forceinline__ void store_out4(const DecodeArgs& a, int D, int b, in
   *reinterpret_cast<uint2*>(a.out + (int64_t(b) * a.H + head) * D + d) =
       make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
-__device__ __forceinline__ float lse_of(float m, float l) { return m * kLn2 + logf(l); }
+// Log-sum-exp from a maximum of scores in units of log2 e and a sum of at least 1 (or
+// 0 where there is no row): the hardware's log2 is off by 2^-22 of itself at most.
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + __log2f(l)) * kLn2; }
+// 1 / l for such a sum, 2 units in the last place, where 0 stays 0.
+__device__ __forceinline__ float inverse_of(float l) { return l == 0.f ? 0.f : __fdividef(1.f, l); }
 
 // A finished row: normalised, with its log-sum-exp.
 __device__ __forceinline__ void store_joined(const DecodeArgs& a, int D, int b, int head, int d, const Joined& s) {
-  const float by = s.sum == 0.f ? 0.f : 1.f / s.sum;
+  const float by = inverse_of(s.sum);
   store_out4(a, D, b, head, d, make_float4(s.o.x * by, s.o.y * by, s.o.z * by, s.o.w * by));
   if (d == 0) a.lse[int64_t(head) * a.B + b] = lse_of(s.top == -INFINITY ? 0.f : s.top, s.sum);
 }
@@ -552,7 +556,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
               sh.m[slot][head] = m[n][e];
               sh.l[slot][head] = l[n][e];
             }
-            const float by = !whole ? 1.f : l[n][e] == 0.f ? 0.f : 1.f / l[n][e];
+            const float by = whole ? inverse_of(l[n][e]) : 1.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               to[o_at<D>(head, 16 * i + g)] = o_acc[i][n][e] * by;
@@ -667,21 +671,24 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   // groups of kGroup are joined first, each by its own last: what one SM reads in a
   // row costs more than a second arrival does.
   if (open[0] < 0 && open[1] < 0) return;
-  __syncthreads();
+  int* counter = nullptr;  // where thread `place` arrives, one of `arrivals`
+  int arrivals = 0;
   if (tid < 2) {
     const int slot = tid == 0 ? open[0] : open[1];
     sh.last[tid] = 0;
     if (slot >= 0) {
       const Stretch& p = sh.part[slot];
-      const int from = deal.taker(static_cast<U>(p.u0)), to = deal.taker(static_cast<U>(p.u0) + p.n - 1);
+      const int from = tid == 1 ? cta : deal.taker(static_cast<U>(p.u0)), to = deal.taker(static_cast<U>(p.u0) + p.n - 1);
       const bool grouped = to - from + 1 > 3 * kGroup;
       const int lead = grouped ? from + (cta - from) / kGroup * kGroup : from;
       sh.from[tid] = from;
       sh.to[tid] = to;
-      sh.last[tid] = grouped ? last_of(a.counters + gridDim.x + 2 * lead + (lead == from), min(kGroup, to + 1 - lead))
-                             : last_of(a.counters + from, to - from + 1);
+      counter = grouped ? a.counters + gridDim.x + 2 * lead + (lead == from) : a.counters + from;
+      arrivals = grouped ? min(kGroup, to + 1 - lead) : to - from + 1;
     }
   }
+  __syncthreads();
+  if (counter) sh.last[tid] = last_of(counter, arrivals);
   __syncthreads();
 #pragma unroll 1
   for (int place = 0; place < 2; ++place) {
