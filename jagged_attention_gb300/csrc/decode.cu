@@ -235,13 +235,16 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   const int part = kSide ? warp & (together - 1) : 0, sub = kSide ? warp / together : warp;
   const int line = (part << sub_bits) + sub;
 
-  // ---- tiles of all requests, and where this CTA's warps begin
-  const int slab = (a.B + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
-  const int b_lo = min(a.B, tid * slab), b_hi = min(a.B, b_lo + slab);
+  // ---- units of all requests, and where this CTA's warps begin.  Up to 32 requests
+  // a warp adds up by itself, a lane for each, and waits for no other warp.
+  const bool few = a.B <= 32;
+  const int slab = few ? 1 : (a.B + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
+  const int b_lo = min(a.B, (few ? lane : tid) * slab), b_hi = min(a.B, b_lo + slab);
   U units = 0;
-  int rows = 0, most = 0;  // rows: requests that have any
+  int rows = 0, most = 0, last_len = 0;  // rows: requests that have any
   for (int b = b_lo; b < b_hi; ++b) {
-    const int n = tiles_of(length_of(a, b));
+    last_len = length_of(a, b);
+    const int n = tiles_of(last_len);
     units += n > 0 ? n + kRowUnits : 0;
     rows += n > 0;
     most = max(most, n);
@@ -255,23 +258,27 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     if (lane >= o) units_to += x, rows_to += y;
   }
   most = __reduce_max_sync(~0u, most);
-  if (lane == 31) {
-    sh.scan_units[warp] = units_to;
-    sh.scan_rows[warp] = rows_to;
-    sh.scan_most[warp] = most;
-  }
-  if (tid < 2 * kDecodeWarps) sh.part[tid].n = 0;
-  __syncthreads();
-  U total = 0;
-  int all_rows = 0;
+  if (lane < 2) sh.part[2 * line + lane].n = 0;
+  U total = __shfl_sync(~0u, units_to, 31);
+  int all_rows = __shfl_sync(~0u, rows_to, 31);
+  if (!few) {
+    if (lane == 0) {
+      sh.scan_units[warp] = total;
+      sh.scan_rows[warp] = all_rows;
+      sh.scan_most[warp] = most;
+    }
+    __syncthreads();
+    total = 0;
+    all_rows = 0;
 #pragma unroll
-  for (int w = 0; w < kDecodeWarps; ++w) {
-    const U x = static_cast<U>(sh.scan_units[w]);
-    const int y = sh.scan_rows[w];
-    if (w < warp) units_to += x, rows_to += y;
-    total += x;
-    all_rows += y;
-    most = max(most, sh.scan_most[w]);
+    for (int w = 0; w < kDecodeWarps; ++w) {
+      const U x = static_cast<U>(sh.scan_units[w]);
+      const int y = sh.scan_rows[w];
+      if (w < warp) units_to += x, rows_to += y;
+      total += x;
+      all_rows += y;
+      most = max(most, sh.scan_most[w]);
+    }
   }
   // few and short rows: a CTA for each, so that nothing is left to be joined between CTAs
   const bool apart = most <= kApartTiles / together && int64_t(all_rows) * vheads <= gridDim.x;
@@ -292,8 +299,11 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   const Deal<U> deal(total, ctas);
   const U cta_lo = cta < ctas ? deal.from(cta) : 0, cta_n = cta < ctas ? deal.from(cta + 1) - cta_lo : 0;
   auto sub_from = [&](int i) -> U { return cta_lo + (cta_n >> sub_bits) * U(i) + min(U(i), cta_n & U(subs - 1)); };
-  sh.first_unit[tid] = (units_to - units) * vheads;
-  __syncthreads();
+  const U first_unit = (units_to - units) * vheads;  // of this thread's requests
+  if (!few) {
+    sh.first_unit[tid] = first_unit;
+    __syncthreads();
+  }
 
   const U lo = sub_from(sub), hi = sub_from(sub + 1);
 
@@ -318,21 +328,28 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     };
     Cursor<U> at;  // of the tile whose rows are looked up next
     {
-      // the last thread whose requests begin at or before the share, by groups of
-      // kDecodeWarps threads and then within the group
-      auto begins = [&](int t) { return static_cast<U>(sh.first_unit[t]) <= lo; };
-      static_assert(kDecodeWarps <= 32, "a group's threads have a lane each");
-      const int t0 = (__popc(__ballot_sync(~0u, begins(lane * kDecodeWarps))) - 1) * kDecodeWarps;
-      const int t = t0 + __popc(__ballot_sync(~0u, lane < kDecodeWarps && begins(t0 + (lane % kDecodeWarps)))) - 1;
-      U r = lo - static_cast<U>(sh.first_unit[t]);
+      // the last thread whose requests begin at or before the share
       at.u = lo;
-      at.b = t * slab;
-      for (;; ++at.b) {
-        at.len = length_of(a, at.b);
+      U r;
+      if (few) {
+        at.b = __popc(__ballot_sync(~0u, first_unit <= lo)) - 1;  // lanes behind the last begin at the end
+        r = lo - __shfl_sync(~0u, first_unit, at.b);
+        at.len = __shfl_sync(~0u, last_len, at.b);
         at.n = tiles_of(at.len);
-        const U all = units_of(at.n) * vheads;
-        if (r < all || at.b + 1 >= a.B) break;
-        r -= all;
+      } else {
+        // by groups of kDecodeWarps threads and then within the group
+        auto begins = [&](int t) { return static_cast<U>(sh.first_unit[t]) <= lo; };
+        static_assert(kDecodeWarps <= 32, "a group's threads have a lane each");
+        const int t0 = (__popc(__ballot_sync(~0u, begins(lane * kDecodeWarps))) - 1) * kDecodeWarps;
+        const int t = t0 + __popc(__ballot_sync(~0u, lane < kDecodeWarps && begins(t0 + (lane % kDecodeWarps)))) - 1;
+        r = lo - static_cast<U>(sh.first_unit[t]);
+        for (at.b = t * slab;; ++at.b) {
+          at.len = length_of(a, at.b);
+          at.n = tiles_of(at.len);
+          const U all = units_of(at.n) * vheads;
+          if (r < all || at.b + 1 >= a.B) break;
+          r -= all;
+        }
       }
       const U per = units_of(at.n);
       at.vh = static_cast<int>(r / per);
