@@ -33,9 +33,9 @@
 // each of 2: 225 us, one part after the other 340 us).
 //
 // Measured (GB300, 6.67 TB/s copied): 96 requests up to 32768 rows, 64 heads on 8,
-// 7.2 GB in 1049 us, 6.8 TB/s; 128 requests of 0 to 8192 rows, 443 MB in 74 us,
-// 6.0 TB/s; one request of 131072, 268 MB in 50 us, 5.3 TB/s; one of 300 rows in
-// 6.4 us.  What is left of the middle sizes is about 2.5 us until the first rows
+// 7.2 GB in 1047 us, 6.9 TB/s; 128 requests of 0 to 8192 rows, 443 MB in 73 us,
+// 6.1 TB/s; one request of 131072, 268 MB in 48.5 us, 5.5 TB/s; one of 300 rows in
+// 6.2 us.  What is left of the middle sizes is about 2.5 us until the first rows
 // arrive (lengths, table, rows: three dependent trips to memory), 3 to 6 us of
 // joining, and SMs whose memory is 7% slower than others'.  128 KB of K and V in
 // the stages of 8 warps measured best: with 192 KB the full cache took 1126 us for
@@ -76,8 +76,8 @@ constexpr int kRowUnits = 2;
 // no difference).
 constexpr int kGroup = 8;
 
-// Few rows of at most this many tiles get a CTA each (4 rows of 300: 6.4 us, spread
-// over more CTAs and joined 7.8).
+// Few rows of at most this many tiles get a CTA each (4 rows of 300: 6.2 us, spread
+// over more CTAs and joined 1.3 us more).
 constexpr int kApartTiles = 12;
 
 // Where a warp stands: tile t of n of (request b, key/value head and pass vh), unit
