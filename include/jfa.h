@@ -570,8 +570,9 @@ int jfa_pager_status(jfa_pager_t pager, void* stream, int* raw);
  *                 counts whether the request was left as it was or not)
  * A page belongs to one request: giving back a page that another table shares
  * puts it onto the free list twice.  `rows` is the capacity of slots and
- * positions.  Distinct outputs must not overlap.  A call whose lens_out and n_free_out are not its lens and n_free
- * can be repeated with the same result.
+ * positions.  Outputs overlap neither one another nor an input, but as said.  A
+ * call whose lens_out and n_free_out are not its lens and n_free can be repeated
+ * with the same result.
  */
 int jfa_paged_tables(jfa_pager_t pager, int B, const int32_t* lens, const int32_t* delta,
                      int32_t* lens_out, int32_t* table, int64_t table_row, int32_t* free_list,
@@ -579,7 +580,7 @@ int jfa_paged_tables(jfa_pager_t pager, int B, const int32_t* lens, const int32_
                      int32_t* positions, int32_t* row_offsets, void* stream);
 
 /* Distances, in elements, of a cache's pages, rows and heads (D contiguous),
- * the same for K and V; multiples of 8. */
+ * the same for K and V; multiples of 8, rows less than 2^32 apart. */
 typedef struct jfa_pages {
   void* k;
   void* v;
