@@ -658,3 +658,14 @@ def test_tables_down_to_the_last_page():
     assert want[-1] == paged_ref.NO_PAGES and want[1] == 0
     want = _run_tables([4, 4, 4], [1, -4, 5], table, free, 2, 6, 4, 6)  # served from what the second gives back
     assert want[-1] == 0 and want[1] == 0
+
+
+@pytest.mark.parametrize("B", [2, 31, 32, 33, 63, 255, 256, 257, 512, 513])
+@pytest.mark.parametrize("most", [50, 700])
+def test_decode_request_counts(B, most):
+    """As many requests as lanes, threads and slabs of threads have, and one more or less; some empty at either end."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, most, B)
+    lens[rng.random(B) < 0.3] = 0
+    lens[-1] = 0 if B % 2 else most
+    _check_decode(*_decode_case(lens, 2, 1, 64, 16, False, B))
