@@ -700,12 +700,14 @@ class Pager:
 
 def _pages(pager: Pager, k_pages, v_pages) -> _Pages:
     shape, dev = (pager.num_pages, pager.page_size, pager.Hkv, pager.D), pager.index
-    st = k_pages.stride()
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != shape or st[3] != 1:
+    st, sv = k_pages.stride(), v_pages.stride()
+    for name, t, one in (("k_pages", k_pages, st[-1]), ("v_pages", v_pages, sv[-1])):
+        if t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != shape or one != 1:
             _refuse(name, t, torch.bfloat16, dev, shape)
-    if st != v_pages.stride():
-        raise ValueError(f"k_pages and v_pages must have the same strides, got {st} and {v_pages.stride()}")
+    if 1 in shape:  # the stride of a dimension of one says nothing
+        st, sv = (tuple(0 if n == 1 else x for n, x in zip(shape, y)) for y in (st, sv))
+    if st != sv:
+        raise ValueError(f"k_pages and v_pages must have the same strides, got {st} and {sv}")
     return _Pages(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2])
 
 

@@ -137,13 +137,13 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
       const int pair = !kInterleaved ? lo + i : i < 4 ? lo / 2 + i : hi / 2 + i - 4;
       const int pos = a.positions[row * a.pos_row + a.turns.axis[pair] * a.pos_axis];
       const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * a.turns.turn[pair];
-      const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
+      const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
       sincospif(half_turns, &s[i], &c[i]);
       if (a.inverse) s[i] = -s[i];
     }
   }
 
-  int64_t page_at = -1;  // offset of this row's slot for scattered jobs, in rows and pages
+  bool placed = false;  // whether the row has a slot, and where
   int page = 0, in_page = 0;
   if (a.slots) {
     const int slot = a.slots[row];
@@ -152,7 +152,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
     } else if (slot >= 0) {
       page = a.div.quot(slot);
       in_page = slot - page * a.div.d;
-      page_at = 0;
+      placed = true;
     }
   }
 
@@ -164,7 +164,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
     const RowJob& job = a.job[j];
     const int h0 = max(first - before, 0), h1 = min(last - before, job.heads);
     before += job.heads;
-    if (job.scatter && page_at < 0) continue;
+    if (job.scatter && !placed) continue;
     const int64_t in = row * job.in_row;
     const int64_t out = job.scatter ? page * job.out_page + in_page * job.out_row : row * job.out_row;
     if (job.f32)

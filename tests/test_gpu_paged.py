@@ -669,3 +669,22 @@ def test_decode_request_counts(B, most):
     lens[rng.random(B) < 0.3] = 0
     lens[-1] = 0 if B % 2 else most
     _check_decode(*_decode_case(lens, 2, 1, 64, 16, False, B))
+
+
+def test_strides_of_dimensions_of_one_do_not_matter():
+    """A single head or page, and pages of one row, whose strides torch leaves at anything."""
+    def odd(x, dim, stride):
+        st = list(x.stride())
+        st[dim] = stride
+        return x.as_strided(x.shape, st)
+
+    for page, hk, lens, dim in ((1, 2, [30, 5], 1), (16, 1, [30, 5], 2), (64, 2, [50], 0)):
+        pager, q, kp, vp, table, n = _decode_case(lens, 2, hk, 64, page, False, 3)
+        if dim == 0:  # one page
+            pager = jfa.Pager(max_seqs=1, max_pages=1, num_pages=1, page_size=64, H=2, Hkv=2, D=64)
+            kp, vp, table = kp[table[0].long()], vp[table[0].long()], torch.zeros_like(table)
+        want = jfa.paged_decode(pager, q, kp, vp, table, n, 0.125)
+        for a, b in ((3, 3), (3, 5), (1 << 40, 7)):
+            got = jfa.paged_decode(pager, q, odd(kp, dim, a), odd(vp, dim, b), table, n, 0.125)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        _check_decode(pager, q, odd(kp, dim, 3), odd(vp, dim, 3), table, n)
