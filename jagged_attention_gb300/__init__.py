@@ -654,9 +654,12 @@ def rotate(rotary: Rotary, positions, q, k=None, *, inverse: bool = False, q_out
 
 class Pager:
     """A jfa_pager_t: the geometry of a paged key/value cache, with its status word
-    and workspace in ``block``, which is cleared on the current stream of the
-    current device.  One pager for each stream that decodes at the same time: its
-    launches must be stream-ordered.  Keep it as long as graphs that captured them."""
+    and workspace in ``block``, which is cleared before the pager is there (created
+    within a capture: by the graph, on the capturing stream).  One pager for each
+    stream that decodes at the same time: its launches must be stream-ordered.  It may
+    be dropped while eager calls run, on whatever streams: the block's memory is not
+    given away before they are done (a stream that is not torch's own has to live as
+    long).  Keep it as long as graphs that captured its calls."""
 
     def __init__(self, *, max_seqs: int, max_pages: int, num_pages: int, page_size: int, H: int, Hkv: int,
                  D: int):
@@ -667,10 +670,14 @@ class Pager:
         self.index = self.device.index
         n = lib().jfa_pager_block_bytes(H, Hkv, D)
         self.block = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+        stream = torch.cuda.current_stream()
+        self._streams = {stream.cuda_stream}  # those that the block's memory is kept for
         h = _vp()
         _check(lib().jfa_pager_create(max_seqs, max_pages, num_pages, page_size, H, Hkv, D, self.block.data_ptr(), n,
-                                      _raw_stream(self.index), ctypes.byref(h)), "jfa_pager_create")
+                                      stream.cuda_stream, ctypes.byref(h)), "jfa_pager_create")
         self._h = h
+        if not torch.cuda.is_current_stream_capturing():
+            stream.synchronize()  # cleared for calls on any stream
 
     @property
     def handle(self):
@@ -678,10 +685,23 @@ class Pager:
             raise RuntimeError("pager already destroyed")
         return self._h
 
+    def stream(self) -> int:
+        """The handle of the current stream, which a call is about to use.  The block
+        belongs to the stream of its creation: of another the allocator is told, once
+        (a captured call's work is no eager work)."""
+        s = _raw_stream(self.index)
+        if s not in self._streams and not torch.cuda.is_current_stream_capturing():
+            self.block.record_stream(torch.cuda.current_stream(self.index))
+            self._streams.add(s)
+        return s
+
     def status(self, stream=None) -> int:
         """The status bits (PAGER_*) set since the last call, which it clears."""
+        if stream is not None:
+            with _on(stream):
+                return self.status()
         raw = ctypes.c_int()
-        rc = lib().jfa_pager_status(self.handle, _stream(stream), ctypes.byref(raw))
+        rc = lib().jfa_pager_status(self.handle, self.stream(), ctypes.byref(raw))
         if rc != 8:  # JFA_ERR_PAGES: the bits say what
             _check(rc, "jfa_pager_status")
         return raw.value
@@ -740,7 +760,7 @@ def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: i
         _ints("free_list", free_list, pager.num_pages, dev), _ints("n_free", n_free, 1, dev),
         _ints("n_free_out", n_free_out, 1, dev), rows, _ints("slots", slots, rows, dev),
         _ints("positions", positions, rows, dev), _ints("row_offsets", row_offsets, B + 1, dev),
-        _raw_stream(dev))
+        pager.stream())
     if rc:
         _check(rc, "jfa_paged_tables")
     return lens_out, n_free_out, slots, positions, row_offsets
@@ -775,7 +795,7 @@ def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary 
     rc = (_lib or lib()).jfa_paged_append(
         pager.handle, rows, *_rows("k", k, shape, torch.bfloat16, dev), *_rows("v", v, shape, torch.bfloat16, dev),
         _ints("slots", slots, rows, dev), ctypes.byref(_pages(pager, k_pages, v_pages)), rot, *pos, *q_args,
-        _raw_stream(dev))
+        pager.stream())
     if rc:
         _check(rc, "jfa_paged_append")
     return q_out
@@ -803,7 +823,7 @@ def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *
         raise ValueError("out must be contiguous")
     rc = (_lib or lib()).jfa_paged_decode(
         pager.handle, B, *q_at, ctypes.byref(_pages(pager, k_pages, v_pages)), *_table(table, pager, B, dev),
-        _ints("lens", lens, B, dev), float(scale), out_at, lse.data_ptr(), _raw_stream(dev))
+        _ints("lens", lens, B, dev), float(scale), out_at, lse.data_ptr(), pager.stream())
     if rc:
         _check(rc, "jfa_paged_decode")
     return out, lse
