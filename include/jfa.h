@@ -612,8 +612,11 @@ int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_r
  * so too for a length outside 0 .. max_pages * page_size
  * (JFA_PAGER_BAD_LENGTH).  Rows on a page outside the cache are left out
  * (JFA_PAGER_BAD_PAGE).  Rows of a page behind lens[b] may hold anything, NaN
- * and infinities included.  Results are the same, bit for bit, from call to
- * call on the same arguments.
+ * and infinities included; an infinite value of V in a counted row makes out
+ * infinite, as any weight above 2^-126 of the largest does.  Scores, softmax
+ * statistics and sums are fp32; a weight enters the product with V as the sum
+ * of two bf16 values, 16 bits in all.  Results are the same, bit for bit, from
+ * call to call on the same arguments.
  */
 int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, const jfa_pages* pages,
                      const int32_t* table, int64_t table_row, const int32_t* lens, float scale,

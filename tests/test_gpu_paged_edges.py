@@ -1,0 +1,71 @@
+"""GPU tests of the paged-cache operators at values and sizes where they can go
+wrong, against their 64-bit plain forms."""
+import numpy as np
+import pytest
+import torch
+
+import jagged_attention_gb300 as jfa
+from tests import paged_ref
+
+pytestmark = pytest.mark.gpu
+BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    jfa.build()
+
+
+def _ints(a):
+    return torch.as_tensor(np.asarray(a), dtype=I32).cuda()
+
+
+def _draw(shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda", dtype=F32).to(BF16)
+
+
+def _case(lens, hq, hk, D, page, seed):
+    """(pager, q, k_pages, v_pages, table, lens): pages dealt out at random."""
+    lens = np.asarray(lens)
+    count = -(-lens // page)
+    width, num_pages = max(1, int(count.max())), max(1, int(count.sum()))
+    order, at = np.random.default_rng(seed).permutation(num_pages), 0
+    table = np.full((len(lens), width), -1)
+    for b, n in enumerate(count):
+        table[b, :n] = order[at:at + n]
+        at += n
+    kp, vp = _draw((num_pages, page, hk, D), seed), _draw((num_pages, page, hk, D), seed + 1)
+    pager = jfa.Pager(max_seqs=len(lens), max_pages=width, num_pages=num_pages, page_size=page, H=hq, Hkv=hk, D=D)
+    return pager, _draw((len(lens), hq, D), seed + 2), kp, vp, _ints(table), _ints(lens)
+
+
+def _same_class(a, b):
+    """NaN, +inf and -inf in the same places."""
+    return torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(a == np.inf, b == np.inf) and \
+        torch.equal(a == -np.inf, b == -np.inf)
+
+
+@pytest.mark.parametrize("lens", [[1], [2, 0, 31], [300, 17], [9000, 40, 1]], ids=str)
+@pytest.mark.parametrize("hq,hk,D", [(1, 1, 64), (4, 2, 128), (16, 1, 128), (24, 1, 64)])
+def test_decode_infinite_values(lens, hq, hk, D):
+    """An infinite value of V among the rows of a request makes its output infinite, as
+    its weight is above 0; infinities of both signs make a NaN; all else is as before."""
+    pager, q, kp, vp, table, dl = _case(lens, hq, hk, D, 16, 3)
+    flat = vp.view(-1, hk, D)
+    for b, n in enumerate(lens):
+        for t in range(0, n, 7):  # one value of a row each, the two signs in columns of their own
+            at = int(table[b, t // 16]) * 16 + t % 16
+            flat[at, t % hk, 2 * (t % (D // 4))] = np.inf
+            flat[at, t % hk, 1 + 2 * (t % (D // 4))] = -np.inf
+        if n > 20:
+            for t, sign in ((3, np.inf), (19, -np.inf)):
+                flat[int(table[b, t // 16]) * 16 + t % 16, 0, D - 3] = sign
+    out, lse = jfa.paged_decode(pager, q, kp, vp, table, dl, D ** -0.5)
+    assert pager.status() == 0
+    ref, ref_lse, off, off_lse = paged_ref.decode(q, kp, vp, table, dl, D ** -0.5)
+    o, finite = out.cpu().double(), torch.isfinite(ref)
+    assert _same_class(o, ref) and torch.isinf(ref).any() and finite.any()
+    assert ((o - ref).abs()[finite] <= off[finite]).all()
+    some = torch.isfinite(ref_lse)
+    assert ((lse.cpu().double() - ref_lse).abs()[some] <= off_lse[some]).all()
