@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kTableThreads, 1) tables_kernel(const __grid_c
   };
 
   // A warp has stretches of 32 * run rows, a lane every 32nd of them: it searches
-  // for the first one's request and walks on from there, the pages of kTogether
-  // rows under way at once.
+  // for the first one's request and from there on for the next ones' (requests
+  // without new rows may lie between), the pages of kTogether rows under way at once.
   constexpr int kTogether = 4;
   const int lane = tid & 31;
   const int run = static_cast<int>(min(int64_t(8), (a.rows + stride - 1) / stride));
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kTableThreads, 1) tables_kernel(const __grid_c
         if (k0 + k < run && r < new_rows) {
           const int row = static_cast<int>(r);
           if (b < 0) b = owner_of(row_at, 0, a.B, row);
-          while (row_at[b + 1] <= row) ++b;
+          if (row_at[b + 1] <= row) b = owner_of(row_at, b + 1, a.B, row);
           const int len = a.lens[b];
           position[k] = static_cast<int>(int64_t(len) + (row - row_at[b]));
           live[k] = served[b];

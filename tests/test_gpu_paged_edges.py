@@ -69,3 +69,57 @@ def test_decode_infinite_values(lens, hq, hk, D):
     assert ((o - ref).abs()[finite] <= off[finite]).all()
     some = torch.isfinite(ref_lse)
     assert ((lse.cpu().double() - ref_lse).abs()[some] <= off_lse[some]).all()
+
+
+def _us(call, n=10):
+    """Microseconds of a captured call, the fastest of five replays of n."""
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            call()
+    best = np.inf
+    for _ in range(6):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        graph.replay()
+        end.record()
+        end.synchronize()
+        best = min(best, start.elapsed_time(end) * 1e3 / n)
+    return best
+
+
+@pytest.mark.parametrize("B,each", [(256, 1500), (5000, 3000), (16384, 1500), (16384, 100000)])
+def test_tables_of_a_few_growing_requests_among_many(B, each):
+    """New rows in the first, a middle and the last request alone: right, and in no more
+    than three times the time that they take next to one another."""
+    page = 16
+    width = -(-each // page)
+    num_pages = 3 * width + 1
+    pager = jfa.Pager(max_seqs=B, max_pages=width, num_pages=num_pages, page_size=page, H=1, Hkv=1, D=64)
+    free = np.random.default_rng(B).permutation(num_pages)
+    lens, n_free = _ints(np.zeros(B)), _ints([num_pages])
+    rows, table = 3 * each + 5, torch.full((B, width), -1, dtype=I32, device="cuda")
+    took = {}
+    for where in ((0, B // 2, B - 1), (0, 1, 2)):
+        delta = np.zeros(B, int)
+        delta[list(where)] = each
+        args, dfree = (lens, _ints(delta), table), _ints(free)
+        slots, positions, offsets = (torch.empty(n, dtype=I32, device="cuda") for n in (rows, rows, B + 1))
+
+        def call():
+            return jfa.paged_tables(pager, *args, dfree, n_free, rows=rows, slots=slots, positions=positions,
+                                    row_offsets=offsets)
+
+        got, new = call(), np.arange(each)
+        assert pager.status() == 0
+        pages = [free[num_pages - 1 - i * width - np.arange(width)] for i in range(3)]
+        want = np.concatenate([p[new // page] * page + new % page for p in pages] + [np.full(5, -1)])
+        assert np.array_equal(got[2].cpu().numpy(), want)
+        assert np.array_equal(got[3].cpu().numpy(), np.concatenate([new, new, new, np.zeros(5, int)]))
+        assert np.array_equal(got[4].cpu().numpy(), np.concatenate([[0], np.cumsum(delta)]))
+        assert np.array_equal(got[0].cpu().numpy(), delta) and int(got[1]) == num_pages - 3 * width
+        for b, p in zip(where, pages):
+            assert np.array_equal(table[b].cpu().numpy(), p)
+        took[where[1]] = _us(call)
+    assert took[B // 2] <= 3 * took[1], took
