@@ -332,11 +332,17 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       c.t = 0;
       if (++c.vh < vheads) return;
       c.vh = 0;
-      do {
-        ++c.b;
-        c.len = length_of(a, c.b);
-        c.n = tiles_of(c.len);
-      } while (c.n == 0 && c.b + 1 < a.B);
+      c.len = length_of(a, ++c.b);
+      // requests without rows: 32 lengths at a time, up to the next that has some (it
+      // is there, as the share goes on)
+      while (c.len == 0 && c.b + 1 < a.B) {
+        const int b = c.b + 1 + lane, len = b < a.B ? length_of(a, b) : 0;
+        const uint32_t some = __ballot_sync(~0u, len > 0);
+        const int to = some ? __ffs(some) - 1 : 31;
+        c.b = min(c.b + 1 + to, a.B - 1);
+        c.len = __shfl_sync(~0u, len, to);
+      }
+      c.n = tiles_of(c.len);
     };
     Cursor<U> at;  // of the tile whose rows are looked up next
     {

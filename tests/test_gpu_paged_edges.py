@@ -123,3 +123,27 @@ def test_tables_of_a_few_growing_requests_among_many(B, each):
             assert np.array_equal(table[b].cpu().numpy(), p)
         took[where[1]] = _us(call)
     assert took[B // 2] <= 3 * took[1], took
+
+
+@pytest.mark.parametrize("B,hq,hk", [(2048, 8, 2), (2048, 24, 1), (16384, 8, 2)])
+def test_decode_of_a_few_requests_among_many(B, hq, hk):
+    """Three requests with rows, far apart and next to one another: the same bits, and
+    in no more than three times the time."""
+    n, page, D, scale = 20000, 16, 128, 128 ** -0.5
+    pager, q3, kp, vp, table3, lens3 = _case([n] * 3, hq, hk, D, page, B)
+    want = jfa.paged_decode(pager, q3, kp, vp, table3, lens3, scale)
+    ref, ref_lse, off, off_lse = paged_ref.decode(q3, kp, vp, table3, lens3, scale)
+    assert ((want[0].cpu().double() - ref).abs() <= off).all()
+    assert ((want[1].cpu().double() - ref_lse).abs() <= off_lse).all()
+    big = jfa.Pager(max_seqs=B, max_pages=pager.max_pages, num_pages=pager.num_pages, page_size=page, H=hq, Hkv=hk, D=D)
+    took, q = {}, _draw((B, hq, D), 1)
+    for where in ([0, B // 2, B - 1], [0, 1, 2], [B - 3, B - 2, B - 1]):
+        table, lens = torch.full((B, pager.max_pages), -1, dtype=I32, device="cuda"), _ints(np.zeros(B))
+        table[where], lens[where], q[where] = table3, lens3, q3
+        out, lse = jfa.paged_decode(big, q, kp, vp, table, lens, scale)
+        assert big.status() == 0
+        assert torch.equal(out[where], want[0]) and torch.equal(lse[:, where], want[1])
+        none = lens == 0
+        assert not out[none].any() and (lse[:, none] == -np.inf).all()
+        took[where[1]] = _us(lambda: jfa.paged_decode(big, q, kp, vp, table, lens, scale))
+    assert took[B // 2] <= 3 * took[1], took
