@@ -186,8 +186,9 @@ cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   int64_t weight = 0;
   for (const RowJob& job : a.job) weight += int64_t(job.heads) * (job.f32 ? 2 : 1);
   const int64_t fill = int64_t(sms) * 1024 / kRowThreads;
-  const int split = static_cast<int>(
-      std::min<int64_t>(a.heads, std::max({fill / blocks, (weight + kHeadsAThread - 1) / kHeadsAThread, int64_t(1)})));
+  constexpr int64_t kMostSplit = 65535;  // the grid's second dimension
+  const int split = static_cast<int>(std::min<int64_t>(
+      {a.heads, kMostSplit, std::max({fill / blocks, (weight + kHeadsAThread - 1) / kHeadsAThread, int64_t(1)})}));
   const int per = (a.heads + split - 1) / split;
   const dim3 grid(static_cast<unsigned>(blocks), (a.heads + per - 1) / per);
   return launch_overlapped(a.turns.interleaved ? rows_kernel<true> : rows_kernel<false>, grid, kRowThreads, 0, stream, a,
