@@ -595,7 +595,8 @@ typedef struct jfa_pages {
  * jfa_paged_tables makes them.  With a rotary handle the keys are rotated on
  * the way by positions (as for jfa_rotate), and so is q [rows, H, D] into
  * q_out when q is given (every row, also those without a slot; q_out may be q
- * with the same row distance).  rotary == NULL: positions, q and q_out are NULL.
+ * with the same row distance).  Otherwise nothing that is written -- the slots'
+ * rows, q_out -- overlaps an input.  rotary == NULL: positions, q and q_out are NULL.
  */
 int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_row, const void* v,
                      int64_t v_row, const int32_t* slots, const jfa_pages* pages,
@@ -608,7 +609,8 @@ int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_r
  *     out[b][h] = softmax(scale * q[b][h] K_b^T) V_b,  lse[h][b] = logsumexp
  * over rows 0 .. lens[b]-1 of request b.  q bf16 [B, H, D] (rows q_row
  * elements apart, heads contiguous), out bf16 [B, H, D], lse fp32 [H, B]
- * (natural log, scale included, as jfa_fwd's).  lens[b] = 0: out 0, lse -inf;
+ * (natural log, scale included, as jfa_fwd's); outputs overlap no input (an out
+ * that overlaps q is JFA_ERR_INVALID_ARG).  lens[b] = 0: out 0, lse -inf;
  * so too for a length outside 0 .. max_pages * page_size
  * (JFA_PAGER_BAD_LENGTH).  Rows on a page outside the cache are left out
  * (JFA_PAGER_BAD_PAGE).  Rows of a page behind lens[b] may hold anything, NaN

@@ -804,7 +804,8 @@ def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary 
 def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *, out=None, lse=None,
                  stream=None):
     """O (bf16 [B, H, D]) and LSE (fp32 [H, B]) of one new token per request over
-    its cached rows, through jfa_paged_decode.  q [B, H, D]; rows may lie apart."""
+    its cached rows, through jfa_paged_decode.  q [B, H, D]; rows may lie apart.
+    out may not be q."""
     if stream is not None:
         with _on(stream):
             return paged_decode(pager, q, k_pages, v_pages, table, lens, scale, out=out, lse=lse)

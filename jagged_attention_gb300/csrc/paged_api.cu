@@ -93,6 +93,14 @@ int check_rows(const void* p, int64_t row, int heads, int D, bool f32) {
   return JFA_OK;
 }
 
+// Whether p and q overlap nowhere: `rows` rows of n bf16 values each, p's one behind
+// the other and q's q_row >= n values apart.
+bool apart(const void* p, const void* q, int64_t rows, int64_t n, int64_t q_row) {
+  using Wide = unsigned __int128;
+  const Wide at = reinterpret_cast<uintptr_t>(p), from = reinterpret_cast<uintptr_t>(q);
+  return at + 2 * Wide(rows) * n <= from || from + 2 * (Wide(rows - 1) * q_row + n) <= at;
+}
+
 int check_pages(const jfa_pages* g) {
   if (!g || !g->k || !g->v || g->page < 0 || g->row < 0 || g->head < 0) return JFA_ERR_INVALID_ARG;
   if (!aligned(g->k, 16) || !aligned(g->v, 16) || g->page % 8 || g->row % 8 || g->head % 8)
@@ -345,6 +353,8 @@ int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, con
   if (int rc = check_pages(pages)) return rc;
   if (pager->div.d > 1 && pages->row > UINT32_MAX) return JFA_ERR_UNSUPPORTED;
   if (!aligned(out, 16) || !aligned(lse, 16) || !aligned(table, 4) || !aligned(lens, 4)) return JFA_ERR_ALIGNMENT;
+  // a row of out may be written while another CTA still reads its query
+  if (!apart(out, q, B, int64_t(pager->H) * pager->D, q_row)) return JFA_ERR_INVALID_ARG;
   if (int rc = check_device(pager)) return rc;
   jfa::DecodeArgs a{};
   a.B = B;

@@ -147,3 +147,23 @@ def test_decode_of_a_few_requests_among_many(B, hq, hk):
         assert not out[none].any() and (lse[:, none] == -np.inf).all()
         took[where[1]] = _us(lambda: jfa.paged_decode(big, q, kp, vp, table, lens, scale))
     assert took[B // 2] <= 3 * took[1], took
+
+
+def test_decode_refuses_an_output_over_its_queries():
+    """q in place, by a part of it, and by the gaps between strided rows; next to it is fine."""
+    pager, q, kp, vp, table, lens = _case([40, 300, 7], 4, 2, 64, 16, 5)
+    want = jfa.paged_decode(pager, q, kp, vp, table, lens, 0.1)
+    buf = torch.zeros((9, 4, 64), dtype=BF16, device="cuda")
+    buf[3:6] = q
+    was = buf.clone()
+    for at in (3, 1, 2, 4, 5):
+        with pytest.raises(jfa.JfaError) as e:
+            jfa.paged_decode(pager, buf[3:6], kp, vp, table, lens, 0.1, out=buf[at:at + 3])
+        assert e.value.code == 1
+    wide = torch.zeros((3, 9, 4, 64), dtype=BF16, device="cuda")
+    with pytest.raises(jfa.JfaError):
+        jfa.paged_decode(pager, wide[:, 2], kp, vp, table, lens, 0.1, out=wide[0, 4:7])
+    assert torch.equal(buf, was)
+    for at in (0, 6):
+        out, lse = jfa.paged_decode(pager, buf[3:6], kp, vp, table, lens, 0.1, out=buf[at:at + 3])
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
