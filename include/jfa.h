@@ -607,7 +607,9 @@ int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_r
 /*
  * Attention of one new token per request over its cache:
  *     out[b][h] = softmax(scale * q[b][h] K_b^T) V_b,  lse[h][b] = logsumexp
- * over rows 0 .. lens[b]-1 of request b.  q bf16 [B, H, D] (rows q_row
+ * over rows 0 .. lens[b]-1 of request b.  scale is below 2^127 in magnitude (else
+ * JFA_ERR_INVALID_ARG), and so are scores: one of -2^127 or less may count as
+ * -infinity.  q bf16 [B, H, D] (rows q_row
  * elements apart, heads contiguous), out bf16 [B, H, D], lse fp32 [H, B]
  * (natural log, scale included, as jfa_fwd's); outputs overlap no input (an out
  * that overlaps q is JFA_ERR_INVALID_ARG).  lens[b] = 0: out 0, lse -inf;

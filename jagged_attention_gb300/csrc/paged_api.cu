@@ -347,7 +347,8 @@ int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_r
 int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, const jfa_pages* pages,
                      const int32_t* table, int64_t table_row, const int32_t* lens, float scale,
                      void* out, float* lse, void* stream) {
-  if (!pager || B < 1 || B > pager->max_seqs || !std::isfinite(scale)) return JFA_ERR_INVALID_ARG;
+  if (!pager || B < 1 || B > pager->max_seqs) return JFA_ERR_INVALID_ARG;
+  if (!(std::fabs(scale) < 0x1p127f)) return JFA_ERR_INVALID_ARG;  // times log2 e it is finite; NaN too
   if (!table || !lens || !out || !lse || table_row < pager->max_pages) return JFA_ERR_INVALID_ARG;
   if (int rc = check_rows(q, q_row, pager->H, pager->D, false)) return rc;
   if (int rc = check_pages(pages)) return rc;

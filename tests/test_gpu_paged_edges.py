@@ -167,3 +167,17 @@ def test_decode_refuses_an_output_over_its_queries():
     for at in (0, 6):
         out, lse = jfa.paged_decode(pager, buf[3:6], kp, vp, table, lens, 0.1, out=buf[at:at + 3])
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_decode_with_the_largest_scales():
+    """Scales from 2^127 on, which times log2 e may be infinite, are refused; below they count."""
+    pager, q, kp, vp, table, lens = _case([40, 1], 2, 1, 64, 16, 6)
+    for scale in (2.0 ** 127, -3.4e38, 3e38, float("inf"), float("nan")):
+        with pytest.raises(jfa.JfaError) as e:
+            jfa.paged_decode(pager, q, kp, vp, table, lens, scale)
+        assert e.value.code == 1
+    zero = torch.zeros_like(q)  # all scores 0, whatever the scale
+    want = jfa.paged_decode(pager, zero, kp, vp, table, lens, 1.0)
+    for scale in (1.7e38, -1.7e38, 1e-45, 0.0):
+        got = jfa.paged_decode(pager, zero, kp, vp, table, lens, scale)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
