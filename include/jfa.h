@@ -519,7 +519,8 @@ int jfa_rotate(jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row, i
  * request, page or row is left out as each call says, and a bit is set in the
  * status word (jfa_pager_status).
  *
- *   max_seqs    requests of one call, at most 16384
+ *   max_seqs    requests of one call, at most 16384; a call of tables or decode has
+ *               at least one (B = 0 is JFA_ERR_INVALID_ARG; no rows are fine)
  *   max_pages   columns of the table; (max_pages + 1) * page_size < 2^31
  *   num_pages   pages of the cache; (num_pages + 1) * page_size < 2^31
  *   page_size   rows of a page, any number >= 1

@@ -734,7 +734,7 @@ def _pages(pager: Pager, k_pages, v_pages) -> _Pages:
 def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: int, lens_out=None,
                  n_free_out=None, slots=None, positions=None, row_offsets=None, stream=None):
     """Lengths, block table, free list, slots and positions of a step through
-    jfa_paged_tables: request b goes from lens[b] to lens[b] + delta[b] rows.
+    jfa_paged_tables: request b of at least one goes from lens[b] to lens[b] + delta[b] rows.
     table [B, max_pages] and free_list [num_pages] are updated in place; lens and
     n_free too where lens_out and n_free_out are given as them.  Returns
     (lens_out, n_free_out, slots, positions, row_offsets)."""
@@ -804,7 +804,7 @@ def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary 
 def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *, out=None, lse=None,
                  stream=None):
     """O (bf16 [B, H, D]) and LSE (fp32 [H, B]) of one new token per request over
-    its cached rows, through jfa_paged_decode.  q [B, H, D]; rows may lie apart.
+    its cached rows, through jfa_paged_decode.  q [B, H, D], B at least 1; rows may lie apart.
     out may not be q."""
     if stream is not None:
         with _on(stream):

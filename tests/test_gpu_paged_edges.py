@@ -181,3 +181,18 @@ def test_decode_with_the_largest_scales():
     for scale in (1.7e38, -1.7e38, 1e-45, 0.0):
         got = jfa.paged_decode(pager, zero, kp, vp, table, lens, scale)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_step_without_requests_is_refused_and_one_without_rows_is_not():
+    pager, q, kp, vp, table, lens = _case([40, 1], 2, 1, 64, 16, 6)
+    free = _ints(np.arange(pager.num_pages))
+    with pytest.raises(jfa.JfaError) as e:
+        jfa.paged_decode(pager, q[:0], kp, vp, table[:0], lens[:0], 0.1)
+    assert e.value.code == 1
+    with pytest.raises(jfa.JfaError) as e:
+        jfa.paged_tables(pager, lens[:0], lens[:0], table[:0], free, _ints([0]), rows=4)
+    assert e.value.code == 1
+    got = jfa.paged_tables(pager, lens, torch.zeros_like(lens), table, free, _ints([0]), rows=0)
+    assert torch.equal(got[0], lens) and got[4].tolist() == [0, 0, 0] and got[2].numel() == 0
+    assert jfa.paged_append(pager, kp[0, :0], vp[0, :0], lens[:0], kp, vp) is None
+    assert pager.status() == 0
