@@ -196,3 +196,69 @@ def test_a_step_without_requests_is_refused_and_one_without_rows_is_not():
     assert torch.equal(got[0], lens) and got[4].tolist() == [0, 0, 0] and got[2].numel() == 0
     assert jfa.paged_append(pager, kp[0, :0], vp[0, :0], lens[:0], kp, vp) is None
     assert pager.status() == 0
+
+
+def _check(case, scale):
+    """One call against the 64-bit form, within its bounds; twice, with the same bits."""
+    pager, q, kp, vp, table, lens = case
+    out, lse = jfa.paged_decode(pager, q, kp, vp, table, lens, scale)
+    again = jfa.paged_decode(pager, q, kp, vp, table, lens, scale)
+    assert pager.status() == 0 and torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    ref, ref_lse, off, off_lse = paged_ref.decode(q, kp, vp, table, lens, scale)
+    assert ((out.cpu().double() - ref).abs() <= off).all()
+    l, some = lse.cpu().double(), torch.isfinite(ref_lse)
+    assert torch.equal(torch.isfinite(l), some) and ((l - ref_lse).abs()[some] <= off_lse[some]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,hq,hk", [
+    ([180, 33, 64, 1, 0, 192], 17, 1), ([180, 33, 64, 1, 0, 192], 34, 2), ([1, 96, 0, 17, 32], 40, 1),
+    ([1, 30, 0, 17, 32], 100, 1), ([1, 30, 0, 17, 32], 130, 1), ([7], 300, 1), ([32] * 20, 260, 2)])
+def test_decode_short_rows_with_parts_side_by_side(D, lens, hq, hk):
+    """A CTA for each row, whose query heads several warps hold, also in two and three passes."""
+    _check(_case(lens, hq, hk, D, 16, hq), D ** -0.5)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq", [130, 300])
+def test_decode_rows_of_many_parts_in_passes(D, hq):
+    """Parts joined in groups first, of more query heads than one pass takes."""
+    _check(_case([20000, 0, 7000, 9001], hq, 1, D, 24, hq), D ** -0.5)
+
+
+@pytest.mark.parametrize("B,hq,hk", [(33, 130, 1), (257, 40, 1), (257, 34, 2), (513, 17, 1)])
+@pytest.mark.parametrize("most", [60, 400])
+def test_decode_many_requests_with_parts_side_by_side(B, hq, hk, most):
+    """More requests than a warp has lanes, and than a CTA has threads, some of them empty."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(1, most, B)
+    lens[rng.random(B) < 0.2] = 0
+    _check(_case(lens, hq, hk, 64, 16, B), 0.125)
+
+
+@pytest.mark.parametrize("hq,hk,D", [(1, 1, 64), (8, 2, 128), (20, 1, 64)])
+def test_decode_lse_of_rows_of_one_tile(hq, hk, D):
+    """Log-sum-exp sums the weights in fp32.  q and k are small whole numbers, so that
+    scores are exact but for the scale: of up to 32 rows in one tile, with S the largest
+    |score|, in steps of 2^-24: a score times scale log2 e is off by three roundings, 3 S,
+    less the maximum by one of at most 2 S; its exponential by 4 (ex2.approx: 2^-22), the
+    sum of n by n; log2 by 4 (of itself, or absolute below 2), the maximum added to it and
+    the factor ln 2 by three roundings of the result."""
+    B = 400
+    lens = np.random.default_rng(1).integers(1, 33, B)
+    lens[:120] = np.arange(120) % 6 + 1
+    pager, q, kp, vp, table, dl = _case(lens, hq, hk, D, 16, 4)
+    q.copy_((q.float() * 1.5).round())
+    kp.copy_((kp.float() * 1.5).round())
+    scale = 2.0 ** -4
+    _, lse = jfa.paged_decode(pager, q, kp, vp, table, dl, scale)
+    worst = 0.0
+    for b in range(B):
+        n, t = int(lens[b]), torch.arange(int(lens[b]), device="cuda")
+        k = kp[table[b, t // 16].long(), t % 16].double().repeat_interleave(hq // hk, 1)  # [n, hq, D]
+        s = scale * torch.einsum("hd,thd->ht", q[b].double(), k)
+        ref = torch.logsumexp(s, 1)
+        log2 = (ref - s.amax(1)).clamp(min=0) / np.log(2)
+        steps = 5 * s.abs().amax(1) + 4 + n + 4 * log2.clamp(min=1) * np.log(2) + 3 * ref.abs()
+        worst = max(worst, float(((lse[:, b].double() - ref).abs() / (1.01 * steps * 2.0 ** -24)).max()))
+    assert worst <= 1, worst
