@@ -685,7 +685,7 @@ class Pager:
             raise RuntimeError("pager already destroyed")
         return self._h
 
-    def stream(self) -> int:
+    def _launch_stream(self) -> int:
         """The handle of the current stream, which a call is about to use.  The block
         belongs to the stream of its creation: of another the allocator is told, once
         (a captured call's work is no eager work)."""
@@ -701,7 +701,7 @@ class Pager:
             with _on(stream):
                 return self.status()
         raw = ctypes.c_int()
-        rc = lib().jfa_pager_status(self.handle, self.stream(), ctypes.byref(raw))
+        rc = lib().jfa_pager_status(self.handle, self._launch_stream(), ctypes.byref(raw))
         if rc != 8:  # JFA_ERR_PAGES: the bits say what
             _check(rc, "jfa_pager_status")
         return raw.value
@@ -760,7 +760,7 @@ def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: i
         _ints("free_list", free_list, pager.num_pages, dev), _ints("n_free", n_free, 1, dev),
         _ints("n_free_out", n_free_out, 1, dev), rows, _ints("slots", slots, rows, dev),
         _ints("positions", positions, rows, dev), _ints("row_offsets", row_offsets, B + 1, dev),
-        pager.stream())
+        pager._launch_stream())
     if rc:
         _check(rc, "jfa_paged_tables")
     return lens_out, n_free_out, slots, positions, row_offsets
@@ -795,7 +795,7 @@ def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary 
     rc = (_lib or lib()).jfa_paged_append(
         pager.handle, rows, *_rows("k", k, shape, torch.bfloat16, dev), *_rows("v", v, shape, torch.bfloat16, dev),
         _ints("slots", slots, rows, dev), ctypes.byref(_pages(pager, k_pages, v_pages)), rot, *pos, *q_args,
-        pager.stream())
+        pager._launch_stream())
     if rc:
         _check(rc, "jfa_paged_append")
     return q_out
@@ -824,7 +824,7 @@ def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *
         raise ValueError("out must be contiguous")
     rc = (_lib or lib()).jfa_paged_decode(
         pager.handle, B, *q_at, ctypes.byref(_pages(pager, k_pages, v_pages)), *_table(table, pager, B, dev),
-        _ints("lens", lens, B, dev), float(scale), out_at, lse.data_ptr(), pager.stream())
+        _ints("lens", lens, B, dev), float(scale), out_at, lse.data_ptr(), pager._launch_stream())
     if rc:
         _check(rc, "jfa_paged_decode")
     return out, lse
