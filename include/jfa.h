@@ -458,8 +458,9 @@ int jfa_simple_release(void);
  * Angles are kept as turns in 64-bit fixed point: inv_freq[i] / (2 pi) is
  * rounded once to a multiple of 2^-64 when the handle is made, its product
  * with an int32 position wraps at whole turns without loss, and its upper 32
- * bits go to the sine and cosine in fp32.  A far position's angle is so exact
- * to 2^-31 turns.  inv_freq must be finite and below 2^31 in magnitude.
+ * bits, rounded to fp32, go to the sine and cosine.  The angle that they see is
+ * so off by about 2^-26 turns (9.5e-8) at most, at any position.  inv_freq must be
+ * finite and below 2^31 in magnitude.
  *
  * The handle holds no device memory: it serves every device and stream, and
  * any number of calls at once.

@@ -34,7 +34,7 @@
 // each of 2: 225 us, one part after the other 340 us).
 //
 // Measured (GB300, 6.67 TB/s copied): 96 requests up to 32768 rows, 64 heads on 8,
-// 7.2 GB in 1047 us, 6.9 TB/s; 128 requests of 0 to 8192 rows, 443 MB in 73 us,
+// 7.2 GB in 1016 to 1048 us (by GPU), 6.9 TB/s; 128 requests of 0 to 8192 rows, 443 MB in 73 us,
 // 6.1 TB/s; one request of 131072, 268 MB in 48.5 us, 5.5 TB/s; one of 300 rows in
 // 6.2 us.  What is left of the middle sizes is about 2.5 us until the first rows
 // arrive (lengths, table, rows: three dependent trips to memory), 3 to 6 us of
@@ -77,8 +77,10 @@ constexpr int kRowUnits = 2;
 // no difference).
 constexpr int kGroup = 8;
 
-// Few rows of at most this many tiles get a CTA each (4 rows of 300: 6.2 us, spread
-// over more CTAs and joined 1.3 us more).
+// Few rows of at most this many tiles get a CTA each.  4 rows of 8 heads on 2: of 250
+// 5.5 us, spread over more CTAs and joined 6.9; of 380 (12 tiles) 6.4 and 7.0; of 440
+// 6.6 and 6.9, of 512 6.8 and 7.1, so that up to 16 it would gain as well, of 540 7.6
+// and 7.3.
 constexpr int kApartTiles = 12;
 
 // Where a warp stands: tile t of n of (request b, key/value head and pass vh), unit
@@ -217,7 +219,8 @@ __device__ __forceinline__ void store_out4(const DecodeArgs& a, int D, int b, in
       make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
 // Log-sum-exp from a maximum of scores in units of log2 e and a sum of at least 1 (or
-// 0 where there is no row): the hardware's log2 is off by 2^-22 of itself at most.
+// 0 where there is no row): the hardware's log2 is off by 2^-22 up to a sum of 2, an
+// error of 1.7e-7 in the result, and by two units in its last place above.
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + __log2f(l)) * kLn2; }
 // 1 / l for such a sum, 2 units in the last place, where 0 stays 0.
 __device__ __forceinline__ float inverse_of(float l) { return l == 0.f ? 0.f : __fdividef(1.f, l); }

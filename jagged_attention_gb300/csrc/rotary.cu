@@ -5,7 +5,8 @@
 // f = inv_freq / (2 pi) in units of 2^-64, position * f in 64-bit integers is
 // the angle in turns modulo 1, exact but for the one rounding of f; its upper
 // 32 bits as a signed number over 2^31 are the angle over pi in [-1, 1), which
-// sincospif takes.  No range reduction in floating point, no 64-bit floats.
+// sincospif takes, rounded to fp32: by 2^-26 turns at most, half a step of fp32
+// below 1.  No range reduction in floating point, no 64-bit floats.
 //
 // Split: a thread has 16 values of a head -- two runs of 8, lo and hi, that hold
 // both members of its 8 pairs -- and walks over the heads of its row, so that
@@ -14,10 +15,10 @@
 // holds four whole pairs.  Either way the D/16 threads of a row read whole
 // 128-byte lines per run.
 //
-// Measured (GB300, 6.67 TB/s copied): 786432 rows of 8 heads, 3.2 GB in 471 us,
-// 6.85 TB/s; 17311 rows of 4 fp32 and 4 bf16 heads, 106 MB in 18.8 us, 5.7 TB/s;
-// 32769 rows into pages, 268 MB in 43.6 us, 6.1 TB/s; 256 rows of 4 heads in 2.8
-// us, 64 rows of 48 in 3.2 us, of which 2 us are the launch.
+// Measured (GB300, 6.67 TB/s copied): 786432 rows of 8 heads, 3.2 GB in 472 us,
+// 6.84 TB/s; 17311 rows of 4 fp32 and 4 bf16 heads, 106 MB in 18.9 us, 5.6 TB/s;
+// 32769 rows into pages, 268 MB in 43.7 us, 6.1 TB/s; 256 rows of 4 heads in 2.7
+// us, 64 rows of 48 in 3.1 us, of which 2 us are the launch.
 #include <algorithm>
 
 #include "paged.h"
@@ -30,8 +31,11 @@ namespace {
 // in each: 64 KB an SM.  786432 rows of 8 heads take 470 us so; with four heads at
 // once in half the threads 514 us, with fewer registers (1280 threads) 529 us.
 constexpr int kRowThreads = 64, kBlocksPerSm = 16;
-// 8980 rows of 32 fp32 and 8 bf16 heads: 57 us, all heads in a thread 65; 17311 rows
-// of 4 and 4: 18.8 us, 8 in a thread 19.7.
+// Heads of a thread, on the average, an fp32 one counting double.  8980 rows of 32
+// fp32 and 8 bf16 heads: 57 us, all heads in a thread 66; 60000 rows of 8 and 8: 115
+// us and 120; 20000 rows of 16 bf16 heads: 31.4 and 34.3.  Between 6 and 16 it makes
+// 3% on the average, and 12% at most: 20000 rows of 12 heads 24.1 us with 10, 26.7
+// with 12.
 constexpr int kHeadsAThread = 12;
 
 // 8 values as they lie in memory.
@@ -180,9 +184,10 @@ cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   if (a.rows == 0 || a.heads == 0) return cudaSuccess;
   const int64_t per_block = kRowThreads / (a.D / 16);
   const int64_t blocks = (a.rows + per_block - 1) / per_block;
-  // A thread walks over at most kHeadsAThread heads of its row (fp32 ones count
-  // double): more even out less over the SMs, fewer form their sines too often.  Of
-  // rows too few to fill the SMs (1024 threads each) the heads are dealt to more.
+  // As many threads to a row as its heads' weight over kHeadsAThread: more heads in a
+  // thread even out less over the SMs, fewer form their sines too often.  Of rows too
+  // few to fill the SMs (1024 threads each) the heads are dealt to more.  They are
+  // dealt by their number alone: of fp32 and bf16 heads some threads have more weight.
   int64_t weight = 0;
   for (const RowJob& job : a.job) weight += int64_t(job.heads) * (job.f32 ? 2 : 1);
   const int64_t fill = int64_t(sms) * 1024 / kRowThreads;
