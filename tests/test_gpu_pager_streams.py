@@ -24,9 +24,9 @@ def _cache():
 
 
 def _busy(stream):
-    """Some 0.1 s of work on the stream."""
+    """Some 0.3 s of work on the stream."""
     with torch.cuda.stream(stream):
-        torch.cuda._sleep(200_000_000)
+        torch.cuda._sleep(600_000_000)
 
 
 def _decode(pager, kp, vp, table, lens, q, stream):
