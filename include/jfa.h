@@ -535,6 +535,30 @@ typedef struct jfa_pager* jfa_pager_t;
 size_t jfa_pager_block_bytes(int H, int Hkv, int D); /* on the current device; 0: unsupported */
 int jfa_pager_create(int max_seqs, int max_pages, int64_t num_pages, int page_size, int H, int Hkv,
                      int D, void* block, size_t block_bytes, void* stream, jfa_pager_t* out);
+/*
+ * A cache in fewer bits.  A pager made with one of these flags serves pages that hold
+ * codes, with scale bytes beside them (jfa_pages and jfa_scales below); flags 0 is
+ * jfa_pager_create.  The block is the same.
+ *
+ * JFA_PAGER_8BIT: a row of a head is D e4m3 codes and one byte c, its values are
+ *     code * 2^(c - 127),
+ * where 2^(c - 127) is the least power of two that takes the row's largest magnitude to
+ * at most 448, c from 79 to 175.
+ * JFA_PAGER_4BIT: D / 2 bytes of e2m1 codes, the first value of two in the lower nibble,
+ * and a scale byte for each 16 values: bits 14 to 7 of a positive fp16 number s, the
+ * block's largest magnitude / 6 rounded to nearest even (5 exponent and 3 mantissa
+ * bits, multiples of 2^-17), at most 10240; its values are code * s.
+ * In both a value over its scale is rounded to the nearest code, halves to the even one,
+ * and to the largest code where it is larger (8 bits: a row of 448 * 2^48 and more, 4
+ * bits: the largest of a block whose scale was rounded down, and what is beyond 61440).
+ * Where a value is NaN or infinite the scale byte is 255, and the row of the head (4
+ * bits: the block) reads as NaN.  With 8 bits other bytes outside 79 .. 175 count as the
+ * nearest of them.  What a code stands for is exact in bf16.
+ */
+#define JFA_PAGER_8BIT 1u
+#define JFA_PAGER_4BIT 2u
+int jfa_pager_create_ex(int max_seqs, int max_pages, int64_t num_pages, int page_size, int H, int Hkv,
+                        int D, unsigned flags, void* block, size_t block_bytes, void* stream, jfa_pager_t* out);
 /* Release a pager (its block stays the caller's). */
 int jfa_pager_destroy(jfa_pager_t pager);
 /* Read the status word (synchronises `stream`), then clear it: JFA_ERR_PAGES
@@ -589,6 +613,16 @@ typedef struct jfa_pages {
   int64_t page, row, head;
 } jfa_pages;
 
+/* Scale bytes of a cache of 8 or 4 bits: a row of a head has n = 1 (8 bits) or D / 16 (4
+ * bits) of them, one behind the other; distances in bytes, multiples of n as the
+ * addresses are.  The pages' distances count bytes then, multiples of 16.  Scales of a
+ * head's rows that lie one behind the other (row = n) are read in the fewest pieces. */
+typedef struct jfa_scales {
+  void* k;
+  void* v;
+  int64_t page, row, head;
+} jfa_scales;
+
 /*
  * Write new rows into the cache: k, v bf16 [rows, Hkv, D] (rows k_row / v_row
  * elements apart, heads contiguous) go to slots[r]; rows with a negative slot
@@ -605,6 +639,33 @@ int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_r
                      jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row,
                      int64_t pos_axis, const void* q, int64_t q_row, void* q_out, int64_t q_out_row,
                      void* stream);
+
+/* jfa_paged_append for a pager of any number of bits: scales is NULL for 16 (then it is
+ * jfa_paged_append), else the keys and values are quantised as they are written.  Keys
+ * that are rotated are rounded to bf16 before.  jfa_paged_append itself refuses a pager
+ * of 8 or 4 bits (JFA_ERR_INVALID_ARG). */
+int jfa_paged_append_ex(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_row, const void* v,
+                        int64_t v_row, const int32_t* slots, const jfa_pages* pages,
+                        const jfa_scales* scales, jfa_rotary_t rotary, const int32_t* positions,
+                        int64_t pos_row, int64_t pos_axis, const void* q, int64_t q_row, void* q_out,
+                        int64_t q_out_row, void* stream);
+
+/*
+ * Read cached rows back, from a cache of any number of bits (scales NULL for 16), into
+ * packed bf16 rows as jfa_fwd takes them: for offsets[b] <= r < offsets[b + 1], row r of
+ * k_out and v_out [rows, Hkv, D] (rows k_row / v_row elements apart, heads contiguous)
+ * is cached row starts[b] + r - offsets[b] of request b; starts NULL: all 0.
+ *   starts    int32 [B] or NULL
+ *   offsets   int32 [B + 1], not decreasing, as jfa_paged_tables' row_offsets
+ * Rows before offsets[0] and from offsets[B] on stay as they were.  A row whose place
+ * is negative or beyond the table is zeros (JFA_PAGER_BAD_LENGTH), so is one on a page
+ * outside the cache (JFA_PAGER_BAD_PAGE); offsets beyond `rows` set JFA_PAGER_BAD_LENGTH
+ * too.  Outputs overlap neither each other nor an input.
+ */
+int jfa_paged_gather(jfa_pager_t pager, int B, const jfa_pages* pages, const jfa_scales* scales,
+                     const int32_t* table, int64_t table_row, const int32_t* starts,
+                     const int32_t* offsets, int64_t rows, void* k_out, int64_t k_row, void* v_out,
+                     int64_t v_row, void* stream);
 
 /*
  * Attention of one new token per request over its cache:
@@ -627,6 +688,14 @@ int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_r
 int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, const jfa_pages* pages,
                      const int32_t* table, int64_t table_row, const int32_t* lens, float scale,
                      void* out, float* lse, void* stream);
+
+/* jfa_paged_decode for a pager of any number of bits: scales is NULL for 16 (then it is
+ * jfa_paged_decode).  With 8 or 4 bits the attention is that over the values the codes
+ * stand for.  A NaN key of a counted row makes its heads' out and lse NaN, a NaN value
+ * its place of out. */
+int jfa_paged_decode_ex(jfa_pager_t pager, int B, const void* q, int64_t q_row, const jfa_pages* pages,
+                        const jfa_scales* scales, const int32_t* table, int64_t table_row,
+                        const int32_t* lens, float scale, void* out, float* lse, void* stream);
 
 /* Human-readable text of a status code (static storage). */
 const char* jfa_status_string(int status);

@@ -20,6 +20,15 @@ Serving from a paged cache, one step:
     lens, n_free, slots, positions, offsets = paged_tables(pager, lens, delta, table, free, n_free, rows=n)
     q = paged_append(pager, k, v, slots, k_pages, v_pages, rotary=rotary, positions=positions, q=q)
     out, lse = paged_decode(pager, q, k_pages, v_pages, table, lens, scale)
+
+The same from a cache of 8 or 4 bits, and its rows read back for the forward of prompts:
+
+    pager = Pager(..., bits=4)
+    k_pages, v_pages, k_scales, v_scales = pager.pages()
+    held = dict(k_scales=k_scales, v_scales=v_scales)
+    q = paged_append(pager, k, v, slots, k_pages, v_pages, **held, rotary=rotary, positions=positions, q=q)
+    k, v = paged_gather(pager, k_pages, v_pages, table, offsets, rows=n, **held)
+    out, lse = paged_decode(pager, q, k_pages, v_pages, table, lens, scale, **held)
 """
 from __future__ import annotations
 
@@ -54,6 +63,8 @@ ROTARY_INTERLEAVED = 1  # JFA_ROTARY_INTERLEAVED
 ROTATE_INVERSE = 1  # JFA_ROTATE_INVERSE
 ROTATE_X_FP32 = 2  # JFA_ROTATE_X_FP32
 ROTATE_Y_FP32 = 4  # JFA_ROTATE_Y_FP32
+PAGER_8BIT = 1  # JFA_PAGER_8BIT
+PAGER_4BIT = 2  # JFA_PAGER_4BIT
 PAGER_NO_PAGES = 1  # JFA_PAGER_NO_PAGES
 PAGER_BAD_LENGTH = 2  # JFA_PAGER_BAD_LENGTH
 PAGER_BAD_PAGE = 4  # JFA_PAGER_BAD_PAGE
@@ -78,6 +89,11 @@ class _Pages(ctypes.Structure):
     """jfa_pages"""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page", ctypes.c_int64),
                 ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class _Scales(ctypes.Structure):
+    """jfa_scales"""
+    _fields_ = _Pages._fields_
 
 
 
@@ -144,6 +160,13 @@ def lib() -> ctypes.CDLL:
                                            _cl, _vp, _cl, _vp]
             L.jfa_paged_decode.argtypes = [_vp, _ci, _vp, _cl, _vp, _vp, _cl, _vp, ctypes.c_float, _vp, _vp,
                                            _vp]
+            L.jfa_pager_create_ex.argtypes = [_ci, _ci, _cl, _ci, _ci, _ci, _ci, _cu, _vp, ctypes.c_size_t, _vp,
+                                              ctypes.POINTER(_vp)]
+            L.jfa_paged_append_ex.argtypes = [_vp, _cl, _vp, _cl, _vp, _cl, _vp, _vp, _vp, _vp, _vp, _cl, _cl, _vp,
+                                              _cl, _vp, _cl, _vp]
+            L.jfa_paged_gather.argtypes = [_vp, _ci, _vp, _vp, _vp, _cl, _vp, _vp, _cl, _vp, _cl, _vp, _cl, _vp]
+            L.jfa_paged_decode_ex.argtypes = [_vp, _ci, _vp, _cl, _vp, _vp, _vp, _cl, _vp, ctypes.c_float, _vp,
+                                              _vp, _vp]
             L.jfa_status_string.argtypes = [ctypes.c_int]
             L.jfa_status_string.restype = ctypes.c_char_p
             for name in ("jfa_plan_create", "jfa_plan_create_ex", "jfa_plan_destroy", "jfa_plan_tiles", "jfa_build_tiles",
@@ -153,7 +176,9 @@ def lib() -> ctypes.CDLL:
                          "jfa_plan_selftest", "jfa_plan_forward_pairs", "jfa_plan_claims",
                          "jfa_plan_forward_form", "jfa_rotary_turns", "jfa_rotary_create",
                          "jfa_rotary_destroy", "jfa_rotate", "jfa_pager_create", "jfa_pager_destroy",
-                         "jfa_pager_status", "jfa_paged_tables", "jfa_paged_append", "jfa_paged_decode"):
+                         "jfa_pager_status", "jfa_paged_tables", "jfa_paged_append", "jfa_paged_decode",
+                         "jfa_pager_create_ex", "jfa_paged_append_ex", "jfa_paged_gather",
+                         "jfa_paged_decode_ex"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -659,11 +684,18 @@ class Pager:
     stream that decodes at the same time: its launches must be stream-ordered.  It may
     be dropped while eager calls run, on whatever streams: the block's memory is not
     given away before they are done (a stream that is not torch's own has to live as
-    long).  Keep it as long as graphs that captured its calls."""
+    long).  Keep it as long as graphs that captured its calls.
+
+    ``bits`` 8 or 4: pages hold uint8 codes [num_pages, page_size, Hkv, D * bits / 8],
+    and uint8 scales [num_pages, page_size, Hkv, n] go with them, n = 1 or D / 16 (see
+    jfa_pager_create_ex; ``pages()`` makes them)."""
 
     def __init__(self, *, max_seqs: int, max_pages: int, num_pages: int, page_size: int, H: int, Hkv: int,
-                 D: int):
+                 D: int, bits: int = 16):
         self._h = None
+        if bits not in (16, 8, 4):
+            raise ValueError(f"bits must be 16, 8 or 4, got {bits}")
+        self.bits, self.scale_bytes = bits, 1 if bits == 8 else D // 16
         self.max_seqs, self.max_pages, self.num_pages, self.page_size = max_seqs, max_pages, num_pages, page_size
         self.H, self.Hkv, self.D = H, Hkv, D
         self.device = torch.device("cuda", torch.cuda.current_device())
@@ -673,8 +705,10 @@ class Pager:
         stream = torch.cuda.current_stream()
         self._streams = {stream.cuda_stream}  # those that the block's memory is kept for
         h = _vp()
-        _check(lib().jfa_pager_create(max_seqs, max_pages, num_pages, page_size, H, Hkv, D, self.block.data_ptr(), n,
-                                      stream.cuda_stream, ctypes.byref(h)), "jfa_pager_create")
+        flags = {16: 0, 8: PAGER_8BIT, 4: PAGER_4BIT}[bits]
+        _check(lib().jfa_pager_create_ex(max_seqs, max_pages, num_pages, page_size, H, Hkv, D, flags,
+                                         self.block.data_ptr(), n, stream.cuda_stream, ctypes.byref(h)),
+               "jfa_pager_create_ex")
         self._h = h
         if not torch.cuda.is_current_stream_capturing():
             stream.synchronize()  # cleared for calls on any stream
@@ -684,6 +718,19 @@ class Pager:
         if self._h is None:
             raise RuntimeError("pager already destroyed")
         return self._h
+
+    def pages(self):
+        """A cache for this pager, all zeros: (k_pages, v_pages, k_scales, v_scales), scales
+        None with 16 bits.  The scales of a head's rows lie one behind the other."""
+        shape = (self.num_pages, self.page_size, self.Hkv)
+        if self.bits == 16:
+            k, v = (torch.zeros((*shape, self.D), dtype=torch.bfloat16, device=self.device) for _ in range(2))
+            return k, v, None, None
+        k, v = (torch.zeros((*shape, self.D * self.bits // 8), dtype=torch.uint8, device=self.device)
+                for _ in range(2))
+        k_scales, v_scales = (torch.zeros((shape[0], shape[2], shape[1], self.scale_bytes), dtype=torch.uint8,
+                                          device=self.device).transpose(1, 2) for _ in range(2))
+        return k, v, k_scales, v_scales
 
     def _launch_stream(self) -> int:
         """The handle of the current stream, which a call is about to use.  The block
@@ -719,16 +766,32 @@ class Pager:
 
 
 def _pages(pager: Pager, k_pages, v_pages) -> _Pages:
-    shape, dev = (pager.num_pages, pager.page_size, pager.Hkv, pager.D), pager.index
-    st, sv = k_pages.stride(), v_pages.stride()
-    for name, t, one in (("k_pages", k_pages, st[-1]), ("v_pages", v_pages, sv[-1])):
-        if t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != shape or one != 1:
-            _refuse(name, t, torch.bfloat16, dev, shape)
+    n, dtype = (pager.D, torch.bfloat16) if pager.bits == 16 else (pager.D * pager.bits // 8, torch.uint8)
+    return _Pages(*_pair("pages", k_pages, v_pages, (pager.num_pages, pager.page_size, pager.Hkv, n), dtype,
+                         pager.index))
+
+
+def _pair(what: str, k, v, shape, dtype, dev: int) -> tuple:
+    """(address of k, of v, distances of pages, rows and heads) of two tensors alike."""
+    st, sv = k.stride(), v.stride()
+    for name, t, s in (("k_" + what, k, st), ("v_" + what, v, sv)):
+        if t.dtype != dtype or t.get_device() != dev or t.shape != shape or s[-1] != 1 and shape[-1] > 1:
+            _refuse(name, t, dtype, dev, shape)
     if 1 in shape:  # the stride of a dimension of one says nothing
         st, sv = (tuple(0 if n == 1 else x for n, x in zip(shape, y)) for y in (st, sv))
     if st != sv:
-        raise ValueError(f"k_pages and v_pages must have the same strides, got {st} and {sv}")
-    return _Pages(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2])
+        raise ValueError(f"k_{what} and v_{what} must have the same strides, got {st} and {sv}")
+    return k.data_ptr(), v.data_ptr(), st[0], st[1], st[2]
+
+
+def _scales(pager: Pager, k_scales, v_scales):
+    """jfa_scales, None with 16 bits."""
+    if (k_scales is None or v_scales is None) != (pager.bits == 16) or (k_scales is None) != (v_scales is None):
+        raise ValueError(f"a cache of {pager.bits} bits {'has no' if pager.bits == 16 else 'needs'} k_scales and v_scales")
+    if k_scales is None:
+        return None
+    shape = (pager.num_pages, pager.page_size, pager.Hkv, pager.scale_bytes)
+    return ctypes.byref(_Scales(*_pair("scales", k_scales, v_scales, shape, torch.uint8, pager.index)))
 
 
 def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: int, lens_out=None,
@@ -766,15 +829,16 @@ def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: i
     return lens_out, n_free_out, slots, positions, row_offsets
 
 
-def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary | None = None,
-                 positions=None, q=None, q_out=None, stream=None):
+def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, k_scales=None, v_scales=None,
+                 rotary: Rotary | None = None, positions=None, q=None, q_out=None, stream=None):
     """New rows k, v [rows, Hkv, D] into the pages at their slots through
-    jfa_paged_append; with ``rotary``, k and q [rows, H, D] rotated by
-    ``positions`` on the way.  Returns q_out (which may be q), None without q."""
+    jfa_paged_append_ex, quantised into a cache of 8 or 4 bits; with ``rotary``, k and q
+    [rows, H, D] rotated by ``positions`` on the way.  Returns q_out (which may be q),
+    None without q."""
     if stream is not None:
         with _on(stream):
-            return paged_append(pager, k, v, slots, k_pages, v_pages, rotary=rotary, positions=positions, q=q,
-                                q_out=q_out)
+            return paged_append(pager, k, v, slots, k_pages, v_pages, k_scales=k_scales, v_scales=v_scales,
+                                rotary=rotary, positions=positions, q=q, q_out=q_out)
     dev = pager.index
     rows = k.shape[0]
     shape = (rows, pager.Hkv, pager.D)
@@ -792,23 +856,53 @@ def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, rotary: Rotary 
         q_args = (*_rows("q", q, q_shape, torch.bfloat16, dev), *_rows("q_out", q_out, q_shape, torch.bfloat16, dev))
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rc = (_lib or lib()).jfa_paged_append(
+    rc = (_lib or lib()).jfa_paged_append_ex(
         pager.handle, rows, *_rows("k", k, shape, torch.bfloat16, dev), *_rows("v", v, shape, torch.bfloat16, dev),
-        _ints("slots", slots, rows, dev), ctypes.byref(_pages(pager, k_pages, v_pages)), rot, *pos, *q_args,
-        pager._launch_stream())
+        _ints("slots", slots, rows, dev), ctypes.byref(_pages(pager, k_pages, v_pages)),
+        _scales(pager, k_scales, v_scales), rot, *pos, *q_args, pager._launch_stream())
     if rc:
-        _check(rc, "jfa_paged_append")
+        _check(rc, "jfa_paged_append_ex")
     return q_out
 
 
-def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *, out=None, lse=None,
-                 stream=None):
+def paged_gather(pager: Pager, k_pages, v_pages, table, offsets, *, rows: int, starts=None, k_scales=None,
+                 v_scales=None, k_out=None, v_out=None, stream=None):
+    """Cached rows read back into packed bf16 rows k_out, v_out [rows, Hkv, D] through
+    jfa_paged_gather: packed row r with offsets[b] <= r < offsets[b + 1] is cached row
+    starts[b] + r - offsets[b] of request b (starts None: 0).  Rows behind offsets[B] stay
+    as they were.  offsets [B + 1], starts [B], table [B, max_pages], B at least 1.  Returns
+    (k_out, v_out), which fwd takes as k and v where Hkv is its H; with grouped heads q
+    [n, H, D] goes there as q.view(n, Hkv, H // Hkv, D).transpose(1, 2).reshape(-1, Hkv, D),
+    its offsets times H // Hkv."""
+    if stream is not None:
+        with _on(stream):
+            return paged_gather(pager, k_pages, v_pages, table, offsets, rows=rows, starts=starts, k_scales=k_scales,
+                                v_scales=v_scales, k_out=k_out, v_out=v_out)
+    dev, B = pager.index, offsets.shape[0] - 1
+    shape = (rows, pager.Hkv, pager.D)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=pager.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=pager.device)
+    rc = (_lib or lib()).jfa_paged_gather(
+        pager.handle, B, ctypes.byref(_pages(pager, k_pages, v_pages)), _scales(pager, k_scales, v_scales),
+        *_table(table, pager, B, dev), None if starts is None else _ints("starts", starts, B, dev),
+        _ints("offsets", offsets, B + 1, dev), rows, *_rows("k_out", k_out, shape, torch.bfloat16, dev),
+        *_rows("v_out", v_out, shape, torch.bfloat16, dev), pager._launch_stream())
+    if rc:
+        _check(rc, "jfa_paged_gather")
+    return k_out, v_out
+
+
+def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *, k_scales=None, v_scales=None,
+                 out=None, lse=None, stream=None):
     """O (bf16 [B, H, D]) and LSE (fp32 [H, B]) of one new token per request over
-    its cached rows, through jfa_paged_decode.  q [B, H, D], B at least 1; rows may lie apart.
+    its cached rows, through jfa_paged_decode_ex.  q [B, H, D], B at least 1; rows may lie apart.
     out may not be q."""
     if stream is not None:
         with _on(stream):
-            return paged_decode(pager, q, k_pages, v_pages, table, lens, scale, out=out, lse=lse)
+            return paged_decode(pager, q, k_pages, v_pages, table, lens, scale, k_scales=k_scales, v_scales=v_scales,
+                                out=out, lse=lse)
     dev, H, D = pager.index, pager.H, pager.D
     B = q.shape[0]
     shape = (B, H, D)
@@ -822,9 +916,10 @@ def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *
     out_at, out_row = _rows("out", out, shape, torch.bfloat16, dev)
     if out_row != H * D:
         raise ValueError("out must be contiguous")
-    rc = (_lib or lib()).jfa_paged_decode(
-        pager.handle, B, *q_at, ctypes.byref(_pages(pager, k_pages, v_pages)), *_table(table, pager, B, dev),
-        _ints("lens", lens, B, dev), float(scale), out_at, lse.data_ptr(), pager._launch_stream())
+    rc = (_lib or lib()).jfa_paged_decode_ex(
+        pager.handle, B, *q_at, ctypes.byref(_pages(pager, k_pages, v_pages)), _scales(pager, k_scales, v_scales),
+        *_table(table, pager, B, dev), _ints("lens", lens, B, dev), float(scale), out_at, lse.data_ptr(),
+        pager._launch_stream())
     if rc:
-        _check(rc, "jfa_paged_decode")
+        _check(rc, "jfa_paged_decode_ex")
     return out, lse

@@ -84,6 +84,8 @@ struct RowJob {
   int64_t out_page, out_head;  // out_page: scattered rows only
   int heads;
   bool f32, scatter, rotate;
+  uint8_t* scales;  // of rows scattered as codes, whose `out` and distances count bytes
+  int64_t scales_page, scales_row, scales_head;
 };
 
 struct RowsArgs {
@@ -98,9 +100,32 @@ struct RowsArgs {
   int64_t num_slots;
   PageDiv div;
   int* status;
+  int bits;  // of scattered rows: 16, or 8 or 4 as codes (coded.cuh)
   Turns turns;
 };
 cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream);
+
+// Where the scale bytes of a cache of 8 or 4 bits are, and their distances in bytes.
+struct Scales {
+  uint8_t *k, *v;
+  int64_t page, row, head;
+};
+
+struct GatherArgs {
+  int B, Hkv, D, bits;
+  int max_pages;
+  int64_t num_pages, rows;
+  PageDiv div;
+  const unsigned char *k, *v;  // pages, their distances in bytes
+  int64_t page, row, head;
+  Scales scales;
+  const int32_t *table, *starts, *offsets;  // starts may be null: 0
+  int64_t table_row;
+  uint16_t *k_out, *v_out;
+  int64_t k_row, v_row;  // elements from row to row
+  int* status;
+};
+cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream);
 
 struct TablesArgs {
   int B, max_pages;
@@ -123,8 +148,10 @@ struct DecodeArgs {
   PageDiv div;
   const uint16_t* q;
   int64_t q_row;
-  const uint16_t *k, *v;
+  const uint16_t *k, *v;   // or codes, whose distances count bytes
   int64_t page, row, head;
+  int bits;                // 16, or 8 or 4
+  Scales scales;
   const int32_t *table, *lens;
   int64_t table_row;
   float scale;
@@ -148,5 +175,6 @@ struct DecodeSpace {
 };
 DecodeSpace decode_space(int D, const QueryParts& parts, int sms);
 cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_decode_coded(const DecodeArgs& a, int sms, cudaStream_t stream);  // 8 or 4 bits
 
 }  // namespace jfa

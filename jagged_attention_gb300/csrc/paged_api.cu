@@ -16,7 +16,7 @@ struct jfa_rotary {
 };
 
 struct jfa_pager {
-  int max_seqs, max_pages, H, Hkv, D, device, sms;
+  int max_seqs, max_pages, H, Hkv, D, bits, device, sms;
   jfa::QueryParts parts;
   int64_t num_pages;
   jfa::PageDiv div;
@@ -108,6 +108,23 @@ int check_pages(const jfa_pages* g) {
   return JFA_OK;
 }
 
+// Pages and scales of a cache of `bits` bits.  Codes are copied 16 bytes at a time,
+// scale bytes a row's head at a time.
+int check_cache(const jfa_pager* p, const jfa_pages* g, const jfa_scales* s) {
+  if ((p->bits < 16) != (s != nullptr)) return JFA_ERR_INVALID_ARG;
+  if (int rc = check_pages(g)) return rc;
+  if (p->bits == 16) return JFA_OK;
+  if (!s->k || !s->v || s->page < 0 || s->row < 0 || s->head < 0) return JFA_ERR_INVALID_ARG;
+  if (g->page % 16 || g->row % 16 || g->head % 16) return JFA_ERR_ALIGNMENT;
+  const int n = p->bits == 8 ? 1 : p->D / 16;
+  if (!aligned(s->k, n) || !aligned(s->v, n) || s->page % n || s->row % n || s->head % n) return JFA_ERR_ALIGNMENT;
+  return JFA_OK;
+}
+jfa::Scales scales_of(const jfa_scales* s) {
+  if (!s) return {};
+  return {static_cast<uint8_t*>(s->k), static_cast<uint8_t*>(s->v), s->page, s->row, s->head};
+}
+
 // A pager's block: status word, counters, then what split rows leave.
 struct Block {
   size_t counters, part_ml, part_o, bytes;
@@ -131,7 +148,7 @@ int check_heads(int H, int Hkv, int D) {
 
 jfa::RowJob dense_job(const void* in, int64_t in_row, void* out, int64_t out_row, int heads, int D,
                       bool f32, bool rotate) {
-  return {in, out, in_row, out_row, 0, D, heads, f32, false, rotate};
+  return {in, out, in_row, out_row, 0, D, heads, f32, false, rotate, nullptr, 0, 0, 0};
 }
 
 // rows of one launch: the grid's first dimension holds 2^31 - 1 blocks of at least 8 rows
@@ -204,6 +221,7 @@ int jfa_rotate(jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row, i
   a.pos_row = pos_row;
   a.pos_axis = pos_axis;
   a.inverse = flags & JFA_ROTATE_INVERSE;
+  a.bits = 16;
   a.turns = rotary->turns;
   return jfa::launch_rows(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
@@ -216,8 +234,14 @@ size_t jfa_pager_block_bytes(int H, int Hkv, int D) {
 
 int jfa_pager_create(int max_seqs, int max_pages, int64_t num_pages, int page_size, int H, int Hkv,
                      int D, void* block, size_t block_bytes, void* stream, jfa_pager_t* out) {
+  return jfa_pager_create_ex(max_seqs, max_pages, num_pages, page_size, H, Hkv, D, 0, block, block_bytes, stream, out);
+}
+
+int jfa_pager_create_ex(int max_seqs, int max_pages, int64_t num_pages, int page_size, int H, int Hkv,
+                        int D, unsigned flags, void* block, size_t block_bytes, void* stream, jfa_pager_t* out) {
   if (!out) return JFA_ERR_INVALID_ARG;
   *out = nullptr;
+  if (flags != 0 && flags != JFA_PAGER_8BIT && flags != JFA_PAGER_4BIT) return JFA_ERR_INVALID_ARG;
   if (max_seqs < 1 || max_pages < 1 || num_pages < 1 || page_size < 1) return JFA_ERR_INVALID_ARG;
   if (int rc = check_heads(H, Hkv, D)) return rc;
   if (max_seqs > JFA_PAGER_MAX_SEQS || num_pages > INT_MAX ||
@@ -238,6 +262,7 @@ int jfa_pager_create(int max_seqs, int max_pages, int64_t num_pages, int page_si
   p->H = H;
   p->Hkv = Hkv;
   p->D = D;
+  p->bits = flags == JFA_PAGER_8BIT ? 8 : flags == JFA_PAGER_4BIT ? 4 : 16;
   p->device = dev;
   p->sms = sms;
   p->parts = k.parts;
@@ -311,6 +336,15 @@ int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_r
                      jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row,
                      int64_t pos_axis, const void* q, int64_t q_row, void* q_out, int64_t q_out_row,
                      void* stream) {
+  return jfa_paged_append_ex(pager, rows, k, k_row, v, v_row, slots, pages, nullptr, rotary, positions, pos_row,
+                             pos_axis, q, q_row, q_out, q_out_row, stream);
+}
+
+int jfa_paged_append_ex(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_row, const void* v,
+                        int64_t v_row, const int32_t* slots, const jfa_pages* pages,
+                        const jfa_scales* scales, jfa_rotary_t rotary, const int32_t* positions,
+                        int64_t pos_row, int64_t pos_axis, const void* q, int64_t q_row, void* q_out,
+                        int64_t q_out_row, void* stream) {
   if (!pager || rows < 0 || rows >= kMaxRows || pos_row < 0 || pos_axis < 0) return JFA_ERR_INVALID_ARG;
   if (!rotary && (positions || q || q_out)) return JFA_ERR_INVALID_ARG;
   if (rotary && rotary->D != pager->D) return JFA_ERR_INVALID_ARG;
@@ -320,15 +354,19 @@ int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_r
   const int D = pager->D;
   if (int rc = check_rows(k, k_row, pager->Hkv, D, false)) return rc;
   if (int rc = check_rows(v, v_row, pager->Hkv, D, false)) return rc;
-  if (int rc = check_pages(pages)) return rc;
+  if (int rc = check_cache(pager, pages, scales)) return rc;
   if (q) {
     if (int rc = check_rows(q, q_row, pager->H, D, false)) return rc;
     if (int rc = check_rows(q_out, q_out_row, pager->H, D, false)) return rc;
   }
   if (int rc = check_device(pager)) return rc;
   jfa::RowsArgs a{};
-  a.job[0] = {k, pages->k, k_row, pages->row, pages->page, pages->head, pager->Hkv, false, true, rotary != nullptr};
-  a.job[1] = {v, pages->v, v_row, pages->row, pages->page, pages->head, pager->Hkv, false, true, false};
+  const jfa::Scales n = scales_of(scales);
+  a.job[0] = {k, pages->k, k_row, pages->row, pages->page, pages->head, pager->Hkv, false, true, rotary != nullptr,
+              n.k, n.page, n.row, n.head};
+  a.job[1] = {v, pages->v, v_row, pages->row, pages->page, pages->head, pager->Hkv, false, true, false,
+              n.v, n.page, n.row, n.head};
+  a.bits = pager->bits;
   if (q) a.job[2] = dense_job(q, q_row, q_out, q_out_row, pager->H, D, false, true);
   a.heads = 2 * pager->Hkv + (q ? pager->H : 0);
   a.D = D;
@@ -347,12 +385,18 @@ int jfa_paged_append(jfa_pager_t pager, int64_t rows, const void* k, int64_t k_r
 int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, const jfa_pages* pages,
                      const int32_t* table, int64_t table_row, const int32_t* lens, float scale,
                      void* out, float* lse, void* stream) {
+  return jfa_paged_decode_ex(pager, B, q, q_row, pages, nullptr, table, table_row, lens, scale, out, lse, stream);
+}
+
+int jfa_paged_decode_ex(jfa_pager_t pager, int B, const void* q, int64_t q_row, const jfa_pages* pages,
+                        const jfa_scales* scales, const int32_t* table, int64_t table_row,
+                        const int32_t* lens, float scale, void* out, float* lse, void* stream) {
   if (!pager || B < 1 || B > pager->max_seqs) return JFA_ERR_INVALID_ARG;
   if (!(std::fabs(scale) < 0x1p127f)) return JFA_ERR_INVALID_ARG;  // times log2 e it is finite; NaN too
   if (!table || !lens || !out || !lse || table_row < pager->max_pages) return JFA_ERR_INVALID_ARG;
   if (int rc = check_rows(q, q_row, pager->H, pager->D, false)) return rc;
-  if (int rc = check_pages(pages)) return rc;
-  if (pager->div.d > 1 && pages->row > UINT32_MAX) return JFA_ERR_UNSUPPORTED;
+  if (int rc = check_cache(pager, pages, scales)) return rc;
+  if (pager->div.d > 1 && (pages->row > UINT32_MAX || (scales && scales->row > UINT32_MAX))) return JFA_ERR_UNSUPPORTED;
   if (!aligned(out, 16) || !aligned(lse, 16) || !aligned(table, 4) || !aligned(lens, 4)) return JFA_ERR_ALIGNMENT;
   // a row of out may be written while another CTA still reads its query
   if (!apart(out, q, B, int64_t(pager->H) * pager->D, q_row)) return JFA_ERR_INVALID_ARG;
@@ -377,6 +421,8 @@ int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, con
   a.page = pages->page;
   a.row = pages->row;
   a.head = pages->head;
+  a.bits = pager->bits;
+  a.scales = scales_of(scales);
   a.table = table;
   a.table_row = table_row;
   a.lens = lens;
@@ -387,7 +433,48 @@ int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, con
   a.counters = pager->d_counters;
   a.part_ml = pager->d_part_ml;
   a.part_o = pager->d_part_o;
-  return jfa::launch_decode(a, pager->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+  const auto launch = a.bits == 16 ? jfa::launch_decode : jfa::launch_decode_coded;
+  return launch(a, pager->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+}
+
+int jfa_paged_gather(jfa_pager_t pager, int B, const jfa_pages* pages, const jfa_scales* scales,
+                     const int32_t* table, int64_t table_row, const int32_t* starts,
+                     const int32_t* offsets, int64_t rows, void* k_out, int64_t k_row, void* v_out,
+                     int64_t v_row, void* stream) {
+  if (!pager || B < 1 || B > pager->max_seqs || rows < 0 || rows > INT_MAX) return JFA_ERR_INVALID_ARG;
+  if (rows == 0) return JFA_OK;
+  if (!table || !offsets || table_row < pager->max_pages) return JFA_ERR_INVALID_ARG;
+  if (!aligned(table, 4) || !aligned(offsets, 4) || !aligned(starts, 4)) return JFA_ERR_ALIGNMENT;
+  if (int rc = check_cache(pager, pages, scales)) return rc;
+  if (int rc = check_rows(k_out, k_row, pager->Hkv, pager->D, false)) return rc;
+  if (int rc = check_rows(v_out, v_row, pager->Hkv, pager->D, false)) return rc;
+  if (int rc = check_device(pager)) return rc;
+  const int unit = pager->bits == 16 ? 2 : 1;  // bytes of an element of the pages
+  jfa::GatherArgs a{};
+  a.B = B;
+  a.Hkv = pager->Hkv;
+  a.D = pager->D;
+  a.bits = pager->bits;
+  a.max_pages = pager->max_pages;
+  a.num_pages = pager->num_pages;
+  a.rows = rows;
+  a.div = pager->div;
+  a.k = static_cast<const unsigned char*>(pages->k);
+  a.v = static_cast<const unsigned char*>(pages->v);
+  a.page = pages->page * unit;
+  a.row = pages->row * unit;
+  a.head = pages->head * unit;
+  a.scales = scales_of(scales);
+  a.table = table;
+  a.starts = starts;
+  a.offsets = offsets;
+  a.table_row = table_row;
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.v_out = static_cast<uint16_t*>(v_out);
+  a.k_row = k_row;
+  a.v_row = v_row;
+  a.status = pager->d_status;
+  return jfa::launch_gather(a, pager->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
 }  // extern "C"

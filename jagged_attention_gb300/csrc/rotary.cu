@@ -20,7 +20,9 @@
 // 32769 rows into pages, 268 MB in 43.7 us, 6.1 TB/s; 256 rows of 4 heads in 2.7
 // us, 64 rows of 48 in 3.1 us, of which 2 us are the launch.
 #include <algorithm>
+#include <type_traits>
 
+#include "coded.cuh"
 #include "paged.h"
 #include "sm103_ptx.cuh"
 
@@ -71,6 +73,28 @@ struct Run {
   }
 };
 
+// Two runs of 8 values turned by (c, s): both members of 8 pairs.
+template <bool kInterleaved>
+__device__ __forceinline__ void turn_runs(float (&x)[8], float (&y)[8], const float (&c)[8], const float (&s)[8]) {
+  if (kInterleaved) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float p = x[2 * e], q = x[2 * e + 1], v = y[2 * e], w = y[2 * e + 1];
+      x[2 * e] = p * c[e] - q * s[e];
+      x[2 * e + 1] = q * c[e] + p * s[e];
+      y[2 * e] = v * c[4 + e] - w * s[4 + e];
+      y[2 * e + 1] = w * c[4 + e] + v * s[4 + e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float p = x[e], q = y[e];
+      x[e] = p * c[e] - q * s[e];
+      y[e] = q * c[e] + p * s[e];
+    }
+  }
+}
+
 // Heads [h0, h1) of one row of a job; `in` and `out` are the row's offsets.
 // The loads of kAtOnce heads are under way together.
 template <bool kInterleaved, bool kF32>
@@ -93,23 +117,7 @@ __device__ __forceinline__ void walk_heads(const RowJob& job, int D, int64_t in,
         float x[8], y[8];
         a[i].unpack(x);
         b[i].unpack(y);
-        if (kInterleaved) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p = x[2 * e], q = x[2 * e + 1], v = y[2 * e], w = y[2 * e + 1];
-            x[2 * e] = p * c[e] - q * s[e];
-            x[2 * e + 1] = q * c[e] + p * s[e];
-            y[2 * e] = v * c[4 + e] - w * s[4 + e];
-            y[2 * e + 1] = w * c[4 + e] + v * s[4 + e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float p = x[e], q = y[e];
-            x[e] = p * c[e] - q * s[e];
-            y[e] = q * c[e] + p * s[e];
-          }
-        }
+        turn_runs<kInterleaved>(x, y, c, s);
         a[i].pack(x);
         b[i].pack(y);
       }
@@ -120,7 +128,62 @@ __device__ __forceinline__ void walk_heads(const RowJob& job, int D, int64_t in,
   }
 }
 
-template <bool kInterleaved>
+// As walk_heads, into codes of 8 or 4 bits: what a bf16 cache would hold, quantised.
+// The threads of a row exchange the largest magnitudes of their runs; with 4 bits a
+// scale's 16 values are two runs, r and r ^ 1, which two threads may hold.
+// scales: where those of the row's head 0 go.
+template <bool kInterleaved, int kBits>
+__device__ __forceinline__ void walk_coded(const RowJob& job, int D, int64_t in, int64_t out, uint8_t* scales, int h0,
+                                           int h1, int u, int turn_units, bool turn, const float (&c)[8],
+                                           const float (&s)[8]) {
+  const int units = D / 16, lane = threadIdx.x & 31, base = lane & -units;
+  const uint32_t mates = ((1u << units) - 1) << base;
+  const int r_lo = u < turn_units ? u : 2 * u, r_hi = u < turn_units ? u + turn_units : 2 * u + 1;
+  const int lo = 8 * r_lo, hi = 8 * r_hi;
+  // the thread with run r, and whether it is its second
+  auto holder = [&](int r) { return base + (r < turn_units ? r : r < 2 * turn_units ? r - turn_units : r / 2); };
+  auto second = [&](int r) { return r < turn_units ? false : r < 2 * turn_units ? true : (r & 1) != 0; };
+  auto* to = static_cast<unsigned char*>(job.out) + out;
+  for (int h = h0; h < h1; ++h) {
+    Run<false> a, b;
+    a.load(job.in, in + int64_t(h) * D + lo);
+    b.load(job.in, in + int64_t(h) * D + hi);
+    float x[8], y[8];
+    a.unpack(x);
+    b.unpack(y);
+    if (turn) {
+      turn_runs<kInterleaved>(x, y, c, s);
+      a.pack(x);  // rounded as in a bf16 cache
+      b.pack(y);
+      a.unpack(x);
+      b.unpack(y);
+    }
+    uint32_t top_lo = top_of(a.w[0]), top_hi = top_of(b.w[0]);
+    unsigned char* codes = to + h * job.out_head;
+    uint8_t* bytes = scales + h * job.scales_head;
+    if (kBits == 8) {
+      uint32_t top = max(top_lo, top_hi);
+      for (int o = 1; o < units; o <<= 1) top = max(top, __shfl_xor_sync(mates, top, o));
+      const int p = power_of(top);
+      *reinterpret_cast<uint2*>(codes + lo) = code8(x, p);
+      *reinterpret_cast<uint2*>(codes + hi) = code8(y, p);
+      if (u == 0) *bytes = static_cast<uint8_t>(p);
+    } else {
+      const uint32_t both = top_lo | top_hi << 16;
+      const uint32_t of_lo = __shfl_sync(mates, both, holder(r_lo ^ 1)), of_hi = __shfl_sync(mates, both, holder(r_hi ^ 1));
+      top_lo = max(top_lo, second(r_lo ^ 1) ? of_lo >> 16 : of_lo & 0xffffu);
+      top_hi = max(top_hi, second(r_hi ^ 1) ? of_hi >> 16 : of_hi & 0xffffu);
+      const int s_lo = scale_of(top_lo), s_hi = scale_of(top_hi);
+      *reinterpret_cast<uint32_t*>(codes + lo / 2) = code4(x, s_lo);
+      *reinterpret_cast<uint32_t*>(codes + hi / 2) = code4(y, s_hi);
+      if (r_lo % 2 == 0) bytes[r_lo / 2] = static_cast<uint8_t>(s_lo);
+      if (r_hi % 2 == 0) bytes[r_hi / 2] = static_cast<uint8_t>(s_hi);
+    }
+  }
+}
+
+// kBits: of scattered rows.
+template <bool kInterleaved, int kBits>
 __global__ void __launch_bounds__(kRowThreads, kBlocksPerSm)
 rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
   wait_for_launch_before();
@@ -171,7 +234,10 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
     if (job.scatter && !placed) continue;
     const int64_t in = row * job.in_row;
     const int64_t out = job.scatter ? page * job.out_page + in_page * job.out_row : row * job.out_row;
-    if (job.f32)
+    if (kBits < 16 && job.scatter)
+      walk_coded<kInterleaved, kBits>(job, a.D, in, out, job.scales + page * job.scales_page + in_page * job.scales_row, h0,
+                                      h1, u, pairs / 8, turning && job.rotate, c, s);
+    else if (job.f32)
       walk_heads<kInterleaved, true>(job, a.D, in, out, h0, h1, lo, hi, turning && job.rotate, c, s);
     else
       walk_heads<kInterleaved, false>(job, a.D, in, out, h0, h1, lo, hi, turning && job.rotate, c, s);
@@ -196,8 +262,13 @@ cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
       {a.heads, kMostSplit, std::max({fill / blocks, (weight + kHeadsAThread - 1) / kHeadsAThread, int64_t(1)})}));
   const int per = (a.heads + split - 1) / split;
   const dim3 grid(static_cast<unsigned>(blocks), (a.heads + per - 1) / per);
-  return launch_overlapped(a.turns.interleaved ? rows_kernel<true> : rows_kernel<false>, grid, kRowThreads, 0, stream, a,
-                           per);
+  auto kernel = [&](auto bits) {
+    return a.turns.interleaved ? rows_kernel<true, decltype(bits)::value> : rows_kernel<false, decltype(bits)::value>;
+  };
+  return launch_overlapped(a.bits == 8   ? kernel(std::integral_constant<int, 8>())
+                           : a.bits == 4 ? kernel(std::integral_constant<int, 4>())
+                                         : kernel(std::integral_constant<int, 16>()),
+                           grid, kRowThreads, 0, stream, a, per);
 }
 
 }  // namespace jfa
