@@ -1,6 +1,6 @@
 """Times of the operators' calls: `python perf/captured.py [NAME ...]`.
 
-For each listed case of operators.py (or those named) the microseconds of one call
+For each listed case of operators.py and more_operators.py (or those named) the microseconds of one call
 in a captured CUDA graph -- the GPU's time, with the launch over the tail of the
 call before -- and of one call among eager calls through the binding, which the
 host bounds where it is slower.  Calls go over as many states of different seeds as
@@ -16,7 +16,7 @@ sys.path.insert(0, str(Path(__file__).resolve().parent.parent))
 
 import torch  # noqa: E402
 
-from perf import operators  # noqa: E402
+from perf import more_operators, operators  # noqa: E402
 
 L2_BYTES = 129 << 20
 
@@ -35,8 +35,8 @@ def _us(run, calls: int) -> float:
     return best
 
 
-def measure(case) -> tuple[float, float]:
-    """(captured, eager) microseconds a call."""
+def measure(operators, case) -> tuple[float, float]:
+    """(captured, eager) microseconds a call of a case of that file."""
     count = max(2, min(16, 1 + 2 * L2_BYTES // max(1, operators.work(case)["bytes"])))
     states = [operators.prepare(case, seed) for seed in range(count)]
 
@@ -60,12 +60,13 @@ def measure(case) -> tuple[float, float]:
 
 
 def main(names) -> None:
-    operators.own = True
-    for case in operators.listed():
-        if not names or case["name"] in names:
-            floor = operators.work(case)["bytes"]
-            print("{:20s} captured {:8.2f} us  eager {:8.2f} us  {:10.3f} MB".format(
-                case["name"], *measure(case), floor / 1e6), flush=True)
+    for cases in (operators, more_operators):
+        cases.own = True
+        for case in cases.listed():
+            if not names or case["name"] in names:
+                floor = cases.work(case)["bytes"]
+                print("{:20s} captured {:8.2f} us  eager {:8.2f} us  {:10.3f} MB".format(
+                    case["name"], *measure(cases, case), floor / 1e6), flush=True)
 
 
 if __name__ == "__main__":
