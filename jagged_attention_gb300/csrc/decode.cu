@@ -1,4 +1,6 @@
 // decode.cu -- attention over a cache of bf16 rows, and what calls of any cache need.
+#include <algorithm>
+
 #include "decode_kernel.cuh"
 
 namespace jfa {
@@ -8,7 +10,7 @@ DecodeSpace decode_space(int D, const QueryParts& parts, int sms) {
   const int ctas = sms * kMostCtasPerSm;  // one block for any number of bits
   // a counter for the row that begins in a CTA's share, two for groups that a CTA
   // leads; two places for each CTA and part
-  const int64_t places = int64_t(ctas) * 2 * parts.together;
+  const int64_t places = int64_t(ctas) * 2 * std::max(parts.together, parts.parts == 1 ? kMostMates : 1);
   return {3 * ctas, places * heads * 2, places * heads * D};
 }
 

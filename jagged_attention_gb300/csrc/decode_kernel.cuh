@@ -164,6 +164,9 @@ __device__ __forceinline__ void cp_async_few(uint32_t dst, const void* src, bool
   const int bytes = take ? N : 0;
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -318,7 +321,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   wait_for_launch_before();
   // A CTA's share is dealt to `subs` sets of `together` warps, one for each part of
   // the query heads; a line is a warp's place with those of its part in a row.
-  const int passes = kSide ? a.passes : 1, vheads = a.Hkv * passes, together = kSide ? a.together : 1;
+  const int vheads = kSide ? a.vheads : a.Hkv, together = kSide ? a.together : 1;
   const int sub_bits = kSide ? __ffs(kDecodeWarps / together) - 1 : __builtin_ctz(kDecodeWarps), subs = 1 << sub_bits;
   const int part = kSide ? warp & (together - 1) : 0, sub = kSide ? warp / together : warp;
   const int line = (part << sub_bits) + sub;
@@ -451,12 +454,19 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     }
     if (at.t >= at.n) next_row(at);
     Cursor<U> now = at;  // of the tile computed next
+    // Offsets in the cache: of bf16 rows and in large caches bytes in 64 bits, else 32 bits
+    // that count 16 bytes of codes, a row's bytes of scales.
+    constexpr bool kWide = kBits == 16 || sizeof(U) == 8;
+    constexpr int kUnit = kWide ? 1 : 16, kScaleUnit = kWide || kBits == 8 ? 1 : D / kBlock;
+    using Off = std::conditional_t<kWide, int64_t, uint32_t>;
+    auto distance = [](int64_t bytes, int unit) { return static_cast<Off>(kWide ? bytes : bytes / unit); };
     const int32_t* table = nullptr;  // at's
-    int64_t head_off = 0, scale_off = 0;
+    int64_t head_off = 0;
+    int kv_at = 0;
     auto row_of_at = [&] {
       table = a.table + at.b * a.table_row;
-      head_off = (at.vh / passes) * a.head;
-      if constexpr (kBits < 16) scale_off = (at.vh / passes) * a.scales.head;
+      kv_at = kSide ? (at.vh * together + part) / a.parts : at.vh;
+      head_off = kv_at * a.head;
     };
     row_of_at();
 
@@ -485,7 +495,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     };
     // Its place in the cache in bytes, and which rows of the tile count; of codes the
     // scale bytes: 8 bits: that of the lane's row, 4 bits: where the row's are.
-    int64_t off[kSub], scale_at[kSub];
+    Off off[kSub], scale_at[kSub];
     uint32_t live[kSub];
     int k_power[kSub], v_power[kSub];
     auto locate = [&] {
@@ -496,9 +506,15 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         if constexpr (kBits == 16) {
           off[z] = in_cache ? (page[z] * a.page + in_page[z]) * 2 : 0;
         } else {
-          auto within = [&](int64_t row) { return static_cast<uint32_t>(place[z]) * static_cast<uint64_t>(static_cast<uint32_t>(row)); };
-          off[z] = in_cache ? page[z] * a.page + static_cast<int64_t>(within(a.row)) + head_off : 0;
-          scale_at[z] = in_cache ? page[z] * a.scales.page + static_cast<int64_t>(within(a.scales.row)) + scale_off : 0;
+          // distances of rows are below 2^32
+          auto place_of = [&](int64_t page_d, int64_t row_d, int64_t head_d, int unit) -> Off {
+            if constexpr (kWide)
+              return page[z] * page_d + static_cast<int64_t>(static_cast<uint32_t>(place[z]) * static_cast<uint64_t>(row_d)) + kv_at * head_d;
+            else
+              return page[z] * distance(page_d, unit) + place[z] * distance(row_d, unit) + kv_at * distance(head_d, unit);
+          };
+          off[z] = in_cache ? place_of(a.page, a.row, a.head, kUnit) : 0;
+          scale_at[z] = in_cache ? place_of(a.scales.page, a.scales.row, a.scales.head, kScaleUnit) : 0;
           if constexpr (kBits == 8) {
             k_power[z] = in_cache ? a.scales.k[scale_at[z]] : kLeastPower;
             v_power[z] = in_cache ? a.scales.v[scale_at[z]] : kLeastPower;
@@ -506,6 +522,12 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         }
         live[z] = __ballot_sync(~0u, in_cache);
       }
+    };
+    auto all_of = [](const uint32_t (&mask)[kSub]) {
+      uint32_t every = ~0u;
+#pragma unroll
+      for (int z = 0; z < kSub; ++z) every &= mask[z];
+      return every == ~0u;
     };
     // Rows of a tile into a stage.  bf16: 8 lanes copy 128 bytes of a row, chunk c of row
     // r to place c ^ (r % 8) of its 8.  Codes: the lanes that a row has chunks of 16 bytes.
@@ -526,21 +548,31 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         constexpr int kChunks = C::kRowBytes / 16, kRows = 32 / kChunks;
         const int row0 = lane / kChunks;
         const char* base = reinterpret_cast<const char*>(from) + (lane % kChunks) * 16;
-        const uint32_t to = chunk_at<C::kRowBytes>(row0, lane % kChunks, v);
+        const uint32_t to = stage + chunk_at<C::kRowBytes>(row0, lane % kChunks, v);
+        const uint8_t* scales = v ? a.scales.v : a.scales.k;
+        const uint32_t to_scale = stage + kTile * C::kRowBytes + lane * C::kScaleBytes;
+        auto rows_at = [&](auto all) {  // all: no row is left out
 #pragma unroll
-        for (int i = 0; i < kTile / kRows; ++i) {
-          const int z = i * kRows / 32, row = i * kRows % 32 + row0;
-          const char* src = base + __shfl_sync(~0u, off[z], row);
-          cp_async16(stage + (to ^ (swizzle_of<C::kRowBytes>(i * kRows, v) << 4)) + i * kRows * C::kRowBytes, src,
-                     (live[z] >> row) & 1, policy);
-        }
-        if constexpr (kBits == 4) {
-          const uint8_t* scales = v ? a.scales.v : a.scales.k;
+          for (int i = 0; i < kTile / kRows; ++i) {
+            const int z = i * kRows / 32, row = i * kRows % 32 + row0;
+            const char* src = base + static_cast<int64_t>(__shfl_sync(~0u, off[z], row)) * kUnit;
+            const uint32_t dst = (to ^ (swizzle_of<C::kRowBytes>(i * kRows, v) << 4)) + i * kRows * C::kRowBytes;
+            if constexpr (decltype(all)::value)
+              cp_async16(dst, src, policy);
+            else
+              cp_async16(dst, src, (live[z] >> row) & 1, policy);
+          }
+          if constexpr (kBits == 4) {
 #pragma unroll
-          for (int z = 0; z < kSub; ++z)
-            cp_async_few<C::kScaleBytes>(stage + kTile * C::kRowBytes + (32 * z + lane) * C::kScaleBytes, scales + scale_at[z],
-                                         (live[z] >> lane) & 1);
-        }
+            for (int z = 0; z < kSub; ++z)
+              cp_async_few<C::kScaleBytes>(to_scale + 32 * z * C::kScaleBytes, scales + static_cast<int64_t>(scale_at[z]) * kScaleUnit,
+                                           decltype(all)::value || (live[z] >> lane) & 1);
+          }
+        };
+        if (all_of(live))
+          rows_at(std::true_type());
+        else
+          rows_at(std::false_type());
       }
     };
 
@@ -590,12 +622,12 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     // with V are four neighbours; its places along D are the lane's own bytes of a row.
     constexpr int kGroups = kTile / 16;  // of 16 rows
     const int row_a = 4 * (g >> 1) + (g & 1);
-    float q_unit = 0.f;
+    float unit_log2 = 0.f;  // of a product of q and codes, in units of log2 e; not negative
     // first of the 4 values of D that the lane has in step ks
     auto k_first = [&](int ks) { return kBits == 4 ? D / 4 * j + 4 * ks : 16 * (j + 4 * (ks / 4)) + 4 * (ks % 4); };
-    // q as fp16, times the power of two that takes the largest of all heads to 2^14 and
-    // more, and its inverse: what 2^-39 of the largest and less loses is below the
-    // roundings of the sums.
+    // q as fp16, times the sign of the scale and the power of two that takes the largest of
+    // all heads to 2^14 and more, and its inverse: what 2^-39 of the largest and less loses
+    // is below the roundings of the sums.
     auto to_halves = [&](uint32_t (&w)[D / 16][NT][2]) -> float {
       uint32_t top = 0;
 #pragma unroll
@@ -604,7 +636,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         for (int n = 0; n < NT; ++n) top = __vmaxu2(top, top_of(w[ks][n][0], w[ks][n][1]));
       top = __reduce_max_sync(~0u, max(top & 0xffffu, top >> 16));
       const int e = max(static_cast<int>(top >> 7) - 127 - 14, -126);
-      const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const float by = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), scale_log2);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
@@ -731,7 +763,8 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o_acc[i][n][e] = 0.f;
         }
-        if constexpr (kBits < 16) q_unit = to_halves(qf);
+        // at least the smallest normal number, so that times -infinity it is that
+        if constexpr (kBits < 16) unit_log2 = fmaxf(to_halves(qf) * fabsf(scale_log2), 0x1p-126f);
       }
       cp_async_wait<1>();  // K is here, V may be on its way
       __syncwarp();
@@ -773,33 +806,42 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       }
       cp_async_commit();
 
-      // Of a row's score: the unit of its codes, what its values' power of two adds to the
+      // 8 bits, of a row's score: its unit, what its values' power of two adds to the
       // exponent, and 2 to the minus that.
-      float k_unit[kGroups][2], v_log2[kGroups][2], v_inverse[kGroups][2];
+      float unit_of[kGroups][2], v_log2[kGroups][2], v_inverse[kGroups][2];
       uint32_t nan_now[kSub] = {};
       bool nan_rows = false;
       if constexpr (kBits == 8) {
 #pragma unroll
         for (int z = 0; z < kSub; ++z) {
-          const float unit = power_value(k_power_now[z]) * q_unit;
+          const float unit = power_value(k_power_now[z]) * unit_log2;
           nan_now[z] = __ballot_sync(~0u, v_power_now[z] == kNanScale);
           nan_rows |= nan_now[z] != 0;
           const int power = v_power_now[z] == kNanScale ? 127 : min(max(v_power_now[z], kLeastPower), kMostPower);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int x = 2 * z + i / 2, from = 16 * (i / 2) + row_a + 2 * (i % 2);
-            k_unit[x][i % 2] = __shfl_sync(~0u, unit, from);
+            unit_of[x][i % 2] = __shfl_sync(~0u, unit, from);
             const int c = __shfl_sync(~0u, power, from);
             v_log2[x][i % 2] = static_cast<float>(c - 127);
             v_inverse[x][i % 2] = __uint_as_float(static_cast<uint32_t>(254 - c) << 23);
           }
         }
-      } else if constexpr (kBits == 4) {
-#pragma unroll
-        for (int x = 0; x < kGroups; ++x)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) k_unit[x][i] = q_unit, v_log2[x][i] = 0.f;
       }
+      if constexpr (kBits < 16) {  // rows that are left out
+        if (!all_of(live_now)) {
+#pragma unroll
+          for (int x = 0; x < kGroups; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!((live_now[x / 2] >> (16 * (x % 2) + row_a + 2 * e)) & 1)) {
+                if constexpr (kBits == 8) unit_of[x][e] = 0.f, v_log2[x][e] = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[x][n][2 * e] = s[x][n][2 * e + 1] = kBits == 8 ? 0.f : -INFINITY;
+              }
+        }
+      }
+
       uint32_t hi_f[kGroups][NT][2], lo_f[kGroups][NT][2]  /* of codes: weights as fp16 alone */;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -811,9 +853,8 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
             if constexpr (kBits == 16) {
               const bool counts = (live_now[0] >> (16 * x + g + (e >> 1) * 8)) & 1;
               s[x][n][e] = counts ? s[x][n][e] * scale_log2 : -INFINITY;
-            } else {
-              const bool counts = (live_now[x / 2] >> (16 * (x % 2) + row_a + (e >> 1) * 2)) & 1;
-              s[x][n][e] = counts ? fmaf(s[x][n][e] * k_unit[x][e >> 1], scale_log2, v_log2[x][e >> 1]) : -INFINITY;
+            } else if constexpr (kBits == 8) {
+              s[x][n][e] = fmaf(s[x][n][e], unit_of[x][e >> 1], v_log2[x][e >> 1]);
             }
             top[e & 1] = fmaxf(top[e & 1], s[x][n][e]);
           }
@@ -822,7 +863,8 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
           top[0] = fmaxf(top[0], __shfl_xor_sync(~0u, top[0], x));
           top[1] = fmaxf(top[1], __shfl_xor_sync(~0u, top[1], x));
         }
-        if constexpr (kBits < 16) top[0] -= kWeightBits, top[1] -= kWeightBits;
+        if constexpr (kBits == 8) top[0] -= kWeightBits, top[1] -= kWeightBits;
+        if constexpr (kBits == 4) top[0] = fmaf(top[0], unit_log2, -kWeightBits), top[1] = fmaf(top[1], unit_log2, -kWeightBits);
         if (__any_sync(~0u, top[0] > m[n][0] || top[1] > m[n][1])) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -841,7 +883,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e] = fast_exp2(s[x][n][e] - ref[e & 1]);
+            p[e] = fast_exp2(kBits == 4 ? fmaf(s[x][n][e], unit_log2, -ref[e & 1]) : s[x][n][e] - ref[e & 1]);
             if constexpr (kBits == 8)
               l[n][e & 1] = fmaf(p[e], v_inverse[x][e >> 1], l[n][e & 1]);
             else
@@ -1143,17 +1185,18 @@ cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
 
 template <int kBits, int D, typename U>
 cudaError_t launch_by_heads(const DecodeArgs& a, int sms, cudaStream_t stream) {
+  if (kBits < 16 && a.together > 1 && a.part_heads <= 8) return launch<kBits, D, kBits < 16 ? 1 : 2, true, U>(a, sms, stream);
   if (a.together > 1) return launch<kBits, D, 2, true, U>(a, sms, stream);
   return a.part_heads <= 8 ? launch<kBits, D, 1, false, U>(a, sms, stream) : launch<kBits, D, 2, false, U>(a, sms, stream);
 }
 
 template <int kBits>
-cudaError_t launch_by_size(const DecodeArgs& a, int sms, cudaStream_t stream) {
+cudaError_t launch_by_size(const DecodeArgs& a, int sms, cudaStream_t stream, bool wide = false) {
   // the units of B full table rows
   constexpr int kTile = DecodeCfg<kBits, 128, 1>::kTile;
   static_assert(kTile == DecodeCfg<kBits, 64, 2>::kTile, "tiles go by the bits alone");
   const int64_t most = int64_t(a.B) * (int64_t(a.max_pages) * a.div.d / kTile + 1 + kRowUnits);
-  if (most > UINT32_MAX / (a.Hkv * a.passes))
+  if (wide || most > UINT32_MAX / a.vheads)
     return a.D == 128 ? launch_by_heads<kBits, 128, uint64_t>(a, sms, stream) : launch_by_heads<kBits, 64, uint64_t>(a, sms, stream);
   return a.D == 128 ? launch_by_heads<kBits, 128, uint32_t>(a, sms, stream) : launch_by_heads<kBits, 64, uint32_t>(a, sms, stream);
 }
