@@ -16,7 +16,7 @@ DecodeSpace decode_space(int D, const QueryParts& parts, int sms) {
 
 QueryParts query_parts(int group) {
   QueryParts k{1, 1, 1, group};
-  while (k.together < kDecodeWarps && k.together * kMostHeads < group) k.together *= 2;
+  while (k.together < kMostTogether && k.together * kMostHeads < group) k.together *= 2;
   k.passes = (group + kMostHeads * k.together - 1) / (kMostHeads * k.together);
   k.parts = k.passes * k.together;
   k.part_heads = (group + k.parts - 1) / k.parts;  // above 8 where there are parts

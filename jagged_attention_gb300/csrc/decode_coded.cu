@@ -3,14 +3,18 @@
 
 namespace jfa {
 
+constexpr int kLineMb = 96, kMatesMb = 2048, kFarMb = 512;
+
 cudaError_t launch_decode_coded(const DecodeArgs& given, int sms, cudaStream_t stream) {
   DecodeArgs a = given;
-  // Rows of neighbouring heads that share lines of 128 bytes, which is what memory gives
-  // at once, are read side by side: 4 bits, 64 heads on 8 of 128, rows outside heads, TODO.
-  const int row_bytes = a.D * a.bits / 8, mates = 128 / row_bytes;
-  if (a.parts == 1 && mates > 1 && a.head == row_bytes && a.Hkv % mates == 0) {
-    a.together = mates;
-    a.vheads = a.Hkv / mates;
+  // Rows of neighbouring heads are read side by side where there is enough to read: TODO.
+  const int row_bytes = a.D * a.bits / 8, mates = row_bytes < 128 ? 128 / row_bytes : 2;
+  const int64_t least = int64_t(row_bytes < 128 ? kLineMb : kMatesMb) << 20;
+  if (a.parts == 1 && a.head == row_bytes && a.Hkv % mates == 0) {
+    a.mates = mates;
+    const int64_t unit = 2 * row_bytes * (a.bits == 8 ? 32 : 64) * a.Hkv;  // of all heads
+    a.mates_units = static_cast<uint32_t>(least / unit);
+    a.far_units = static_cast<uint32_t>((int64_t(kFarMb) << 20) / unit);
   }
   // whether 32 bits hold offsets as the kernel counts them
   const int n = a.bits == 8 ? 1 : a.D / kBlock;

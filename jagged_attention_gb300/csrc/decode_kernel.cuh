@@ -53,8 +53,8 @@
 namespace jfa {
 namespace {
 
-constexpr int kDecodeWarps = 8;
 constexpr int kMostHeads = 16;   // query heads that a warp holds
+constexpr int kMostTogether = 8;  // warps side by side
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kWeightBits = 15.f;  // of codes: the largest weight is 2^15, as fp16 has it
 
@@ -69,7 +69,8 @@ struct DecodeCfg {
   static constexpr int kOutBytes = kHeads * D * 4;          // a stretch's O
   static constexpr int kVBytes = kOutBytes > kStageBytes ? kOutBytes : kStageBytes;  // holds a stretch's O when V is read
   static constexpr int kWarpBytes = kStageBytes + kVBytes + kOutBytes;  // K, V, park
-  static constexpr int kSmemBytes = kDecodeWarps * kWarpBytes;
+  static constexpr int kWarps = 8;
+  static constexpr int kSmemBytes = kWarps * kWarpBytes;
   static constexpr int kCtasPerSm = D == 64 || (kBits < 16 && NT == 1) ? 2 : 1;
 };
 constexpr int kMostCtasPerSm = 2;
@@ -89,6 +90,9 @@ constexpr int kGroup = 8;
 // 6.6 and 6.9, of 512 6.8 and 7.1, so that up to 16 it would gain as well, of 540 7.6
 // and 7.3.
 constexpr int kApartRows = 12 * 32;
+
+// Of codes a CTA's share is 2^kLeastBits units at least.
+constexpr int kLeastBits = 2;
 
 // Where a warp stands: tile t of n of (request b, key/value head and pass vh), unit
 // u of all.
@@ -128,13 +132,13 @@ struct Joined {
   }
 };
 
-template <int NT>
+template <int kWarps, int NT>
 struct DecodeShared {
-  Stretch part[2 * kDecodeWarps];                 // first and last of each warp
-  float m[2 * kDecodeWarps][8 * NT], l[2 * kDecodeWarps][8 * NT];
-  int64_t scan_units[kDecodeWarps];
-  int scan_rows[kDecodeWarps], scan_most[kDecodeWarps];
-  int64_t first_unit[kDecodeWarps * 32];  // of the requests that a thread adds up
+  Stretch part[2 * kWarps];                 // first and last of each warp
+  float m[2 * kWarps][8 * NT], l[2 * kWarps][8 * NT];
+  int64_t scan_units[kWarps];
+  int scan_rows[kWarps], scan_most[kWarps];
+  int64_t first_unit[kWarps * 32];  // of the requests that a thread adds up
   int from[2], to[2], last[2];
 };
 
@@ -148,9 +152,12 @@ __device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % k
 
 // The cache is read once a launch: its lines are the first to leave L2, before the
 // lengths, tables and queries (1 to 6% of a call of 23 to 75 us).
-__device__ __forceinline__ uint64_t read_once_policy() {
+__device__ __forceinline__ uint64_t read_once_policy(bool twice) {
   uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  if (twice)
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  else
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take, uint64_t policy) {
@@ -203,7 +210,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 }
 
 __device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -217,30 +224,9 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
-  uint4 w;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
-  return w;
-}
-__device__ __forceinline__ uint2 ld_shared_v2(uint32_t at) {
-  uint2 w;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(at) : "memory");
-  return w;
-}
-__device__ __forceinline__ uint32_t ld_shared(uint32_t at) {
-  uint32_t w;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
-  return w;
-}
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t at) {
-  uint32_t w;
-  asm volatile("{.reg .u16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;}" : "=r"(w) : "r"(at) : "memory");
-  return w;
-}
-__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t at) {
-  uint32_t w;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
-  return w;
+template <typename T>
+__device__ __forceinline__ T at_shared(const unsigned char* p) {
+  return *reinterpret_cast<const T*>(p);
 }
 
 // Place of value (head, d) of a stretch's O in shared memory: the exclusive or
@@ -311,25 +297,18 @@ __device__ __forceinline__ void store_joined(const DecodeArgs& a, int D, int b, 
 // wide enough for more; 64 bits cost 0.3 to 0.6 us.
 // kSide: parts of query heads side by side.
 template <int kBits, int D, int NT, bool kSide, typename U>
-__global__ void __launch_bounds__(kDecodeWarps * 32, DecodeCfg<kBits, D, NT>::kCtasPerSm)
+__global__ void __launch_bounds__(DecodeCfg<kBits, D, NT>::kWarps * 32, DecodeCfg<kBits, D, NT>::kCtasPerSm)
 decode_kernel(const __grid_constant__ DecodeArgs a) {
   using C = DecodeCfg<kBits, D, NT>;
-  constexpr int kTile = C::kTile, kSub = C::kSub;
+  constexpr int kTile = C::kTile, kSub = C::kSub, kWarps = C::kWarps;
   extern __shared__ __align__(256) unsigned char smem[];
-  __shared__ DecodeShared<NT> sh;
+  __shared__ DecodeShared<kWarps, NT> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   wait_for_launch_before();
-  // A CTA's share is dealt to `subs` sets of `together` warps, one for each part of
-  // the query heads; a line is a warp's place with those of its part in a row.
-  const int vheads = kSide ? a.vheads : a.Hkv, together = kSide ? a.together : 1;
-  const int sub_bits = kSide ? __ffs(kDecodeWarps / together) - 1 : __builtin_ctz(kDecodeWarps), subs = 1 << sub_bits;
-  const int part = kSide ? warp & (together - 1) : 0, sub = kSide ? warp / together : warp;
-  const int line = (part << sub_bits) + sub;
-
   // ---- units of all requests, and where this CTA's warps begin.  Up to 32 requests
   // a warp adds up by itself, a lane for each, and waits for no other warp.
   const bool few = a.B <= 32;
-  const int slab = few ? 1 : (a.B + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
+  const int slab = few ? 1 : (a.B + kWarps * 32 - 1) / (kWarps * 32);
   const int b_lo = min(a.B, (few ? lane : tid) * slab), b_hi = min(a.B, b_lo + slab);
   U units = 0;
   int rows = 0, most = 0, last_len = 0;  // rows: requests that have any
@@ -349,7 +328,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     if (lane >= o) units_to += x, rows_to += y;
   }
   most = __reduce_max_sync(~0u, most);
-  if (lane < 2) sh.part[2 * line + lane].n = 0;
+  if (lane < 2) sh.part[2 * warp + lane].n = 0;
   U total = __shfl_sync(~0u, units_to, 31);
   int all_rows = __shfl_sync(~0u, rows_to, 31);
   if (!few) {
@@ -362,7 +341,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     total = 0;
     all_rows = 0;
 #pragma unroll
-    for (int w = 0; w < kDecodeWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       const U x = static_cast<U>(sh.scan_units[w]);
       const int y = sh.scan_rows[w];
       if (w < warp) units_to += x, rows_to += y;
@@ -371,6 +350,16 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       most = max(most, sh.scan_most[w]);
     }
   }
+  // A CTA's share is dealt to `subs` sets of `together` warps, one for each part of
+  // the query heads, or for each of a few key/value heads whose rows lie side by side; a
+  // line is a warp's place with those of its part in a row.
+  const bool mates = kBits < 16 && kSide && a.mates > 1 && total >= a.mates_units;
+  const bool far = total >= a.far_units;
+  const int vheads = mates ? a.Hkv / a.mates : kSide ? a.vheads : a.Hkv, together = mates ? a.mates : kSide ? a.together : 1;
+  const int sub_bits = kSide ? __ffs(kWarps / together) - 1 : __builtin_ctz(kWarps), subs = 1 << sub_bits;
+  const int part = kSide ? warp & (together - 1) : 0, sub = kSide ? warp / together : warp;
+  const int line = (part << sub_bits) + sub;
+
   // few and short rows: a CTA for each, so that nothing is left to be joined between CTAs
   const bool apart = most <= kApartRows / C::kTile / together && int64_t(all_rows) * vheads <= gridDim.x;
   if (apart) {
@@ -380,12 +369,13 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   }
   auto units_of = [&](int n) -> U { return n == 0 ? 0 : apart ? most : n + kRowUnits; };
   total *= vheads;
-  // fewer CTAs than there are where each warp would not have a unit
+  // fewer CTAs than there are where each warp, or few of them, would not have a unit
+  const int least_bits = kBits == 16 ? sub_bits : min(sub_bits, kLeastBits);
   int ctas = static_cast<int>(gridDim.x);
   if (apart)
     ctas = max(1, all_rows * vheads);
-  else if (total < U(ctas) << sub_bits)
-    ctas = max(1, static_cast<int>(total >> sub_bits));
+  else if (total < U(ctas) << least_bits)
+    ctas = max(1, static_cast<int>(total >> least_bits));
   const int cta = blockIdx.x;
   const Deal<U> deal(total, ctas);
   const U cta_lo = cta < ctas ? deal.from(cta) : 0, cta_n = cta < ctas ? deal.from(cta + 1) - cta_lo : 0;
@@ -399,6 +389,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   const U lo = sub_from(sub), hi = sub_from(sub + 1);
 
   unsigned char* mine_smem = smem + line * C::kWarpBytes;
+  const unsigned char *k_codes = mine_smem, *v_codes = mine_smem + C::kStageBytes;
   const uint32_t k_stage = smem_u32(mine_smem), v_stage = k_stage + C::kStageBytes;
   float* v_floats = reinterpret_cast<float*>(mine_smem + C::kStageBytes);
   float* park = reinterpret_cast<float*>(mine_smem + C::kStageBytes + C::kVBytes);
@@ -434,11 +425,11 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         at.len = __shfl_sync(~0u, last_len, at.b);
         at.n = tiles_of<C::kTile>(at.len);
       } else {
-        // by groups of kDecodeWarps threads and then within the group
+        // by groups of kWarps threads and then within the group
         auto begins = [&](int t) { return static_cast<U>(sh.first_unit[t]) <= lo; };
-        static_assert(kDecodeWarps <= 32, "a group's threads have a lane each");
-        const int t0 = (__popc(__ballot_sync(~0u, begins(lane * kDecodeWarps))) - 1) * kDecodeWarps;
-        const int t = t0 + __popc(__ballot_sync(~0u, lane < kDecodeWarps && begins(t0 + (lane % kDecodeWarps)))) - 1;
+        static_assert(kWarps <= 32, "a group's threads have a lane each");
+        const int t0 = (__popc(__ballot_sync(~0u, begins(lane * kWarps))) - 1) * kWarps;
+        const int t = t0 + __popc(__ballot_sync(~0u, lane < kWarps && begins(t0 + (lane % kWarps)))) - 1;
         r = lo - static_cast<U>(sh.first_unit[t]);
         for (at.b = t * slab;; ++at.b) {
           at.len = length_of(a, at.b);
@@ -531,7 +522,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     };
     // Rows of a tile into a stage.  bf16: 8 lanes copy 128 bytes of a row, chunk c of row
     // r to place c ^ (r % 8) of its 8.  Codes: the lanes that a row has chunks of 16 bytes.
-    const uint64_t policy = read_once_policy();
+    const uint64_t policy = read_once_policy(mates && far);
     const uint32_t to_even = (lane >> 3) * (D * 2) + (((lane & 7) ^ (lane >> 3)) << 4), to_odd = to_even ^ 64;
     auto copy = [&](uint32_t stage, const uint16_t* from, bool v) {
       if constexpr (kBits == 16) {
@@ -646,91 +637,79 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
             w[ks][n][i] = pack_f16x2(__uint_as_float(w[ks][n][i] << 16) * by, __uint_as_float(w[ks][n][i] & 0xffff0000u) * by);
       return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     };
-    // K of group x: rows row_a and row_a + 2.
-    auto load_k = [&](int x, uint32_t (&f)[D / 16][4]) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = 16 * x + row_a + 2 * i;
-        if constexpr (kBits == 8) {
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            const uint4 w = ld_shared_v4(k_stage + chunk_at<C::kRowBytes>(row, j + 4 * h, false));
-            halves_of_e4m3x4(w.x, f[4 * h][i], f[4 * h][2 + i]);
-            halves_of_e4m3x4(w.y, f[4 * h + 1][i], f[4 * h + 1][2 + i]);
-            halves_of_e4m3x4(w.z, f[4 * h + 2][i], f[4 * h + 2][2 + i]);
-            halves_of_e4m3x4(w.w, f[4 * h + 3][i], f[4 * h + 3][2 + i]);
-          }
+    // Words of codes of K that a lane takes up at a time from a row: 4 (of 8 codes for 2
+    // steps, or of 4 for one), a 16-byte chunk, or the 2 that there are.
+    constexpr int kWords = kBits == 4 ? D / 32 : 4, kParts = kBits == 8 ? D / 64 : 1, kSteps = kBits == 4 ? 2 : 1;
+    // Part h of rows 16 x + row_a + 2 i.
+    auto load_k = [&](int x, int i, int h, uint32_t (&w)[kWords], uint32_t (&by)[2]) {
+      const int row = 16 * x + row_a + 2 * i;
+      if constexpr (kBits == 8 || D == 128) {
+        const uint4 q = at_shared<uint4>(k_codes + chunk_at<C::kRowBytes>(row, j + 4 * h, false));
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+      } else {
+        const uint2 q = at_shared<uint2>(k_codes + chunk_at<C::kRowBytes>(row, j >> 1, false) + 8 * (j & 1));
+        w[0] = q.x, w[1] = q.y;
+      }
+      if constexpr (kBits == 4) {
+        const unsigned char* scales = k_codes + kTile * C::kRowBytes + row * C::kScaleBytes;
+        if constexpr (D == 128) {
+          const uint32_t c = at_shared<uint16_t>(scales + 2 * j);
+          by[0] = (c & 0xffu) * 0x00800080u;
+          by[1] = (c >> 8) * 0x00800080u;
         } else {
-          uint32_t w[D / 32];
-          const uint32_t scales = k_stage + kTile * C::kRowBytes + row * C::kScaleBytes;
-          uint32_t by[2];
-          if constexpr (D == 128) {
-            const uint4 q = ld_shared_v4(k_stage + chunk_at<C::kRowBytes>(row, j, false));
-            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-            const uint32_t c = ld_shared_u16(scales + 2 * j);
-            by[0] = (c & 0xffu) * 0x00800080u;
-            by[1] = (c >> 8) * 0x00800080u;
-          } else {
-            const uint2 q = ld_shared_v2(k_stage + chunk_at<C::kRowBytes>(row, j >> 1, false) + 8 * (j & 1));
-            w[0] = q.x, w[1] = q.y;
-            by[0] = by[1] = ld_shared_u8(scales + j) * 0x00800080u;
-          }
-#pragma unroll
-          for (int t = 0; t < D / 32; ++t) {
-            uint32_t h[4];
-            halves_of_e2m1x8(w[t], h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[2 * t + e / 2][2 * (e % 2) + i] = mul_f16x2(h[e], by[t / 2]);
-          }
+          by[0] = by[1] = at_shared<uint8_t>(scales + j) * 0x00800080u;
         }
       }
     };
-    // V of group x: values D / 8 g and on of rows 4 j .. 4 j + 3, pairs of rows together.
-    auto load_v = [&](int x, uint32_t (&f)[D / 16][4]) {
+    // Word t of a part: rows row_a + 2 i of the fragments of its steps.
+    auto halves_of_k = [&](uint32_t w, const uint32_t (&by)[2], int t, int i, uint32_t (&f)[kSteps][4]) {
+      if constexpr (kBits == 8) {
+        halves_of_e4m3x4(w, f[0][i], f[0][2 + i]);
+      } else {
+        uint32_t h[4];
+        halves_of_e2m1x8(w, h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e / 2][2 * (e % 2) + i] = mul_f16x2(h[e], by[t / 2]);
+      }
+    };
+    // Values D / 8 g and on of V, of rows 16 x + 4 j + r: words, and (4 bits) scales.
+    constexpr int kVWords = kBits == 8 ? D / 32 : D / 64, kVTiles = kBits == 8 ? 2 : 4;  // of O a word
+    auto load_v = [&](int x, uint32_t (&w)[4][kVWords], uint32_t (&by)[2]) {
+      by[0] = by[1] = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * x + 4 * j + r;
+        if constexpr (kVWords == 4) {
+          const uint4 q = at_shared<uint4>(v_codes + chunk_at<C::kRowBytes>(row, g, true));
+          w[r][0] = q.x, w[r][1] = q.y, w[r][2] = q.z, w[r][3] = q.w;
+        } else if constexpr (kVWords == 2) {
+          const uint2 q = at_shared<uint2>(v_codes + chunk_at<C::kRowBytes>(row, g >> 1, true) + 8 * (g & 1));
+          w[r][0] = q.x, w[r][1] = q.y;
+        } else {
+          w[r][0] = at_shared<uint32_t>(v_codes + chunk_at<C::kRowBytes>(row, g >> 2, true) + 4 * (g & 3));
+        }
+        if constexpr (kBits == 4) {
+          const unsigned char* scales = v_codes + kTile * C::kRowBytes + row * C::kScaleBytes;
+          by[r / 2] += at_shared<uint8_t>(scales + (D == 128 ? g : g >> 1)) * (r % 2 ? 1u << 23 : 1u << 7);
+        }
+      }
+    };
+    // Word t of the rows: fragments of O's tiles kVTiles t and on.
+    auto halves_of_v = [&](const uint32_t (&w)[4][kVWords], const uint32_t (&by)[2], int t, uint32_t (&f)[kVTiles][4]) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {  // rows 2 i, 2 i + 1 of the four
-        const int row = 16 * x + 4 * j + 2 * i;
+        const uint32_t a = w[2 * i][t], b = w[2 * i + 1][t];
         if constexpr (kBits == 8) {
-          uint32_t w[2][D / 32];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            if constexpr (D == 128) {
-              const uint4 q = ld_shared_v4(v_stage + chunk_at<C::kRowBytes>(row + r, g, true));
-              w[r][0] = q.x, w[r][1] = q.y, w[r][2] = q.z, w[r][3] = q.w;
-            } else {
-              const uint2 q = ld_shared_v2(v_stage + chunk_at<C::kRowBytes>(row + r, g >> 1, true) + 8 * (g & 1));
-              w[r][0] = q.x, w[r][1] = q.y;
-            }
-          }
-#pragma unroll
-          for (int t = 0; t < D / 32; ++t) {
-            halves_of_e4m3x4(__byte_perm(w[0][t], w[1][t], 0x5140), f[2 * t][2 * i], f[2 * t][2 * i + 1]);
-            halves_of_e4m3x4(__byte_perm(w[0][t], w[1][t], 0x7362), f[2 * t + 1][2 * i], f[2 * t + 1][2 * i + 1]);
-          }
+          halves_of_e4m3x4(__byte_perm(a, b, 0x5140), f[0][2 * i], f[0][2 * i + 1]);
+          halves_of_e4m3x4(__byte_perm(a, b, 0x7362), f[1][2 * i], f[1][2 * i + 1]);
         } else {
-          uint32_t w[2][D / 64], by = 0;
+          uint32_t even[4], odd[4];  // first and second value of each pair
+          halves_of_e2m1x8((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even);
+          halves_of_e2m1x8(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t scales = v_stage + kTile * C::kRowBytes + (row + r) * C::kScaleBytes;
-            if constexpr (D == 128) {
-              const uint2 q = ld_shared_v2(v_stage + chunk_at<C::kRowBytes>(row + r, g >> 1, true) + 8 * (g & 1));
-              w[r][0] = q.x, w[r][1] = q.y;
-              by += ld_shared_u8(scales + g) << (r ? 23 : 7);
-            } else {
-              w[r][0] = ld_shared(v_stage + chunk_at<C::kRowBytes>(row + r, g >> 2, true) + 4 * (g & 3));
-              by += ld_shared_u8(scales + (g >> 1)) << (r ? 23 : 7);
-            }
-          }
-#pragma unroll
-          for (int t = 0; t < D / 64; ++t) {
-            uint32_t even[4], odd[4];  // first and second value of each pair
-            halves_of_e2m1x8((w[0][t] & 0x0f0f0f0fu) | ((w[1][t] << 4) & 0xf0f0f0f0u), even);
-            halves_of_e2m1x8(((w[0][t] >> 4) & 0x0f0f0f0fu) | (w[1][t] & 0xf0f0f0f0u), odd);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[4 * t + e][2 * i] = mul_f16x2(even[e], by);
-              f[4 * t + e][2 * i + 1] = mul_f16x2(odd[e], by);
-            }
+          for (int e = 0; e < 4; ++e) {
+            f[e][2 * i] = mul_f16x2(even[e], by[i]);
+            f[e][2 * i + 1] = mul_f16x2(odd[e], by[i]);
           }
         }
       }
@@ -789,14 +768,34 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
           }
         }
       } else {
+        // two groups at a time: two chains of sums side by side
 #pragma unroll
-        for (int x = 0; x < kGroups; ++x) {
-          uint32_t kf[D / 16][4];
-          load_k(x, kf);
+        for (int x = 0; x < kGroups; x += 2) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
+          for (int h = 0; h < kParts; ++h) {
+            uint32_t w[2][2][kWords], by[2][2][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16816_f16(s[x][n], kf[ks], qf[ks][n][0], qf[ks][n][1]);
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) load_k(x + y, i, h, w[y][i], by[y][i]);
+#pragma unroll
+            for (int t = 0; t < kWords; ++t) {
+              uint32_t f[2][kSteps][4];
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) halves_of_k(w[y][i][t], by[y][i], t, i, f[y]);
+#pragma unroll
+              for (int z = 0; z < kSteps; ++z)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) {
+                    const int ks = (h * kWords + t) * kSteps + z;
+                    mma_16816_f16(s[x + y][n], f[y][z], qf[ks][n][0], qf[ks][n][1]);
+                  }
+            }
+          }
         }
       }
       __syncwarp();  // K is read
@@ -923,12 +922,17 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       } else {
 #pragma unroll
         for (int x = 0; x < kGroups; ++x) {
-          uint32_t vf[D / 16][4];
-          load_v(x, vf);
+          uint32_t w[4][kVWords], by[2];
+          load_v(x, w, by);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
+          for (int t = 0; t < kVWords; ++t) {
+            uint32_t f[kVTiles][4];
+            halves_of_v(w, by, t, f);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16816_f16(o_acc[i][n], vf[i], hi_f[x][n][0], hi_f[x][n][1]);
+            for (int i = 0; i < kVTiles; ++i)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_16816_f16(o_acc[kVTiles * t + i][n], f[i], hi_f[x][n][0], hi_f[x][n][1]);
+          }
         }
       }
       __syncwarp();  // V is read
@@ -998,9 +1002,9 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (length_of(a, b) > 0) continue;
     if (tid == 0 && a.lens[b] != 0) atomicOr(a.status, kPagerBadLength);
-    for (int i = tid; i < a.H * (D / 4); i += kDecodeWarps * 32)
+    for (int i = tid; i < a.H * (D / 4); i += kWarps * 32)
       store_out4(a, D, b, i / (D / 4), 4 * (i % (D / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
-    for (int h = tid; h < a.H; h += kDecodeWarps * 32) a.lse[int64_t(h) * a.B + b] = -INFINITY;
+    for (int h = tid; h < a.H; h += kWarps * 32) a.lse[int64_t(h) * a.B + b] = -INFINITY;
   }
   if (cta_n == 0) return;
   __syncthreads();
@@ -1012,8 +1016,9 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int kQuads = D / 4;
   uint32_t held, heads_at;  // slots that hold a part, and those where a row's first part is
   {
-    const Stretch p = sh.part[lane & (2 * kDecodeWarps - 1)];
-    const bool have = lane < 2 * kDecodeWarps && p.n > 0;
+    static_assert(2 * kWarps <= 32, "a lane for each slot");
+    const Stretch p = sh.part[lane & (2 * kWarps - 1)];
+    const bool have = lane < 2 * kWarps && p.n > 0;
     held = __ballot_sync(~0u, have);
     const uint32_t below = held & ((1u << lane) - 1);
     const int prev = below ? 31 - __clz(below) : lane;
@@ -1022,16 +1027,16 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   }
   // as many rows at once as have threads for their heads
   int row_threads = 32;
-  while (row_threads < a.part_heads * kQuads && row_threads < kDecodeWarps * 32) row_threads *= 2;
-  const int row_tid = tid & (row_threads - 1), my_turn = tid / row_threads, turns = kDecodeWarps * 32 / row_threads;
+  while (row_threads < a.part_heads * kQuads && row_threads < kWarps * 32) row_threads *= 2;
+  const int row_tid = tid & (row_threads - 1), my_turn = tid / row_threads, turns = kWarps * 32 / row_threads;
   // a slot of what goes on in other CTAs, by its place in global memory: 0 begun
   // before, 1 begun here (all parts of its query heads alike)
   int open[2] = {-1, -1};
   for (int turn = 0; heads_at; ++turn) {
     const int s = __ffs(heads_at) - 1;
     heads_at &= heads_at - 1;
-    const int end = heads_at ? __ffs(heads_at) - 1 : 2 * kDecodeWarps;
-    const uint32_t parts = held & ((1u << end) - (1u << s));
+    const uint32_t behind = heads_at ? ~0u << (__ffs(heads_at) - 1) : 0u;  // slots of later rows
+    const uint32_t parts = held & ~behind & (~0u << s);
     const Stretch& p = sh.part[s];
     const bool whole = p.t0 == 0 && sh.part[31 - __clz(parts)].t1 == p.n;
     const int place = p.t0 == 0 ? 1 : 0;
@@ -1110,7 +1115,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
         const int first_at = (2 * base + (base == from ? 1 : 0)) * together + y;
         const int next_at = 2 * base * together + y, step_at = 2 * step * together;
         // 4 values of kItems heads to a thread, the loads of a batch of parts under way together
-        constexpr int kThreads = kDecodeWarps * 32;
+        constexpr int kThreads = kWarps * 32;
         constexpr int kItems = C::kHeads * kQuads > kThreads ? C::kHeads * kQuads / kThreads : 1;
         static_assert(kItems * kThreads >= C::kHeads * kQuads, "one round for all heads");
         Joined sum[kItems];
@@ -1176,17 +1181,17 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
 template <int kBits, int D, int NT, bool kSide, typename U>
 cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
   using C = DecodeCfg<kBits, D, NT>;
-  static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<NT>) + 1024) <= 233472, "shared memory of an SM");
+  static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<C::kWarps, NT>) + 1024) <= 233472, "shared memory of an SM");
   cudaError_t e = set_smem_limit_once<decode_kernel<kBits, D, NT, kSide, U>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(decode_kernel<kBits, D, NT, kSide, U>, dim3(sms * C::kCtasPerSm), kDecodeWarps * 32,
+  return launch_overlapped(decode_kernel<kBits, D, NT, kSide, U>, dim3(sms * C::kCtasPerSm), C::kWarps * 32,
                            C::kSmemBytes, stream, a);
 }
 
 template <int kBits, int D, typename U>
 cudaError_t launch_by_heads(const DecodeArgs& a, int sms, cudaStream_t stream) {
-  if (kBits < 16 && a.together > 1 && a.part_heads <= 8) return launch<kBits, D, kBits < 16 ? 1 : 2, true, U>(a, sms, stream);
-  if (a.together > 1) return launch<kBits, D, 2, true, U>(a, sms, stream);
+  if (kBits < 16 && a.mates > 1 && a.part_heads <= 8) return launch<kBits, D, kBits < 16 ? 1 : 2, true, U>(a, sms, stream);
+  if (a.together > 1 || a.mates > 1) return launch<kBits, D, 2, true, U>(a, sms, stream);
   return a.part_heads <= 8 ? launch<kBits, D, 1, false, U>(a, sms, stream) : launch<kBits, D, 2, false, U>(a, sms, stream);
 }
 

@@ -143,7 +143,9 @@ struct DecodeArgs {
   int B, H, Hkv, D;
   int group;                                // H / Hkv
   int parts, together, passes, part_heads;  // QueryParts
-  int vheads;  // sets of `together` parts or heads: Hkv * passes, or fewer where heads go side by side
+  int vheads;           // Hkv * passes: sets of `together` parts
+  int mates;            // key/value heads that may go side by side instead, 1 where none do,
+  uint32_t mates_units, far_units;  // if the requests have so many units; TODO
   int64_t num_pages;
   int max_pages;
   PageDiv div;
@@ -163,13 +165,12 @@ struct DecodeArgs {
   float *part_ml, *part_o;   // what CTAs leave of split rows
 };
 // A key/value head's query heads in parts of at most 16: `together` of them (1, 2,
-// 4 or 8) side by side in a CTA, in `passes` over the cache.  Heads with one part may
-// go side by side instead: parts 1, as many together as kMostMates.
+// 4 or 8) side by side in a CTA, in `passes` over the cache.
 struct QueryParts {
   int parts, together, passes, part_heads;
 };
 QueryParts query_parts(int group);
-constexpr int kMostMates = 4;
+constexpr int kMostMates = 4;  // heads of one part that go side by side
 
 // Workspace of a decode launch: counters (int), part_ml and part_o (float).
 struct DecodeSpace {

@@ -412,6 +412,7 @@ int jfa_paged_decode_ex(jfa_pager_t pager, int B, const void* q, int64_t q_row, 
   a.passes = pager->parts.passes;
   a.part_heads = pager->parts.part_heads;
   a.vheads = pager->Hkv * pager->parts.passes;
+  a.mates = 1;
   a.num_pages = pager->num_pages;
   a.max_pages = pager->max_pages;
   a.div = pager->div;
