@@ -696,6 +696,10 @@ class Pager:
         if bits not in (16, 8, 4):
             raise ValueError(f"bits must be 16, 8 or 4, got {bits}")
         self.bits, self.scale_bytes = bits, 1 if bits == 8 else D // 16
+        shape = (num_pages, page_size, Hkv)
+        self._pages_shape = (*shape, D if bits == 16 else D * bits // 8)
+        self._pages_dtype = torch.bfloat16 if bits == 16 else torch.uint8
+        self._scales_shape = (*shape, self.scale_bytes)
         self.max_seqs, self.max_pages, self.num_pages, self.page_size = max_seqs, max_pages, num_pages, page_size
         self.H, self.Hkv, self.D = H, Hkv, D
         self.device = torch.device("cuda", torch.cuda.current_device())
@@ -722,14 +726,12 @@ class Pager:
     def pages(self):
         """A cache for this pager, all zeros: (k_pages, v_pages, k_scales, v_scales), scales
         None with 16 bits.  The scales of a head's rows lie one behind the other."""
-        shape = (self.num_pages, self.page_size, self.Hkv)
+        k, v = (torch.zeros(self._pages_shape, dtype=self._pages_dtype, device=self.device) for _ in range(2))
         if self.bits == 16:
-            k, v = (torch.zeros((*shape, self.D), dtype=torch.bfloat16, device=self.device) for _ in range(2))
             return k, v, None, None
-        k, v = (torch.zeros((*shape, self.D * self.bits // 8), dtype=torch.uint8, device=self.device)
-                for _ in range(2))
-        k_scales, v_scales = (torch.zeros((shape[0], shape[2], shape[1], self.scale_bytes), dtype=torch.uint8,
-                                          device=self.device).transpose(1, 2) for _ in range(2))
+        pages, rows, heads, n = self._scales_shape
+        k_scales, v_scales = (torch.zeros((pages, heads, rows, n), dtype=torch.uint8, device=self.device).transpose(1, 2)
+                              for _ in range(2))
         return k, v, k_scales, v_scales
 
     def _launch_stream(self) -> int:
@@ -766,32 +768,32 @@ class Pager:
 
 
 def _pages(pager: Pager, k_pages, v_pages) -> _Pages:
-    n, dtype = (pager.D, torch.bfloat16) if pager.bits == 16 else (pager.D * pager.bits // 8, torch.uint8)
-    return _Pages(*_pair("pages", k_pages, v_pages, (pager.num_pages, pager.page_size, pager.Hkv, n), dtype,
-                         pager.index))
+    return _Pages(*_pair("pages", k_pages, v_pages, pager._pages_shape, pager._pages_dtype, pager.index))
 
 
 def _pair(what: str, k, v, shape, dtype, dev: int) -> tuple:
-    """(address of k, of v, distances of pages, rows and heads) of two tensors alike."""
+    """(address of k, of v, distances of pages, rows and heads) of two tensors alike.  The
+    stride of a dimension of one says nothing: 0."""
     st, sv = k.stride(), v.stride()
-    for name, t, s in (("k_" + what, k, st), ("v_" + what, v, sv)):
-        if t.dtype != dtype or t.get_device() != dev or t.shape != shape or s[-1] != 1 and shape[-1] > 1:
-            _refuse(name, t, dtype, dev, shape)
-    if 1 in shape:  # the stride of a dimension of one says nothing
-        st, sv = (tuple(0 if n == 1 else x for n, x in zip(shape, y)) for y in (st, sv))
-    if st != sv:
+    pages, rows, heads, n = shape
+    if k.dtype != dtype or k.get_device() != dev or k.shape != shape or st[3] != 1 and n > 1:
+        _refuse("k_" + what, k, dtype, dev, shape)
+    if v.dtype != dtype or v.get_device() != dev or v.shape != shape or sv[3] != 1 and n > 1:
+        _refuse("v_" + what, v, dtype, dev, shape)
+    page, row, head = st[0] if pages > 1 else 0, st[1] if rows > 1 else 0, st[2] if heads > 1 else 0
+    if st != sv and (page, row, head) != (sv[0] if pages > 1 else 0, sv[1] if rows > 1 else 0, sv[2] if heads > 1 else 0):
         raise ValueError(f"k_{what} and v_{what} must have the same strides, got {st} and {sv}")
-    return k.data_ptr(), v.data_ptr(), st[0], st[1], st[2]
+    return k.data_ptr(), v.data_ptr(), page, row, head
 
 
 def _scales(pager: Pager, k_scales, v_scales):
     """jfa_scales, None with 16 bits."""
-    if (k_scales is None or v_scales is None) != (pager.bits == 16) or (k_scales is None) != (v_scales is None):
-        raise ValueError(f"a cache of {pager.bits} bits {'has no' if pager.bits == 16 else 'needs'} k_scales and v_scales")
-    if k_scales is None:
-        return None
-    shape = (pager.num_pages, pager.page_size, pager.Hkv, pager.scale_bytes)
-    return ctypes.byref(_Scales(*_pair("scales", k_scales, v_scales, shape, torch.uint8, pager.index)))
+    if pager.bits == 16:
+        if k_scales is None and v_scales is None:
+            return None
+    elif k_scales is not None and v_scales is not None:
+        return ctypes.byref(_Scales(*_pair("scales", k_scales, v_scales, pager._scales_shape, torch.uint8, pager.index)))
+    raise ValueError(f"a cache of {pager.bits} bits {'has no' if pager.bits == 16 else 'needs'} k_scales and v_scales")
 
 
 def paged_tables(pager: Pager, lens, delta, table, free_list, n_free, *, rows: int, lens_out=None,
@@ -882,13 +884,18 @@ def paged_gather(pager: Pager, k_pages, v_pages, table, offsets, *, rows: int, s
     shape = (rows, pager.Hkv, pager.D)
     if k_out is None:
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=pager.device)
+        to_k = k_out.data_ptr(), pager.Hkv * pager.D
+    else:
+        to_k = _rows("k_out", k_out, shape, torch.bfloat16, dev)
     if v_out is None:
         v_out = torch.empty(shape, dtype=torch.bfloat16, device=pager.device)
+        to_v = v_out.data_ptr(), pager.Hkv * pager.D
+    else:
+        to_v = _rows("v_out", v_out, shape, torch.bfloat16, dev)
     rc = (_lib or lib()).jfa_paged_gather(
         pager.handle, B, ctypes.byref(_pages(pager, k_pages, v_pages)), _scales(pager, k_scales, v_scales),
         *_table(table, pager, B, dev), None if starts is None else _ints("starts", starts, B, dev),
-        _ints("offsets", offsets, B + 1, dev), rows, *_rows("k_out", k_out, shape, torch.bfloat16, dev),
-        *_rows("v_out", v_out, shape, torch.bfloat16, dev), pager._launch_stream())
+        _ints("offsets", offsets, B + 1, dev), rows, *to_k, *to_v, pager._launch_stream())
     if rc:
         _check(rc, "jfa_paged_gather")
     return k_out, v_out

@@ -30,26 +30,31 @@ __host__ __device__ constexpr int scale_bytes(int D) {
 
 // ---- values to codes.  `top`: the largest magnitude of bf16 values, as its bits.
 
-__device__ __forceinline__ uint32_t top_of(uint32_t a, uint32_t b) { return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu); }
-__device__ __forceinline__ uint32_t top_of(const uint4& w) {
-  const uint32_t t = __vmaxu2(top_of(w.x, w.y), top_of(w.z, w.w));
-  return max(t & 0xffffu, t >> 16);
+// The larger magnitudes of two pairs of bf16 values, as their bits; NaN is the largest.
+// Sign bits may be set.
+__device__ __forceinline__ uint32_t max_of(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
 }
+__device__ __forceinline__ uint32_t top_of(uint32_t pair) { return max(pair & 0x7fffu, (pair >> 16) & 0x7fffu); }
+__device__ __forceinline__ uint32_t max_of(const uint4& w) { return max_of(max_of(w.x, w.y), max_of(w.z, w.w)); }
 // The byte of the least power of two that takes `top` to 448 = 1.75 * 2^8 at most: its
 // exponent less 8, one more from a mantissa of 97/128 on.
 __device__ __forceinline__ int power_of(uint32_t top) {
   if (top >= 0x7f80u) return kNanScale;
   return min(max(static_cast<int>((top + 31) >> 7) - 8, kLeastPower), kMostPower);
 }
-// The byte of a block's scale, top / 6 to nearest even.  The quotient's rounding to
-// fp32 moves no value over or onto a border between two scales: a border has 5 bits,
-// six times it 7 or fewer, as bf16 has 8.
+// The byte of a block's scale, top / 6 to nearest even.  Half way between two scales lie
+// numbers of 5 bits; six times one has 7, so that top, of 8 bits, is that or 2^-9 off it.
+// top times the rounded 1/6 is off by 2^-23, and rounded to 12 bits it is the number
+// again, or on the right side of it.
 __device__ __forceinline__ int scale_of(uint32_t top) {
   if (top >= 0x7f80u) return kNanScale;
-  const float s = fminf(__fdiv_rn(__uint_as_float(top << 16), 6.f), kMostScale);
-  if (s < 0x1p-14f) return __float2int_rn(s * 0x1p17f);
-  const uint32_t bits = __float_as_uint(s);
-  return static_cast<int>((bits + 0x7ffffu + ((bits >> 20) & 1)) >> 20) - (112 << 3);
+  const float s = fminf(__uint_as_float(top << 16) * (1.f / 6.f), kMostScale);
+  const uint32_t bits = (__float_as_uint(s) + 0x800u) & 0xfffff000u;
+  const int byte = static_cast<int>((bits + 0x7ffffu + ((bits >> 20) & 1)) >> 20) - (112 << 3);
+  return s < 0x1p-14f ? __float2int_rn(__uint_as_float(bits) * 0x1p17f) : byte;
 }
 __device__ __forceinline__ float scale_value(int byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
@@ -60,29 +65,39 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
       "mov.b32 %0, {x, y};}" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
+// Codes of 8 numbers, by way of fp16.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
   uint32_t r;
-  asm("{.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};}"
+  asm("{.reg .b8 a, b, c, d;\n\t.reg .b32 s, t, u, v;\n\tcvt.rn.f16x2.f32 s, %2, %1;\n\tcvt.rn.f16x2.f32 t, %4, %3;\n\t"
+      "cvt.rn.f16x2.f32 u, %6, %5;\n\tcvt.rn.f16x2.f32 v, %8, %7;\n\tcvt.rn.satfinite.e2m1x2.f16x2 a, s;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b, t;\n\tcvt.rn.satfinite.e2m1x2.f16x2 c, u;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 d, v;\n\tmov.b32 %0, {a, b, c, d};}"
       : "=r"(r) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 // 8 bf16 values as e4m3 codes of a row with power byte c.
 __device__ __forceinline__ uint2 code8(const float (&x)[8], int c) {
   const float by = __uint_as_float(static_cast<uint32_t>(254 - c) << 23);  // c = 255: whatever, all is NaN
-  return make_uint2(e4m3x4(x[0] * by, x[1] * by, x[2] * by, x[3] * by), e4m3x4(x[4] * by, x[5] * by, x[6] * by, x[7] * by));
-}
-// 8 bf16 values as e2m1 codes of a block with scale byte c.  x / s is a value half way
-// between two codes or at least 2^-11 from it (8 bits of x, 4 of s); x times the rounded
-// 1 / s is off by 2^-21, and rounded to a multiple of 2^-14 it is that value again, or on
-// the right side of it.
-__device__ __forceinline__ uint32_t code4(const float (&x)[8], int c) {
-  const float s = scale_value(c);
-  const float by = s > 0.f ? __frcp_rn(s) : 0.f;  // 0 for NaN
+  const uint64_t by2 = f2_pack(by, by);
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)  // zero keeps the sign
-    y[i] = copysignf(__fsub_rn(__fadd_rn(__fmul_rn(x[i], by), 768.f), 768.f), x[i]);
+  for (int i = 0; i < 8; i += 2) f2_unpack(f2_mul(f2_pack(x[i], x[i + 1]), by2), y[i], y[i + 1]);
+  return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+}
+// 1 / s for a block with scale byte c; 0 where s is 0 or NaN, and all codes are 0.
+__device__ __forceinline__ float inverse_scale(int c) {
+  const float s = scale_value(c);
+  return s > 0.f ? __fdividef(1.f, s) : 0.f;
+}
+// 8 bf16 values as e2m1 codes of a block with that inverse scale.  x / s is a value half way
+// between two codes, of 3 bits, or at least 2^-8 of itself from it (8 bits of x, 4 of s); x
+// times 1 / s as the hardware has it is off by 2^-21, and rounded to the 11 bits of fp16 it
+// is that value again, or on the right side of it.
+__device__ __forceinline__ uint32_t code4(const float (&x)[8], float by) {
+  const uint64_t by2 = f2_pack(by, by);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) f2_unpack(f2_mul(f2_pack(x[i], x[i + 1]), by2), y[i], y[i + 1]);
   return e2m1x8(y);
 }
 

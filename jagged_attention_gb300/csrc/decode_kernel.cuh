@@ -624,8 +624,8 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) top = __vmaxu2(top, top_of(w[ks][n][0], w[ks][n][1]));
-      top = __reduce_max_sync(~0u, max(top & 0xffffu, top >> 16));
+        for (int n = 0; n < NT; ++n) top = max_of(top, max_of(w[ks][n][0], w[ks][n][1]));
+      top = __reduce_max_sync(~0u, top_of(top));
       const int e = max(static_cast<int>(top >> 7) - 127 - 14, -126);
       const float by = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), scale_log2);
 #pragma unroll

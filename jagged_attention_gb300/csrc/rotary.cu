@@ -128,69 +128,92 @@ __device__ __forceinline__ void walk_heads(const RowJob& job, int D, int64_t in,
   }
 }
 
+constexpr int kCodedBlocksPerSm = 14, kCodedHeadsAThread = 16;
+
 // As walk_heads, into codes of 8 or 4 bits: what a bf16 cache would hold, quantised.
 // The threads of a row exchange the largest magnitudes of their runs; with 4 bits a
 // scale's 16 values are two runs, r and r ^ 1, which two threads may hold.
-// scales: where those of the row's head 0 go.
+// Whole warps come here, so that lanes exchange without regard to rows; `stores`: whether
+// the thread's row has a slot.  scales: where those of the row's head 0 go.
 template <bool kInterleaved, int kBits>
-__device__ __forceinline__ void walk_coded(const RowJob& job, int D, int64_t in, int64_t out, uint8_t* scales, int h0,
-                                           int h1, int u, int turn_units, bool turn, const float (&c)[8],
+__device__ __forceinline__ void walk_coded(const RowJob& job, int D, int64_t in, int64_t out, int64_t scales, int h0,
+                                           int h1, int u, int turn_units, bool turn, bool stores, const float (&c)[8],
                                            const float (&s)[8]) {
-  const int units = D / 16, lane = threadIdx.x & 31, base = lane & -units;
-  const uint32_t mates = ((1u << units) - 1) << base;
+  const int units = D / 16, base = (threadIdx.x & 31) & -units;
   const int r_lo = u < turn_units ? u : 2 * u, r_hi = u < turn_units ? u + turn_units : 2 * u + 1;
   const int lo = 8 * r_lo, hi = 8 * r_hi;
-  // the thread with run r, and whether it is its second
+  // 4 bits: lane k of a row makes the scale of block k, of runs 2 k and 2 k + 1: who has
+  // those, and how far their magnitudes are shifted in what that lane gives
   auto holder = [&](int r) { return base + (r < turn_units ? r : r < 2 * turn_units ? r - turn_units : r / 2); };
-  auto second = [&](int r) { return r < turn_units ? false : r < 2 * turn_units ? true : (r & 1) != 0; };
-  auto* to = static_cast<unsigned char*>(job.out) + out;
+  auto shift = [&](int r) { return (r < turn_units ? false : r < 2 * turn_units ? true : (r & 1) != 0) ? 16 : 0; };
+  const int from_a = holder(2 * u), from_b = holder(2 * u + 1), shift_a = shift(2 * u), shift_b = shift(2 * u + 1);
+  const auto* p = static_cast<const uint16_t*>(job.in) + in + int64_t(h0) * D;
+  auto* codes = static_cast<unsigned char*>(job.out) + out + h0 * job.out_head;
+  uint8_t* bytes = job.scales + scales + h0 * job.scales_head;
+  Run<false> next_a, next_b;  // the next head's, under way
+  if (h0 < h1) {
+    next_a.load(p, lo);
+    next_b.load(p, hi);
+  }
   for (int h = h0; h < h1; ++h) {
-    Run<false> a, b;
-    a.load(job.in, in + int64_t(h) * D + lo);
-    b.load(job.in, in + int64_t(h) * D + hi);
+    Run<false> a = next_a, b = next_b;
+    p += D;
+    if (h + 1 < h1) {
+      next_a.load(p, lo);
+      next_b.load(p, hi);
+    }
     float x[8], y[8];
-    a.unpack(x);
-    b.unpack(y);
     if (turn) {
+      a.unpack(x);
+      b.unpack(y);
       turn_runs<kInterleaved>(x, y, c, s);
       a.pack(x);  // rounded as in a bf16 cache
       b.pack(y);
-      a.unpack(x);
-      b.unpack(y);
     }
-    uint32_t top_lo = top_of(a.w[0]), top_hi = top_of(b.w[0]);
-    unsigned char* codes = to + h * job.out_head;
-    uint8_t* bytes = scales + h * job.scales_head;
+    const uint32_t max_lo = max_of(a.w[0]), max_hi = max_of(b.w[0]);
+    a.unpack(x);
+    b.unpack(y);
     if (kBits == 8) {
-      uint32_t top = max(top_lo, top_hi);
-      for (int o = 1; o < units; o <<= 1) top = max(top, __shfl_xor_sync(mates, top, o));
-      const int p = power_of(top);
-      *reinterpret_cast<uint2*>(codes + lo) = code8(x, p);
-      *reinterpret_cast<uint2*>(codes + hi) = code8(y, p);
-      if (u == 0) *bytes = static_cast<uint8_t>(p);
+      uint32_t top = top_of(max_of(max_lo, max_hi));
+      top = max(top, __shfl_xor_sync(~0u, top, 1));
+      top = max(top, __shfl_xor_sync(~0u, top, 2));
+      if (units == 8) top = max(top, __shfl_xor_sync(~0u, top, 4));
+      const int byte = power_of(top);
+      const uint2 code_lo = code8(x, byte), code_hi = code8(y, byte);
+      if (stores) {
+        *reinterpret_cast<uint2*>(codes + lo) = code_lo;
+        *reinterpret_cast<uint2*>(codes + hi) = code_hi;
+        if (u == 0) *bytes = static_cast<uint8_t>(byte);
+      }
     } else {
-      const uint32_t both = top_lo | top_hi << 16;
-      const uint32_t of_lo = __shfl_sync(mates, both, holder(r_lo ^ 1)), of_hi = __shfl_sync(mates, both, holder(r_hi ^ 1));
-      top_lo = max(top_lo, second(r_lo ^ 1) ? of_lo >> 16 : of_lo & 0xffffu);
-      top_hi = max(top_hi, second(r_hi ^ 1) ? of_hi >> 16 : of_hi & 0xffffu);
-      const int s_lo = scale_of(top_lo), s_hi = scale_of(top_hi);
-      *reinterpret_cast<uint32_t*>(codes + lo / 2) = code4(x, s_lo);
-      *reinterpret_cast<uint32_t*>(codes + hi / 2) = code4(y, s_hi);
-      if (r_lo % 2 == 0) bytes[r_lo / 2] = static_cast<uint8_t>(s_lo);
-      if (r_hi % 2 == 0) bytes[r_hi / 2] = static_cast<uint8_t>(s_hi);
+      const uint32_t both = top_of(max_lo) | top_of(max_hi) << 16;
+      const int byte = scale_of(max(__shfl_sync(~0u, both, from_a) >> shift_a & 0xffffu,
+                                    __shfl_sync(~0u, both, from_b) >> shift_b & 0xffffu));
+      const float by = inverse_scale(byte);
+      const uint32_t code_lo = code4(x, __shfl_sync(~0u, by, base + r_lo / 2));
+      const uint32_t code_hi = code4(y, __shfl_sync(~0u, by, base + r_hi / 2));
+      if (stores) {
+        *reinterpret_cast<uint32_t*>(codes + lo / 2) = code_lo;
+        *reinterpret_cast<uint32_t*>(codes + hi / 2) = code_hi;
+        bytes[u] = static_cast<uint8_t>(byte);
+      }
     }
+    codes += job.out_head;
+    bytes += job.scales_head;
   }
 }
 
 // kBits: of scattered rows.
 template <bool kInterleaved, int kBits>
-__global__ void __launch_bounds__(kRowThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kRowThreads, kBits == 16 ? kBlocksPerSm : kCodedBlocksPerSm)
 rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
   wait_for_launch_before();
   const int units = a.D / 16;  // threads of a row: 4 or 8
   const int u = threadIdx.x % units;
-  const int64_t row = int64_t(blockIdx.x) * (kRowThreads / units) + threadIdx.x / units;
-  if (row >= a.rows) return;
+  int64_t row = int64_t(blockIdx.x) * (kRowThreads / units) + threadIdx.x / units;
+  const bool here = row < a.rows;
+  if (kBits == 16 && !here) return;
+  if (kBits < 16 && !here) row = a.rows - 1;  // for company
   const int pairs = a.turns.pairs;
   const bool turning = u < pairs / 8;
   // the two runs of 8 values this thread has in every head
@@ -212,7 +235,7 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
 
   bool placed = false;  // whether the row has a slot, and where
   int page = 0, in_page = 0;
-  if (a.slots) {
+  if (a.slots && here) {
     const int slot = a.slots[row];
     if (slot >= a.num_slots) {
       if (u == 0) atomicOr(a.status, kPagerBadPage);
@@ -231,12 +254,13 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
     const RowJob& job = a.job[j];
     const int h0 = max(first - before, 0), h1 = min(last - before, job.heads);
     before += job.heads;
-    if (job.scatter && !placed) continue;
+    if (job.scatter && (kBits == 16 ? !placed : !__any_sync(~0u, placed))) continue;
+    if (kBits < 16 && !job.scatter && !here) continue;
     const int64_t in = row * job.in_row;
     const int64_t out = job.scatter ? page * job.out_page + in_page * job.out_row : row * job.out_row;
     if (kBits < 16 && job.scatter)
-      walk_coded<kInterleaved, kBits>(job, a.D, in, out, job.scales + page * job.scales_page + in_page * job.scales_row, h0,
-                                      h1, u, pairs / 8, turning && job.rotate, c, s);
+      walk_coded<kInterleaved, kBits>(job, a.D, in, out, page * job.scales_page + in_page * job.scales_row, h0, h1, u,
+                                      pairs / 8, turning && job.rotate, placed, c, s);
     else if (job.f32)
       walk_heads<kInterleaved, true>(job, a.D, in, out, h0, h1, lo, hi, turning && job.rotate, c, s);
     else
@@ -256,10 +280,11 @@ cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   // dealt by their number alone: of fp32 and bf16 heads some threads have more weight.
   int64_t weight = 0;
   for (const RowJob& job : a.job) weight += int64_t(job.heads) * (job.f32 ? 2 : 1);
-  const int64_t fill = int64_t(sms) * 1024 / kRowThreads;
+  const int64_t fill = int64_t(sms) * (a.bits == 16 ? kBlocksPerSm : kCodedBlocksPerSm);
+  const int64_t most = a.bits == 16 ? kHeadsAThread : kCodedHeadsAThread;
   constexpr int64_t kMostSplit = 65535;  // the grid's second dimension
   const int split = static_cast<int>(std::min<int64_t>(
-      {a.heads, kMostSplit, std::max({fill / blocks, (weight + kHeadsAThread - 1) / kHeadsAThread, int64_t(1)})}));
+      {a.heads, kMostSplit, std::max({fill / blocks, (weight + most - 1) / most, int64_t(1)})}));
   const int per = (a.heads + split - 1) / split;
   const dim3 grid(static_cast<unsigned>(blocks), (a.heads + per - 1) / per);
   auto kernel = [&](auto bits) {
