@@ -1,20 +1,45 @@
-// decode_coded.cu -- attention over a cache of 8 or 4 bits.
+// decode_coded.cu -- attention over a cache of 8 or 4 bits: how its launches differ.
+#include <algorithm>
+
 #include "decode_kernel.cuh"
 
 namespace jfa {
 
-constexpr int kLineMb = 96, kMatesMb = 2048, kFarMb = 512;
+namespace {
+
+// Memory gives 128 bytes at a time, and gives 256 in a row faster.  Rows of neighbouring
+// heads that lie within so much are read side by side, by warps of one CTA, where there is
+// enough to read; in between the lines are in L2.  That halves the warps along a row and
+// doubles the parts that CTAs join.
+//   rows of 64 and 32 bytes: 96 requests up to 32768 rows, 8 heads: 4 bits of 128 values 394
+//   us, one head after the other 596; 8 bits of 64 values 284 and 531; 128 mixed requests,
+//   126 MB, 41.9 and 43.5; one of 131072 rows, 76 MB, 32 either way; 32 mixed ones, 32 MB,
+//   21.3 and 18.9.
+//   rows of 128 bytes: the full cache of 8 bits 540 us and 605 (of one GPU; of another 539
+//   and 546), 512 mixed requests, 0.9 GB, 152 and 164, 128, 224 MB, 46 either way; one of
+//   131072 rows, 134 MB, 35 and 31.
+constexpr int kLineMb = 96, kPairMb = 256;
+
+// Where so much is read as comes and goes in L2 meanwhile, 4-bit lines are not marked to
+// leave first, or their second reader would miss them: the full cache 394 us, marked 472;
+// 256 mixed requests, 250 MB, 70.2 and 67.7.  Of 8 bits they always are (548 and 540).
+constexpr int kFarMb = 512;
+
+constexpr int kCodedTile = DecodeCfg<8, 128, 1>::kTile;
+static_assert(kCodedTile == DecodeCfg<4, 128, 1>::kTile, "units of either");
+
+}  // namespace
 
 cudaError_t launch_decode_coded(const DecodeArgs& given, int sms, cudaStream_t stream) {
   DecodeArgs a = given;
-  // Rows of neighbouring heads are read side by side where there is enough to read: TODO.
   const int row_bytes = a.D * a.bits / 8, mates = row_bytes < 128 ? 128 / row_bytes : 2;
-  const int64_t least = int64_t(row_bytes < 128 ? kLineMb : kMatesMb) << 20;
+  static_assert(kMostMates >= 128 / (64 * 4 / 8), "room for what mates leave");
   if (a.parts == 1 && a.head == row_bytes && a.Hkv % mates == 0) {
+    const int64_t unit = int64_t(2) * row_bytes * kCodedTile * a.Hkv;  // bytes of a tile of all heads
+    auto units = [&](int mb) { return static_cast<uint32_t>((int64_t(mb) << 20) / unit); };
     a.mates = mates;
-    const int64_t unit = 2 * row_bytes * (a.bits == 8 ? 32 : 64) * a.Hkv;  // of all heads
-    a.mates_units = static_cast<uint32_t>(least / unit);
-    a.far_units = static_cast<uint32_t>((int64_t(kFarMb) << 20) / unit);
+    a.mates_units = units(row_bytes < 128 ? kLineMb : kPairMb);
+    a.far_units = a.bits == 4 ? units(kFarMb) : UINT32_MAX;
   }
   // whether 32 bits hold offsets as the kernel counts them
   const int n = a.bits == 8 ? 1 : a.D / kBlock;

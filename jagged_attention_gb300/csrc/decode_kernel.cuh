@@ -61,7 +61,7 @@ constexpr float kWeightBits = 15.f;  // of codes: the largest weight is 2^15, as
 template <int kBits, int D, int NT>  // NT: tiles of 8 query heads
 struct DecodeCfg {
   static constexpr int kHeads = 8 * NT;
-  static constexpr int kTile = kBits == 4 ? 64 : 32;        // cached rows of a tile
+  static constexpr int kTile = kBits == 16 ? 32 : 64;       // cached rows of a tile
   static constexpr int kSub = kTile / 32;                   // of which a lane looks up so many
   static constexpr int kRowBytes = D * kBits / 8;
   static constexpr int kScaleBytes = kBits == 4 ? D / kBlock : 0;  // of a row, in the stage
@@ -71,7 +71,7 @@ struct DecodeCfg {
   static constexpr int kWarpBytes = kStageBytes + kVBytes + kOutBytes;  // K, V, park
   static constexpr int kWarps = 8;
   static constexpr int kSmemBytes = kWarps * kWarpBytes;
-  static constexpr int kCtasPerSm = D == 64 || (kBits < 16 && NT == 1) ? 2 : 1;
+  static constexpr int kCtasPerSm = D == 64 || (kBits == 4 && NT == 1) ? 2 : 1;
 };
 constexpr int kMostCtasPerSm = 2;
 

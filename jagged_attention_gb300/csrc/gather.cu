@@ -8,8 +8,8 @@
 // and last of them, 32 places of the offsets at a time, and then a lane a row's page; all
 // threads then take 16 values of a row's head of K and of V at a time.
 //
-// Measured (GB300, 6.79 TB/s copied): 394,687 rows of 8 heads, 1.6 GB from 4 bits in 249 us,
-// 6.5 TB/s; from 8 bits, 1.9 GB in 284 us, 6.7 TB/s; 32,657 rows, 171 MB from 4 bits in 33.6
+// Measured (GB300, 6.79 TB/s copied): 394,687 rows of 8 heads, 1.6 GB from 4 bits in 251 us,
+// 6.4 TB/s; from 8 bits, 1.9 GB in 292 us, 6.5 TB/s; 32,657 rows, 171 MB from 4 bits in 33.5
 // us, 5.1 TB/s; 720 rows of 4 heads in 2.2 us, which is the launch.
 #include <algorithm>
 
@@ -20,12 +20,11 @@
 namespace jfa {
 namespace {
 
-constexpr int kGatherThreads = 256;
+constexpr int kGatherThreads = 128;
 constexpr int kGatherRows = 32;    // most packed rows of a block: a lane looks each up
-// Pieces, of 16 values of K and V, that a block has where there are many: the 1.6 GB take
-// 273 us with 256, 255 with 1024 and 249 with 512; with two pieces of a thread under way at
-// a time 261.
-constexpr int kGatherUnits = 512;
+// Pieces, of 16 values of K and V, that a block has where there are many: 1.6 GB from 4
+// bits take 251 us so, with 512 pieces 259, with 256 threads and 512 pieces 263, 1024 260.
+constexpr int kGatherUnits = 256;
 
 // The last b of [0, n) with offsets[b] <= r, for two r at a time; -1 where there is none:
 // 32 places at a time.  Offsets that decrease somewhere give some b of the range.

@@ -144,8 +144,9 @@ struct DecodeArgs {
   int group;                                // H / Hkv
   int parts, together, passes, part_heads;  // QueryParts
   int vheads;           // Hkv * passes: sets of `together` parts
-  int mates;            // key/value heads that may go side by side instead, 1 where none do,
-  uint32_t mates_units, far_units;  // if the requests have so many units; TODO
+  int mates;            // key/value heads that go side by side instead, 1 where none do,
+  uint32_t mates_units; // if the requests have so many units,
+  uint32_t far_units;   // and with so many their lines are not marked to leave L2 first
   int64_t num_pages;
   int max_pages;
   PageDiv div;
