@@ -553,7 +553,8 @@ int jfa_pager_create(int max_seqs, int max_pages, int64_t num_pages, int page_si
  * bits: the largest of a block whose scale was rounded down, and what is beyond 61440).
  * Where a value is NaN or infinite the scale byte is 255, and the row of the head (4
  * bits: the block) reads as NaN.  With 8 bits other bytes outside 79 .. 175 count as the
- * nearest of them.  What a code stands for is exact in bf16.
+ * nearest of them; with 4 bits bytes from 227 to 254 are not to be used (append makes none).
+ * What a code stands for is exact in bf16.
  */
 #define JFA_PAGER_8BIT 1u
 #define JFA_PAGER_4BIT 2u

@@ -626,6 +626,19 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) top = max_of(top, max_of(w[ks][n][0], w[ks][n][1]));
       top = __reduce_max_sync(~0u, top_of(top));
+      if (top >= 0x7f80u) {  // the largest that is finite: heads have their own infinities and NaN
+        top = 0;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t lo = w[ks][n][i] & 0x7fffu, hi = (w[ks][n][i] >> 16) & 0x7fffu;
+              top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+            }
+        top = __reduce_max_sync(~0u, top);
+      }
       const int e = max(static_cast<int>(top >> 7) - 127 - 14, -126);
       const float by = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), scale_log2);
 #pragma unroll

@@ -12,6 +12,7 @@ E4M3 = np.array([m / 8 * 2.0 ** -6 for m in range(8)] +
 E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 SCALES = np.array([m * 2.0 ** -17 for m in range(8)] + [(8 + m) * 2.0 ** (e - 18) for e in range(1, 31) for m in range(8)])
 MOST_SCALE = 10240.0
+FP16_HALF_STEP = torch.finfo(torch.float16).eps / 2  # 2^-11
 
 
 def scale_bytes(bits, D):
@@ -70,7 +71,8 @@ def decode(q, k, v, table, lens, scale):
     additions; exponentials and the running rescale add 2^-17 relative; a sum of n weights
     or weighted values adds 2 n 2^-24.  So far delta; it moves the output by at most
     2 delta sum p |v|, lse by delta.  A weight enters the product with V as one fp16 number:
-    half a step of 11 bits, 2^-12 relative, or half the smallest, 2^-25, where the largest
+    1 + m / 1024 times a power of two, m whole, so steps are 2^-10 of the power and half of
+    one is at most 2^-11 of the weight (finfo.eps / 2); or half the smallest, 2^-25, where the largest
     weight (8 bits: times its row's power of two) is 2^15: 2^-40 of the largest, times codes
     of at most 448, of which a row's largest is above 224."""
     B, H, D = q.shape
@@ -99,7 +101,7 @@ def decode(q, k, v, table, lens, scale):
             size = float((abs(scale) * (kb[:, g].abs() @ q[b, h].abs())).max())
             delta = 2 * D * 2.0 ** -24 * size + 2.0 ** -17 + 2 * n * 2.0 ** -24
             mass = w @ vb[:, g].abs()
-            off[b, h] = (2 * delta + 2.0 ** -12) * mass + n * 2.0 ** -39 * vb[:, g].abs().amax()
+            off[b, h] = (2 * delta + FP16_HALF_STEP) * mass + n * 2.0 ** -39 * vb[:, g].abs().amax()
             off_lse[h, b] = delta + 2.0 ** -23 * abs(float(lse[h, b]))
     step = torch.finfo(torch.bfloat16).eps / 2
     return out, lse, off * (1 + step) + step * out.abs(), off_lse

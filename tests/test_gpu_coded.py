@@ -374,6 +374,21 @@ def test_decode_huge_and_tiny_queries(bits):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_decode_queries_that_are_not_finite(bits, bad):
+    """One head's infinities and NaN leave the heads beside it, of the same keys, as they are."""
+    pager, held, table, dl = _case([300, 40, 1], 12, 2, 64, 16, "rows", bits, 9)
+    q = _draw((3, 12, 64), 2)
+    want = jfa.paged_decode(pager, q, *held[:2], table, dl, 0.1, **_scales(held))
+    q[0, 3, 5], q[1, 7, 63], q[2, 0] = bad, bad, bad
+    hit = torch.zeros((3, 12), dtype=torch.bool, device="cuda")
+    hit[0, 3] = hit[1, 7] = hit[2, 0] = True
+    out, lse = jfa.paged_decode(pager, q, *held[:2], table, dl, 0.1, **_scales(held))
+    assert torch.equal(out[~hit], want[0][~hit]) and torch.equal(lse.T[~hit], want[1].T[~hit])
+    assert not torch.isfinite(lse.T[hit]).any()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("lens", [[1], [2, 0, 31], [300, 17], [9000, 40, 1]], ids=str)
 @pytest.mark.parametrize("hq,hk,D", [(1, 1, 64), (4, 2, 128), (24, 1, 64)])
 def test_decode_nan_rows(bits, lens, hq, hk, D):
@@ -446,6 +461,127 @@ def test_past_32_bit_offsets(bits, layout):
     out, lse = jfa.paged_decode(pager, q, *held[:2], table, lens, 0.09, **_scales(held))
     ref, ref_lse, off, off_lse = coded_ref.decode(q, kp.cpu().double(), vp.cpu().double(), _ints(np.stack([np.arange(11)] * 2)), lens, 0.09)
     assert ((out.cpu().double() - ref).abs() <= off).all() and ((lse.cpu().double() - ref_lse).abs()[:, 0] <= off_lse[:, 0]).all()
+
+
+def _check_on_the_gpu(pager, held, table, lens, q, scale):
+    """decode against 64 bits over the rows that gather reads back, a request at a time, within coded_ref's bounds."""
+    out, lse = jfa.paged_decode(pager, q, *held[:2], table, lens, scale, **_scales(held))
+    again = jfa.paged_decode(pager, q, *held[:2], table, lens, scale, **_scales(held))
+    assert pager.status() == 0 and torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    group, D, step = pager.H // pager.Hkv, pager.D, torch.finfo(BF16).eps / 2
+    for b, n in enumerate(lens.tolist()):
+        if n == 0:
+            assert not out[b].any() and (lse[:, b] == -math.inf).all()
+            continue
+        k, v = jfa.paged_gather(pager, *held[:2], table[b:b + 1], _ints([0, n]), rows=n, **_scales(held))
+        for g in range(pager.Hkv):
+            heads = slice(g * group, (g + 1) * group)
+            kd, vd, qd = k[:, g].double(), v[:, g].double(), q[b, heads].double()
+            s = scale * qd @ kd.T
+            w, ref = torch.softmax(s, 1), torch.logsumexp(s, 1)
+            size = (abs(scale) * qd.abs() @ kd.abs().T).amax(1)
+            delta = 2 * D * 2.0 ** -24 * size + 2.0 ** -17 + 2 * n * 2.0 ** -24
+            want = w @ vd
+            off = (2 * delta + coded_ref.FP16_HALF_STEP)[:, None] * (w @ vd.abs()) + n * 2.0 ** -39 * vd.abs().amax()
+            assert ((out[b, heads].double() - want).abs() <= off * (1 + step) + step * want.abs()).all()
+            assert ((lse[heads, b].double() - ref).abs() <= delta + 2.0 ** -23 * ref.abs()).all()
+
+
+@pytest.mark.parametrize("bits,D,hk,group,mb", [
+    (4, 128, 8, 2, 100), (4, 128, 2, 12, 100), (4, 128, 4, 8, 530), (4, 64, 4, 3, 100), (4, 64, 8, 16, 540),
+    (8, 64, 2, 4, 100), (8, 64, 4, 9, 100), (8, 128, 2, 8, 270), (8, 128, 4, 11, 270), (4, 128, 3, 4, 120),
+    (8, 128, 1, 8, 270)])
+@pytest.mark.parametrize("few", [True, False])
+def test_decode_heads_side_by_side(bits, D, hk, group, mb, few):
+    """As much to read as makes neighbouring heads go side by side, and stay in L2; few long requests and many."""
+    page, row = 16, D * bits // 8
+    rows = (mb << 20) // (2 * hk * row)
+    rng = np.random.default_rng(rows)
+    B = 5 if few else 70
+    lens = rng.dirichlet(np.full(B, 0.7)) * rows
+    lens = np.maximum(lens.astype(np.int64), 0)
+    lens[0], lens[-1] = 0, rows - lens[1:-1].sum()
+    count = -(-lens // page)
+    width, num_pages = int(count.max()), int(count.sum())
+    pager = jfa.Pager(max_seqs=B, max_pages=width, num_pages=num_pages, page_size=page, H=hk * group, Hkv=hk, D=D, bits=bits)
+    held = pager.pages()
+    table, order, at = np.full((B, width), -1), rng.permutation(num_pages), 0
+    for b, n in enumerate(count):
+        table[b, :n] = order[at:at + n]
+        at += n
+    slots = torch.arange(num_pages * page, device="cuda", dtype=I32)
+    for i in range(0, len(slots), 1 << 17):
+        part = slots[i:i + (1 << 17)]
+        jfa.paged_append(pager, _draw((len(part), hk, D), i), _draw((len(part), hk, D), i + 1), part, *held[:2], **_scales(held))
+    _check_on_the_gpu(pager, held, _ints(table), _ints(lens), _draw((B, hk * group, D), 5), D ** -0.5)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("hq,hk,D", [(16, 8, 64), (32, 2, 64), (40, 2, 64), (10, 2, 128), (32, 2, 128), (70, 2, 128)])
+def test_decode_tables_wide_enough_for_64_bit_counts(bits, hq, hk, D):
+    """A table of which full rows would hold more tiles than 32 bits count."""
+    pager, held, table, lens = _case([300, 5000, 0, 17], hq, hk, D, 1024, "rows", bits, 12)
+    q = _draw((4, hq, D), 1)
+    pages = (1 << 21) - 2
+    wide = torch.full((130, pages), -1, dtype=I32, device="cuda")  # 1.1 GB; only the rows of 130 requests count
+    wide[:4, :table.shape[1]] = table
+    big = jfa.Pager(max_seqs=130, max_pages=pages, num_pages=pager.num_pages, page_size=1024, H=hq, Hkv=hk, D=D, bits=bits)
+    assert 130 * (pages * 1024 // 64) > 2**32 // hk
+    many, some = torch.zeros((130, hq, D), dtype=BF16, device="cuda"), torch.zeros(130, dtype=I32, device="cuda")
+    many[:4], some[:4] = q, lens
+    out, lse = jfa.paged_decode(big, many, *held[:2], wide, some, 0.1, **_scales(held))
+    assert big.status() == 0 and not out[4:].any() and (lse[:, 4:] == -math.inf).all()
+    ref, ref_lse, off, off_lse = coded_ref.decode(q, *_values(held, bits), table, lens, 0.1)
+    assert ((out[:4].cpu().double() - ref).abs() <= off).all()
+    fine = ~torch.isinf(ref_lse)
+    assert ((lse[:, :4].cpu().double() - ref_lse).abs()[fine] <= off_lse[fine]).all()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (6, 2)])
+def test_decode_the_most_requests(bits, hq, hk):
+    """16384 requests of 0 to 40 rows, a page of 40 each, in the bounds of coded_ref, all at once."""
+    B, page, D = 16384, 40, 64
+    rng = np.random.default_rng(1)
+    lens, order = rng.integers(0, page + 1, B), rng.permutation(B)
+    pager = jfa.Pager(max_seqs=B, max_pages=1, num_pages=B, page_size=page, H=hq, Hkv=hk, D=D, bits=bits)
+    held = pager.pages()
+    slots = torch.arange(B * page, device="cuda", dtype=I32)
+    jfa.paged_append(pager, _draw((B * page, hk, D), 1), _draw((B * page, hk, D), 2), slots, *held[:2], **_scales(held))
+    q, table, dl = _draw((B, hq, D), 3), _ints(order[:, None]), _ints(lens)
+    out, lse = jfa.paged_decode(pager, q, *held[:2], table, dl, 0.125, **_scales(held))
+    k, v = jfa.paged_gather(pager, *held[:2], table, _ints(np.arange(B + 1) * page), rows=B * page, **_scales(held))
+    assert pager.status() == 0
+    k, v = (x.view(B, page, hk, D).double().repeat_interleave(hq // hk, 2) for x in (k, v))
+    s = 0.125 * torch.einsum("bhd,bthd->bht", q.double(), k)
+    size = 0.125 * torch.einsum("bhd,bthd->bht", q.double().abs(), k.abs()).amax(-1)
+    dead = torch.arange(page, device="cuda")[None, None] >= dl[:, None, None]
+    w = torch.softmax(s.masked_fill(dead, -math.inf), -1).nan_to_num(0.0)
+    want, mass = torch.einsum("bht,bthd->bhd", w, v), torch.einsum("bht,bthd->bhd", w, v.abs())
+    delta = (2 * D * 2.0 ** -24 * size + 2.0 ** -17 + 2 * page * 2.0 ** -24)[..., None]
+    step = torch.finfo(BF16).eps / 2
+    off = (2 * delta + coded_ref.FP16_HALF_STEP) * mass + page * 2.0 ** -39 * v.abs().amax((1, 3))[..., None]
+    assert ((out.double() - want).abs() <= off * (1 + step) + step * want.abs()).all()
+    ref = torch.logsumexp(s.masked_fill(dead, -math.inf), -1)
+    some = (dl > 0)[:, None].expand_as(ref)
+    assert ((lse.T.double() - ref).abs()[some] <= (delta[..., 0] + 2.0 ** -23 * ref.abs())[some]).all()
+    assert (lse.T[~some] == -math.inf).all()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_two_pagers_on_two_streams(bits):
+    pager, held, table, lens = _case([2000, 300, 64, 5], 8, 2, 128, 16, "rows", bits, 9)
+    other = jfa.Pager(max_seqs=4, max_pages=pager.max_pages, num_pages=pager.num_pages, page_size=16, H=8, Hkv=2, D=128, bits=bits)
+    q = _draw((4, 8, 128), 1)
+    want, _ = jfa.paged_decode(pager, q, *held[:2], table, lens, 0.1, **_scales(held))
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(30):
+        for s, p, o in zip(streams, (pager, other), outs):
+            with torch.cuda.stream(s):
+                o.append(jfa.paged_decode(p, q, *held[:2], table, lens, 0.1, **_scales(held))[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for o in outs for x in o)
 
 
 @pytest.mark.parametrize("bits", [8, 4])
