@@ -77,8 +77,11 @@ constexpr int kMostCtasPerSm = 2;
 
 // Units of work: the n tiles of a (request, key/value head) count n units, and
 // kRowUnits behind them stand for its beginning and end (256 requests up to 300
-// rows: 34.6 us without, 32.5 with; 128 mixed ones 74.7 and 74.2).
-constexpr int kRowUnits = 2;
+// rows: 34.6 us without, 32.5 with; 128 mixed ones 74.7 and 74.2).  Of codes, whose tiles
+// are larger, one: 500 requests up to 900 rows in 4 bits 55.7 us, with two 59.0, none 60.8,
+// 512 mixed ones in 8 bits 147, 152 and 149.
+template <int kBits>
+constexpr int kRowUnits = kBits == 16 ? 2 : 1;
 
 // Parts of a row that one CTA joins at a time, where a row has more than three times
 // as many (38 parts of 16 heads: 22.9 us, all at once 28.7; up to 24 parts it makes
@@ -315,7 +318,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   for (int b = b_lo; b < b_hi; ++b) {
     last_len = length_of(a, b);
     const int n = tiles_of<C::kTile>(last_len);
-    units += n > 0 ? n + kRowUnits : 0;
+    units += n > 0 ? n + kRowUnits<kBits> : 0;
     rows += n > 0;
     most = max(most, n);
   }
@@ -367,7 +370,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     units_to = U(rows_to) * U(most);
     total = U(all_rows) * U(most);
   }
-  auto units_of = [&](int n) -> U { return n == 0 ? 0 : apart ? most : n + kRowUnits; };
+  auto units_of = [&](int n) -> U { return n == 0 ? 0 : apart ? most : n + kRowUnits<kBits>; };
   total *= vheads;
   // fewer CTAs than there are where each warp, or few of them, would not have a unit
   const int least_bits = kBits == 16 ? sub_bits : min(sub_bits, kLeastBits);
@@ -1213,7 +1216,7 @@ cudaError_t launch_by_size(const DecodeArgs& a, int sms, cudaStream_t stream, bo
   // the units of B full table rows
   constexpr int kTile = DecodeCfg<kBits, 128, 1>::kTile;
   static_assert(kTile == DecodeCfg<kBits, 64, 2>::kTile, "tiles go by the bits alone");
-  const int64_t most = int64_t(a.B) * (int64_t(a.max_pages) * a.div.d / kTile + 1 + kRowUnits);
+  const int64_t most = int64_t(a.B) * (int64_t(a.max_pages) * a.div.d / kTile + 1 + kRowUnits<kBits>);
   if (wide || most > UINT32_MAX / a.vheads)
     return a.D == 128 ? launch_by_heads<kBits, 128, uint64_t>(a, sms, stream) : launch_by_heads<kBits, 64, uint64_t>(a, sms, stream);
   return a.D == 128 ? launch_by_heads<kBits, 128, uint32_t>(a, sms, stream) : launch_by_heads<kBits, 64, uint32_t>(a, sms, stream);
