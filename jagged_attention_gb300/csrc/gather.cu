@@ -8,9 +8,9 @@
 // and last of them, 32 places of the offsets at a time, and then a lane a row's page; all
 // threads then take 16 values of a row's head of K and of V at a time.
 //
-// Measured (GB300, 6.79 TB/s copied): 394,687 rows of 8 heads, 1.6 GB from 4 bits in 251 us,
-// 6.4 TB/s; from 8 bits, 1.9 GB in 292 us, 6.5 TB/s; 32,657 rows, 171 MB from 4 bits in 33.5
-// us, 5.1 TB/s; 720 rows of 4 heads in 2.2 us, which is the launch.
+// Measured (GB300, 6.79 TB/s copied): 394,687 rows of 8 heads, 1.6 GB from 4 bits in 240 us,
+// 6.7 TB/s; from 8 bits, 1.9 GB in 279 us, 6.8 TB/s; 32,657 rows, 171 MB from 4 bits in 30.5
+// us, 5.6 TB/s; 720 rows of 4 heads in 2.1 us, which is the launch.
 #include <algorithm>
 
 #include "coded.cuh"
@@ -22,8 +22,8 @@ namespace {
 
 constexpr int kGatherThreads = 128;
 constexpr int kGatherRows = 32;    // most packed rows of a block: a lane looks each up
-// Pieces, of 16 values of K and V, that a block has where there are many: 1.6 GB from 4
-// bits take 251 us so, with 512 pieces 259, with 256 threads and 512 pieces 263, 1024 260.
+// Pieces, of 16 values of K and V, that a block has where there are many: 12,000 rows of 3
+// heads take 5.1 us so, with 512 pieces 5.7; 394,687 of 8 heads 240 and 241.
 constexpr int kGatherUnits = 256;
 
 // The last b of [0, n) with offsets[b] <= r, for two r at a time; -1 where there is none:
@@ -47,8 +47,11 @@ __device__ __forceinline__ void requests_of(const int32_t* offsets, int n, const
 }
 
 template <int kBits>
-__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ GatherArgs a, int block_rows) {
-  __shared__ int page_of[kGatherRows], row_of[kGatherRows];  // page -1: zeros, -2: the row stays as it was
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ GatherArgs a, int block_rows,
+                                                               const __grid_constant__ PageDiv per_row, bool whole) {
+  // Where a row's head 0 and its scale bytes are; codes kZeros: zeros, kLeft: the row stays as it was.
+  constexpr int64_t kZeros = -1, kLeft = -2;
+  __shared__ int64_t codes_at[kGatherRows], scales_at[kGatherRows];
   wait_for_launch_before();
   const int64_t r0 = int64_t(blockIdx.x) * block_rows;
   const int rows = static_cast<int>(min(int64_t(block_rows), a.rows - r0));
@@ -65,37 +68,38 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
         b[1] = mid - 1;
     }
     const int64_t from = a.offsets[b[0]], to = a.offsets[b[0] + 1];
-    int page = -2, in_page = 0;
+    int64_t codes = kLeft, scales = 0;
     if (r >= from && r < to) {
       const int64_t pos = int64_t(a.starts ? a.starts[b[0]] : 0) + r - from;
-      page = -1;
+      codes = kZeros;
       if (pos < 0 || pos >= int64_t(a.max_pages) * a.div.d) {
         atomicOr(a.status, kPagerBadLength);
       } else {
-        const int t = a.div.quot(static_cast<int>(pos));
-        page = a.table[b[0] * a.table_row + t];
-        in_page = static_cast<int>(pos) - t * a.div.d;
+        const int t = a.div.quot(static_cast<int>(pos)), in_page = static_cast<int>(pos) - t * a.div.d;
+        const int page = a.table[b[0] * a.table_row + t];
         if (page < 0 || page >= a.num_pages) {
           atomicOr(a.status, kPagerBadPage);
-          page = -1;
+        } else {
+          codes = page * a.page + in_page * a.row;
+          scales = page * a.scales.page + in_page * a.scales.row;
         }
       }
     }
-    page_of[lane] = page;
-    row_of[lane] = in_page;
+    codes_at[lane] = codes;
+    scales_at[lane] = scales;
     if (blockIdx.x == 0 && lane == 0 && a.offsets[a.B] > a.rows) atomicOr(a.status, kPagerBadLength);
   }
   __syncthreads();
-  const int runs = a.D / 16, per_row = a.Hkv * runs;
-  for (int i = threadIdx.x; i < rows * per_row; i += kGatherThreads) {
-    const int row = i / per_row, h = (i - row * per_row) / runs, u = i % runs;
-    const int page = page_of[row];
-    if (page == -2) continue;
+  const int run_bits = a.D == 128 ? 3 : 2;  // a head's pieces
+  for (int i = threadIdx.x; i < rows * per_row.d; i += kGatherThreads) {
+    const int row = per_row.quot(i), place = i - row * per_row.d, h = place >> run_bits, u = place & ((1 << run_bits) - 1);
+    const int64_t from_row = codes_at[row];
+    if (from_row == kLeft) continue;
     uint4 c[2][kBits == 16 ? 2 : 1] = {};  // 16 codes of K and of V
     int byte[2] = {};
-    if (page >= 0) {
-      const int64_t at = page * a.page + row_of[row] * a.row + h * a.head + u * (2 * kBits);
-      const int64_t scales = page * a.scales.page + row_of[row] * a.scales.row + h * a.scales.head + (kBits == 4 ? u : 0);
+    if (from_row != kZeros) {
+      const int64_t at = from_row + h * a.head + u * (2 * kBits);
+      const int64_t scales = scales_at[row] + h * a.scales.head + (kBits == 4 ? u : 0);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const unsigned char* from = (x ? a.v : a.k) + at;
@@ -132,9 +136,14 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
         lo = make_uint4(bf16_of(w[0], by), bf16_of(w[1], by), bf16_of(w[2], by), bf16_of(w[3], by));
         hi = make_uint4(bf16_of(w[4], by), bf16_of(w[5], by), bf16_of(w[6], by), bf16_of(w[7], by));
       }
-      uint4* to = reinterpret_cast<uint4*>((x ? a.v_out + (r0 + row) * a.v_row : a.k_out + (r0 + row) * a.k_row) + h * a.D + 16 * u);
-      to[0] = lo;
-      to[1] = hi;
+      uint4* to = reinterpret_cast<uint4*>((x ? a.v_out + (r0 + row) * a.v_row : a.k_out + (r0 + row) * a.k_row) + 16 * place);
+      if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(lo.x), "r"(lo.y), "r"(lo.z),
+                     "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+      } else {
+        to[0] = lo;
+        to[1] = hi;
+      }
     }
   }
 }
@@ -144,12 +153,15 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
 cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream) {
   // As many rows to a block as have that many pieces, fewer where that would not make two
   // blocks an SM: 64 rows of 8 heads take 2.3 us so, with 16 rows a block 6.0.
-  const int64_t per_row = int64_t(a.Hkv) * (a.D / 16);
-  const int64_t few = a.rows / (2 * sms), many = std::max<int64_t>(1, kGatherUnits / per_row);
+  const int per_row = a.Hkv * (a.D / 16);
+  const int64_t few = a.rows / (2 * sms), many = std::max(1, kGatherUnits / per_row);
   const int block_rows = static_cast<int>(std::max<int64_t>(1, std::min({few, many, int64_t(kGatherRows)})));
+  // A piece's 32 bytes go out at once where they are a sector of memory: 1.6 GB from 4 bits
+  // take 240 us so, in halves 297.
+  const bool whole = (reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.v_out) | 2 * a.k_row | 2 * a.v_row) % 32 == 0;
   const dim3 grid(static_cast<unsigned>((a.rows + block_rows - 1) / block_rows));
   auto* kernel = a.bits == 8 ? gather_kernel<8> : a.bits == 4 ? gather_kernel<4> : gather_kernel<16>;
-  return launch_overlapped(kernel, grid, kGatherThreads, 0, stream, a, block_rows);
+  return launch_overlapped(kernel, grid, kGatherThreads, 0, stream, a, block_rows, make_page_div(per_row), whole);
 }
 
 }  // namespace jfa

@@ -220,8 +220,13 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
   const int lo = turning ? 8 * u : 2 * pairs + 16 * (u - pairs / 8);
   const int hi = turning ? lo + pairs : lo + 8;
 
+  const int first = blockIdx.y * heads_per_block;
+  const int last = min(a.heads, first + heads_per_block);
+  // of codes, blocks without a head that turns form no sines
+  const bool sines = kBits == 16 || first < (a.job[0].rotate ? a.job[0].heads : 0) || last > a.job[0].heads + a.job[1].heads;
+
   float c[8], s[8];
-  if (turning) {
+  if (turning && sines) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int pair = !kInterleaved ? lo + i : i < 4 ? lo / 2 + i : hi / 2 + i - 4;
@@ -246,8 +251,6 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
     }
   }
 
-  const int first = blockIdx.y * heads_per_block;
-  const int last = min(a.heads, first + heads_per_block);
   int before = 0;
 #pragma unroll
   for (int j = 0; j < 3; ++j) {

@@ -243,6 +243,23 @@ def test_gather(bits, lens, hk, D, page, layout):
 
 
 @pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("k_off,v_off,gap", [(8, 0, 0), (0, 24, 0), (16, 16, 8), (0, 0, 24), (16, 32, 16)])
+def test_gather_to_any_16_bytes(bits, k_off, v_off, gap):
+    """Outputs that begin at, and have rows, multiples of 16 bytes apart, not of 32."""
+    pager, held, table, dl = _case([70, 0, 33], 2, 2, 64, 16, "rows", bits, 3)
+    row, n = 2 * 64 + gap, 103
+    bufs = [torch.full((n * row + 64,), 7.0, dtype=BF16, device="cuda") for _ in range(2)]
+    outs = [x[off:].as_strided((n, 2, 64), (row, 64, 1)) for x, off in zip(bufs, (k_off, v_off))]
+    assert outs[0].data_ptr() % 32 == 2 * k_off % 32
+    want = jfa.paged_gather(pager, *held[:2], table, _ints([0, 70, 70, 103]), rows=n, **_scales(held))
+    jfa.paged_gather(pager, *held[:2], table, _ints([0, 70, 70, 103]), rows=n, **_scales(held), k_out=outs[0], v_out=outs[1])
+    for x, off, out, w in zip(bufs, (k_off, v_off), outs, want):
+        assert torch.equal(out, w)
+        out.fill_(7.0)
+        assert (x == 7.0).all()  # nothing beside
+
+
+@pytest.mark.parametrize("bits", [16, 8, 4])
 def test_gather_of_any_bytes(bits):
     """What is not written by append reads as it says: NaN, other bytes as the nearest power, all codes."""
     hk, D, page, n = 2, 64, 16, 300
