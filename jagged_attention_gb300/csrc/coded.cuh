@@ -87,7 +87,9 @@ __device__ __forceinline__ uint2 code8(const float (&x)[8], int c) {
 // 1 / s for a block with scale byte c; 0 where s is 0 or NaN, and all codes are 0.
 __device__ __forceinline__ float inverse_scale(int c) {
   const float s = scale_value(c);
-  return s > 0.f ? __fdividef(1.f, s) : 0.f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));  // a unit in the last place
+  return s > 0.f ? r : 0.f;
 }
 // 8 bf16 values as e2m1 codes of a block with that inverse scale.  x / s is a value half way
 // between two codes, of 3 bits, or at least 2^-8 of itself from it (8 bits of x, 4 of s); x

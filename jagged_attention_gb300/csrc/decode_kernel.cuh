@@ -9,15 +9,28 @@
 // as its own rounding to bf16 does, and saves 0.5% of the time (9% at G = 24).
 // Both are above 0 where the weight is, so that an infinite value of V stays one.
 //
+// Codes (coded.cuh) become fp16 on their way from shared memory to the tensor cores, which
+// is exact: cvt takes two e4m3 or e2m1 codes, 4-bit ones are then multiplied by their
+// scale.  q becomes fp16 too, times a power of two that leaves its 8 bits.  8 bits: with
+// 2^e_t and 2^f_t the powers of two of row t of K and V, s_t = scale 2^e_t q . c_t and
+//     out = sum 2^(s_t + f_t - r) c'_t / sum 2^(s_t - r)   (s_t in units of log2 e),
+// where r is the running maximum of s_t + f_t rather than of s_t: the weights of the codes
+// are then at most 1 whatever the rows' sizes, and those of the sum within 2^48 of that.
+// A weight enters the product as one fp16 number of 11 bits, times 2^15 so that it is not
+// subnormal before 2^-29 of the largest; its rounding, 2^-11 at most, is an eighth of that
+// of the output to bf16, and a second number would cost as many products again.
+//
 // Bound: every cached row is read once, 4 D bytes for 4 D G flops (G query heads
 // to a key/value head), so memory bandwidth bounds it while G is small.  The
 // products use mma.sync, transposed -- rows of the cache are the long side of the
 // 16 x 8 tile, up to 8 query heads (16: two tiles) the short one -- which wastes
 // least of the tile and leaves the cache rows in the layout that ldmatrix reads;
 // tcgen05 would want 64 or 128 query rows per product.  The tensor pipe is 12%
-// busy at G = 8.
+// busy at G = 8.  Of 4-bit codes the conversions (an instruction for two values, one for
+// their scale) and the rest of a value's instructions bound it before memory does: a
+// tile of 64 rows takes 1,360 instructions, 9,216 bytes.
 //
-// Split: a tile is 32 cached rows for one key/value head.  All tiles of all
+// Split: a tile is 32 cached rows (of codes 64) for one key/value head.  All tiles of all
 // requests in the order (request, head, row) are dealt in equal contiguous shares
 // to the CTAs, and a CTA's share to its warps; a warp streams its tiles by
 // cp.async through a stage for K and one for V -- the next K is on its way while V
@@ -41,6 +54,15 @@
 // joining, and SMs whose memory is 7% slower than others'.  128 KB of K and V in
 // the stages of 8 warps measured best: with 192 KB the full cache took 1126 us for
 // 1070, with 6 warps 1094 for 1064.
+//
+// Codes, same GPU as the above: the full cache, 3.6 GB of 8 bits in 526 to 541 us, 6.9 to 6.7
+// TB/s; 2.0 GB of 4 bits in 394 us, 5.1 TB/s (by heads outside rows 389); 128 mixed requests, 224 MB
+// in 45 us and 126 MB in 41; one of 131072, 76 MB of 4 bits in 30 us; one of 300 rows in 6.3.
+// Codes in the warps' registers want tiles of 64 rows: of 32 the full caches take 590 and 417 us.
+// 4 bits run best with 16 warps an SM of 128 registers each; with 8 of 255 they take 8% fewer
+// instructions and 415 us.  Scores of two groups of 16 rows are summed side by side (4% of the
+// full cache of 4 bits).  Bit moves in place of cvt are slower, and so are 4-bit integers
+// (values per clock of an SM, conversion and product alone: e2m1 62, 4-bit integers 45).
 #pragma once
 #include <climits>
 #include <type_traits>
