@@ -93,7 +93,10 @@ struct DecodeCfg {
   static constexpr int kWarpBytes = kStageBytes + kVBytes + kOutBytes;  // K, V, park
   static constexpr int kWarps = 8;
   static constexpr int kSmemBytes = kWarps * kWarpBytes;
-  static constexpr int kCtasPerSm = D == 64 || (kBits == 4 && NT == 1) ? 2 : 1;
+  // 8 bits of 64 values with 16 heads a warp: 380 us for the full cache so, with two CTAs of
+  // 128 registers, which spill, 568; 4 bits 377 and 333.
+  static constexpr int kCtasPerSm = kBits == 16 ? (D == 64 ? 2 : 1) : kBits == 8 ? (D == 64 && NT == 1 ? 2 : 1)
+                                                                              : (D == 64 || NT == 1 ? 2 : 1);
 };
 constexpr int kMostCtasPerSm = 2;
 
