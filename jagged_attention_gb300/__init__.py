@@ -33,6 +33,7 @@ The same from a cache of 8 or 4 bits, and its rows read back for the forward of 
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
 from pathlib import Path
 
@@ -94,6 +95,9 @@ class _Pages(ctypes.Structure):
 class _Scales(ctypes.Structure):
     """jfa_scales"""
     _fields_ = _Pages._fields_
+
+
+_packed = struct.Struct("@5q").pack  # either, in a quarter of the time: ctypes takes bytes for a pointer
 
 
 
@@ -767,8 +771,9 @@ class Pager:
             pass
 
 
-def _pages(pager: Pager, k_pages, v_pages) -> _Pages:
-    return _Pages(*_pair("pages", k_pages, v_pages, pager._pages_shape, pager._pages_dtype, pager.index))
+def _pages(pager: Pager, k_pages, v_pages) -> bytes:
+    """jfa_pages."""
+    return _packed(*_pair("pages", k_pages, v_pages, pager._pages_shape, pager._pages_dtype, pager.index))
 
 
 def _pair(what: str, k, v, shape, dtype, dev: int) -> tuple:
@@ -792,7 +797,7 @@ def _scales(pager: Pager, k_scales, v_scales):
         if k_scales is None and v_scales is None:
             return None
     elif k_scales is not None and v_scales is not None:
-        return ctypes.byref(_Scales(*_pair("scales", k_scales, v_scales, pager._scales_shape, torch.uint8, pager.index)))
+        return _packed(*_pair("scales", k_scales, v_scales, pager._scales_shape, torch.uint8, pager.index))
     raise ValueError(f"a cache of {pager.bits} bits {'has no' if pager.bits == 16 else 'needs'} k_scales and v_scales")
 
 
@@ -855,12 +860,15 @@ def paged_append(pager: Pager, k, v, slots, k_pages, v_pages, *, k_scales=None, 
         q_shape = (rows, pager.H, pager.D)
         if q_out is None:
             q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=pager.device)
-        q_args = (*_rows("q", q, q_shape, torch.bfloat16, dev), *_rows("q_out", q_out, q_shape, torch.bfloat16, dev))
+            to_q = q_out.data_ptr(), pager.H * pager.D
+        else:
+            to_q = _rows("q_out", q_out, q_shape, torch.bfloat16, dev)
+        q_args = (*_rows("q", q, q_shape, torch.bfloat16, dev), *to_q)
     elif q_out is not None:
         raise ValueError("q_out without q")
     rc = (_lib or lib()).jfa_paged_append_ex(
         pager.handle, rows, *_rows("k", k, shape, torch.bfloat16, dev), *_rows("v", v, shape, torch.bfloat16, dev),
-        _ints("slots", slots, rows, dev), ctypes.byref(_pages(pager, k_pages, v_pages)),
+        _ints("slots", slots, rows, dev), _pages(pager, k_pages, v_pages),
         _scales(pager, k_scales, v_scales), rot, *pos, *q_args, pager._launch_stream())
     if rc:
         _check(rc, "jfa_paged_append_ex")
@@ -893,7 +901,7 @@ def paged_gather(pager: Pager, k_pages, v_pages, table, offsets, *, rows: int, s
     else:
         to_v = _rows("v_out", v_out, shape, torch.bfloat16, dev)
     rc = (_lib or lib()).jfa_paged_gather(
-        pager.handle, B, ctypes.byref(_pages(pager, k_pages, v_pages)), _scales(pager, k_scales, v_scales),
+        pager.handle, B, _pages(pager, k_pages, v_pages), _scales(pager, k_scales, v_scales),
         *_table(table, pager, B, dev), None if starts is None else _ints("starts", starts, B, dev),
         _ints("offsets", offsets, B + 1, dev), rows, *to_k, *to_v, pager._launch_stream())
     if rc:
@@ -924,7 +932,7 @@ def paged_decode(pager: Pager, q, k_pages, v_pages, table, lens, scale: float, *
     if out_row != H * D:
         raise ValueError("out must be contiguous")
     rc = (_lib or lib()).jfa_paged_decode_ex(
-        pager.handle, B, *q_at, ctypes.byref(_pages(pager, k_pages, v_pages)), _scales(pager, k_scales, v_scales),
+        pager.handle, B, *q_at, _pages(pager, k_pages, v_pages), _scales(pager, k_scales, v_scales),
         *_table(table, pager, B, dev), _ints("lens", lens, B, dev), float(scale), out_at, lse.data_ptr(),
         pager._launch_stream())
     if rc:

@@ -101,6 +101,17 @@ bool apart(const void* p, const void* q, int64_t rows, int64_t n, int64_t q_row)
   return at + 2 * Wide(rows) * n <= from || from + 2 * (Wide(rows - 1) * q_row + n) <= at;
 }
 
+// Whether two outputs of `rows` rows of n bf16 values overlap nowhere: apart as a whole, or
+// side by side in rows the same distance apart (of a fused tensor, say).
+bool side_by_side(const void* p, int64_t p_row, const void* q, int64_t q_row, int64_t rows, int64_t n) {
+  using Wide = unsigned __int128;
+  const Wide a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  if (a + 2 * (Wide(rows - 1) * p_row + n) <= b || b + 2 * (Wide(rows - 1) * q_row + n) <= a) return true;
+  if (p_row != q_row) return false;
+  const Wide row = 2 * Wide(p_row), d = (a < b ? b - a : a - b) % row;
+  return d >= 2 * Wide(n) && d + 2 * Wide(n) <= row;
+}
+
 int check_pages(const jfa_pages* g) {
   if (!g || !g->k || !g->v || g->page < 0 || g->row < 0 || g->head < 0) return JFA_ERR_INVALID_ARG;
   if (!aligned(g->k, 16) || !aligned(g->v, 16) || g->page % 8 || g->row % 8 || g->head % 8)
@@ -450,6 +461,7 @@ int jfa_paged_gather(jfa_pager_t pager, int B, const jfa_pages* pages, const jfa
   if (int rc = check_cache(pager, pages, scales)) return rc;
   if (int rc = check_rows(k_out, k_row, pager->Hkv, pager->D, false)) return rc;
   if (int rc = check_rows(v_out, v_row, pager->Hkv, pager->D, false)) return rc;
+  if (!side_by_side(k_out, k_row, v_out, v_row, rows, int64_t(pager->Hkv) * pager->D)) return JFA_ERR_INVALID_ARG;
   if (int rc = check_device(pager)) return rc;
   const int unit = pager->bits == 16 ? 2 : 1;  // bytes of an element of the pages
   jfa::GatherArgs a{};

@@ -260,6 +260,23 @@ def test_gather_to_any_16_bytes(bits, k_off, v_off, gap):
 
 
 @pytest.mark.parametrize("bits", [16, 8, 4])
+def test_gather_outputs_that_overlap(bits):
+    """Slices of one tensor are fine; the same rows, shifted ones and half of them are refused."""
+    pager, held, table, dl = _case([40, 7], 2, 2, 64, 16, "rows", bits, 3)
+    call = lambda k, v: jfa.paged_gather(pager, *held[:2], table, _ints([0, 40, 47]), rows=47, **_scales(held), k_out=k, v_out=v)  # noqa: E731
+    want = jfa.paged_gather(pager, *held[:2], table, _ints([0, 40, 47]), rows=47, **_scales(held))
+    one = torch.zeros((100, 5, 64), dtype=BF16, device="cuda")
+    for k, v in ((one[:47, :2], one[:47, 2:4]), (one[:47, 3:], one[:47, 1:3]), (one[:47, 3:], one[20:67, :2]), (one[:47, :2], one[47:94, :2])):
+        got = call(k, v)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for k, v in ((one[:47, :2], one[:47, :2]), (one[:47, :2], one[:47, 1:3]), (one[:47, :2], one[20:67, :2]), (one[:47, 3:], one[20:67, 2:4]),
+                 (one[:47, :2], one[:94:2, 3:])):
+        with pytest.raises(jfa.JfaError) as e:
+            call(k, v)
+        assert e.value.code == 1
+
+
+@pytest.mark.parametrize("bits", [16, 8, 4])
 def test_gather_of_any_bytes(bits):
     """What is not written by append reads as it says: NaN, other bytes as the nearest power, all codes."""
     hk, D, page, n = 2, 64, 16, 300
