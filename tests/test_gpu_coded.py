@@ -449,6 +449,46 @@ def test_decode_nan_rows(bits, lens, hq, hk, D):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
+def test_strided_tables_and_queries(bits):
+    """Rows of tables and queries that lie apart; fewer requests than the pager holds."""
+    pager, held, table, dl = _case([300, 17, 0, 900], 8, 2, 128, 16, "rows", bits, 6)
+    q = _draw((4, 8, 128), 2)
+    want = jfa.paged_decode(pager, q, *held[:2], table, dl, 0.1, **_scales(held))
+    off = _ints([0, 300, 317, 317, 1217])
+    rows = jfa.paged_gather(pager, *held[:2], table, off, rows=1217, **_scales(held))
+    wide = torch.full((4, pager.max_pages + 5), -9, dtype=I32, device="cuda")
+    wide[:, :pager.max_pages] = table
+    more = torch.zeros((4, 13, 128), dtype=BF16, device="cuda")
+    more[:, 2:10] = q
+    big = jfa.Pager(max_seqs=50, max_pages=pager.max_pages, num_pages=pager.num_pages, page_size=16, H=8, Hkv=2, D=128, bits=bits)
+    got = jfa.paged_decode(big, more[:, 2:10], *held[:2], wide[:, :pager.max_pages], dl, 0.1, **_scales(held))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    got = jfa.paged_gather(big, *held[:2], wide[:, :pager.max_pages], off, rows=1217, **_scales(held))
+    assert torch.equal(got[0], rows[0]) and torch.equal(got[1], rows[1]) and big.status() == 0
+    for n in (1, 2, 3):
+        got = jfa.paged_decode(big, q[:n], *held[:2], table[:n], dl[:n], 0.1, **_scales(held))
+        ref, ref_lse, bound, _ = coded_ref.decode(q[:n], *_values(held, bits), table[:n], dl[:n], 0.1)
+        assert ((got[0].cpu().double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_every_page_and_length_at_its_limit(bits):
+    """A table as full as it can be, the last page of the cache, and offsets up to all of it."""
+    page, width, B, hk, D = 16, 5, 7, 2, 64
+    pager, held, table, dl = _case([page * width] * B, 4, hk, D, page, "rows", bits, 6, width=width)
+    full = pager.num_pages - 3
+    assert int(table.max()) < pager.num_pages and full == B * width
+    _check_decode(pager, held, table, dl)
+    _check_gather(pager, held, table, np.arange(B + 1) * page * width)
+    tight = jfa.Pager(max_seqs=B, max_pages=width, num_pages=int(table.max()) + 1, page_size=page, H=4, Hkv=hk, D=D, bits=bits)
+    some = [t[:tight.num_pages] for t in held]
+    _check_decode(tight, some, table, dl)
+    _check_gather(tight, some, table, np.arange(B + 1) * page * width)
+    dl += 1
+    _check_decode(tight, some, table, dl, status=jfa.PAGER_BAD_LENGTH)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
 def test_decode_bad_lengths_and_pages(bits):
     pager, held, table, lens = _case([40, 100, 64, 33, 16], 4, 2, 64, 16, "heads", bits, 5)
     lens[0], lens[3] = -1, 2**31 - 1
