@@ -13,12 +13,12 @@ namespace {
 // doubles the parts that CTAs join.
 //   rows of 64 and 32 bytes: 96 requests up to 32768 rows, 8 heads: 4 bits of 128 values 394
 //   us, one head after the other 596; 8 bits of 64 values 284 and 531; 128 mixed requests,
-//   126 MB, 41.9 and 43.5; one of 131072 rows, 76 MB, 32 either way; 32 mixed ones, 32 MB,
-//   21.3 and 18.9.
+//   126 MB, 40.5 and 42.5, 96, 95 MB, 33.9 and 34.5, 32, 32 MB, 21.3 and 18.9; one of 131072
+//   rows, 76 MB, 33.1 and 30.1.
 //   rows of 128 bytes: the full cache of 8 bits 540 us and 605 (of one GPU; of another 539
 //   and 546), 512 mixed requests, 0.9 GB, 152 and 164, 128, 224 MB, 46 either way; one of
 //   131072 rows, 134 MB, 35 and 31.
-constexpr int kLineMb = 96, kPairMb = 256;
+constexpr int kLineMb = 80, kPairMb = 256;
 
 // Where so much is read as comes and goes in L2 meanwhile, 4-bit lines are not marked to
 // leave first, or their second reader would miss them: the full cache 394 us, marked 472;
