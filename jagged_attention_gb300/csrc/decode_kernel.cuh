@@ -356,7 +356,6 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     if (lane >= o) units_to += x, rows_to += y;
   }
   most = __reduce_max_sync(~0u, most);
-  if (lane < 2) sh.part[2 * warp + lane].n = 0;
   U total = __shfl_sync(~0u, units_to, 31);
   int all_rows = __shfl_sync(~0u, rows_to, 31);
   if (!few) {
@@ -387,6 +386,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   const int sub_bits = kSide ? __ffs(kWarps / together) - 1 : __builtin_ctz(kWarps), subs = 1 << sub_bits;
   const int part = kSide ? warp & (together - 1) : 0, sub = kSide ? warp / together : warp;
   const int line = (part << sub_bits) + sub;
+  if (lane < 2) sh.part[2 * line + lane].n = 0;  // its own: no barrier stands before what it writes there
 
   // few and short rows: a CTA for each, so that nothing is left to be joined between CTAs
   const bool apart = most <= kApartRows / C::kTile / together && int64_t(all_rows) * vheads <= gridDim.x;
