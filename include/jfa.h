@@ -505,7 +505,7 @@ int jfa_rotate(jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row, i
  *
  * The caller owns the pages, tables, lengths and the list of free pages, all
  * in device memory, and the pager's block: device memory of at least
- * jfa_pager_block_bytes bytes, 256-byte aligned, which holds the status word
+ * jfa_pager_block_bytes_ex bytes, 256-byte aligned, which holds the status word
  * and the workspace in which the parts of a split row are joined.  Creating
  * the pager clears part of it on `stream`; it belongs to the pager until that
  * is destroyed and its launches and graphs are done.  A pager belongs to the
@@ -532,13 +532,16 @@ typedef struct jfa_pager* jfa_pager_t;
 #define JFA_PAGER_NO_PAGES 1   /* status: a request found no free page */
 #define JFA_PAGER_BAD_LENGTH 2 /* status: a length, or its change, outside the table's or the rows' bounds */
 #define JFA_PAGER_BAD_PAGE 4   /* status: a page, slot or free count outside the cache */
-size_t jfa_pager_block_bytes(int H, int Hkv, int D); /* on the current device; 0: unsupported */
+/* On the current device, 0: unsupported.  _ex: bytes of a pager with those flags (0, or one
+ * of JFA_PAGER_*BIT below); without: the most of any flags. */
+size_t jfa_pager_block_bytes(int H, int Hkv, int D);
+size_t jfa_pager_block_bytes_ex(int H, int Hkv, int D, unsigned flags);
 int jfa_pager_create(int max_seqs, int max_pages, int64_t num_pages, int page_size, int H, int Hkv,
                      int D, void* block, size_t block_bytes, void* stream, jfa_pager_t* out);
 /*
  * A cache in fewer bits.  A pager made with one of these flags serves pages that hold
  * codes, with scale bytes beside them (jfa_pages and jfa_scales below); flags 0 is
- * jfa_pager_create.  The block is the same.
+ * jfa_pager_create.
  *
  * JFA_PAGER_8BIT: a row of a head is D e4m3 codes and one byte c, its values are
  *     code * 2^(c - 127),

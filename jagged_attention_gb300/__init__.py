@@ -154,6 +154,8 @@ def lib() -> ctypes.CDLL:
                                      _cl, _ci, _vp]
             L.jfa_pager_block_bytes.argtypes = [_ci, _ci, _ci]
             L.jfa_pager_block_bytes.restype = ctypes.c_size_t
+            L.jfa_pager_block_bytes_ex.argtypes = [_ci, _ci, _ci, _cu]
+            L.jfa_pager_block_bytes_ex.restype = ctypes.c_size_t
             L.jfa_pager_create.argtypes = [_ci, _ci, _cl, _ci, _ci, _ci, _ci, _vp, ctypes.c_size_t, _vp,
                                            ctypes.POINTER(_vp)]
             L.jfa_pager_destroy.argtypes = [_vp]
@@ -708,12 +710,12 @@ class Pager:
         self.H, self.Hkv, self.D = H, Hkv, D
         self.device = torch.device("cuda", torch.cuda.current_device())
         self.index = self.device.index
-        n = lib().jfa_pager_block_bytes(H, Hkv, D)
+        flags = {16: 0, 8: PAGER_8BIT, 4: PAGER_4BIT}[bits]
+        n = lib().jfa_pager_block_bytes_ex(H, Hkv, D, flags)
         self.block = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
         stream = torch.cuda.current_stream()
         self._streams = {stream.cuda_stream}  # those that the block's memory is kept for
         h = _vp()
-        flags = {16: 0, 8: PAGER_8BIT, 4: PAGER_4BIT}[bits]
         _check(lib().jfa_pager_create_ex(max_seqs, max_pages, num_pages, page_size, H, Hkv, D, flags,
                                          self.block.data_ptr(), n, stream.cuda_stream, ctypes.byref(h)),
                "jfa_pager_create_ex")

@@ -32,9 +32,9 @@ static_assert(kCodedTile == DecodeCfg<4, 128, 1>::kTile, "units of either");
 
 cudaError_t launch_decode_coded(const DecodeArgs& given, int sms, cudaStream_t stream) {
   DecodeArgs a = given;
-  const int row_bytes = a.D * a.bits / 8, mates = row_bytes < 128 ? 128 / row_bytes : 2;
-  static_assert(kMostMates >= 128 / (64 * 4 / 8), "room for what mates leave");
-  if (a.parts == 1 && a.head == row_bytes && a.Hkv % mates == 0) {
+  const int row_bytes = a.D * a.bits / 8;
+  const int mates = decode_mates(a.bits, a.D, a.Hkv, {a.parts, a.together, a.passes, a.part_heads});
+  if (mates > 1 && a.head == row_bytes) {
     const int64_t unit = int64_t(2) * row_bytes * kCodedTile * a.Hkv;  // bytes of a tile of all heads
     auto units = [&](int mb) { return static_cast<uint32_t>((int64_t(mb) << 20) / unit); };
     a.mates = mates;

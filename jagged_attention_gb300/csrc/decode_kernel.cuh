@@ -98,7 +98,6 @@ struct DecodeCfg {
   static constexpr int kCtasPerSm = kBits == 16 ? (D == 64 ? 2 : 1) : kBits == 8 ? (D == 64 && NT == 1 ? 2 : 1)
                                                                               : (D == 64 || NT == 1 ? 2 : 1);
 };
-constexpr int kMostCtasPerSm = 2;
 
 // Units of work: the n tiles of a (request, key/value head) count n units, and
 // kRowUnits behind them stand for its beginning and end (256 requests up to 300

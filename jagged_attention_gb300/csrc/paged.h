@@ -171,14 +171,15 @@ struct QueryParts {
   int parts, together, passes, part_heads;
 };
 QueryParts query_parts(int group);
-constexpr int kMostMates = 4;  // heads of one part that go side by side
+// Key/value heads that may go side by side over a cache of so many bits, 1 where none do.
+int decode_mates(int bits, int D, int Hkv, const QueryParts& parts);
 
 // Workspace of a decode launch: counters (int), part_ml and part_o (float).
 struct DecodeSpace {
   int counters;
   int64_t part_ml, part_o;
 };
-DecodeSpace decode_space(int D, const QueryParts& parts, int sms);
+DecodeSpace decode_space(int bits, int D, int Hkv, const QueryParts& parts, int sms);
 cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_decode_coded(const DecodeArgs& a, int sms, cudaStream_t stream);  // 8 or 4 bits
 

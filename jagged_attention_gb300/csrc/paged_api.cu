@@ -2,6 +2,7 @@
 // in include/jfa.h: argument checks, handles and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -141,16 +142,20 @@ struct Block {
   size_t counters, part_ml, part_o, bytes;
   jfa::QueryParts parts;
 };
-Block block_of(int H, int Hkv, int D, int sms) {
+Block block_of(int bits, int H, int Hkv, int D, int sms) {
   Block k;
   k.parts = jfa::query_parts(H / Hkv);
-  const jfa::DecodeSpace n = jfa::decode_space(D, k.parts, sms);
+  const jfa::DecodeSpace n = jfa::decode_space(bits, D, Hkv, k.parts, sms);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   k.counters = 256;
   k.part_ml = up(k.counters + n.counters * sizeof(int));
   k.part_o = up(k.part_ml + n.part_ml * sizeof(float));
   k.bytes = up(k.part_o + n.part_o * sizeof(float));
   return k;
+}
+// Bits of a pager with these flags, 0: no such flags.
+int bits_of(unsigned flags) {
+  return flags == 0 ? 16 : flags == JFA_PAGER_8BIT ? 8 : flags == JFA_PAGER_4BIT ? 4 : 0;
 }
 int check_heads(int H, int Hkv, int D) {
   if (Hkv < 1 || H < Hkv || H % Hkv) return JFA_ERR_INVALID_ARG;
@@ -237,10 +242,16 @@ int jfa_rotate(jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row, i
   return jfa::launch_rows(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
-size_t jfa_pager_block_bytes(int H, int Hkv, int D) {
+size_t jfa_pager_block_bytes_ex(int H, int Hkv, int D, unsigned flags) {
   int sms = 0;
-  if (check_heads(H, Hkv, D) != JFA_OK || sm_count(&sms) != JFA_OK) return 0;
-  return block_of(H, Hkv, D, sms).bytes;
+  if (!bits_of(flags) || check_heads(H, Hkv, D) != JFA_OK || sm_count(&sms) != JFA_OK) return 0;
+  return block_of(bits_of(flags), H, Hkv, D, sms).bytes;
+}
+
+size_t jfa_pager_block_bytes(int H, int Hkv, int D) {
+  size_t most = 0;
+  for (unsigned flags : {0u, JFA_PAGER_8BIT, JFA_PAGER_4BIT}) most = std::max(most, jfa_pager_block_bytes_ex(H, Hkv, D, flags));
+  return most;
 }
 
 int jfa_pager_create(int max_seqs, int max_pages, int64_t num_pages, int page_size, int H, int Hkv,
@@ -252,7 +263,8 @@ int jfa_pager_create_ex(int max_seqs, int max_pages, int64_t num_pages, int page
                         int D, unsigned flags, void* block, size_t block_bytes, void* stream, jfa_pager_t* out) {
   if (!out) return JFA_ERR_INVALID_ARG;
   *out = nullptr;
-  if (flags != 0 && flags != JFA_PAGER_8BIT && flags != JFA_PAGER_4BIT) return JFA_ERR_INVALID_ARG;
+  const int bits = bits_of(flags);
+  if (!bits) return JFA_ERR_INVALID_ARG;
   if (max_seqs < 1 || max_pages < 1 || num_pages < 1 || page_size < 1) return JFA_ERR_INVALID_ARG;
   if (int rc = check_heads(H, Hkv, D)) return rc;
   if (max_seqs > JFA_PAGER_MAX_SEQS || num_pages > INT_MAX ||
@@ -262,7 +274,7 @@ int jfa_pager_create_ex(int max_seqs, int max_pages, int64_t num_pages, int page
   int sms = 0, dev = 0;
   if (int rc = sm_count(&sms)) return rc;
   if (cudaGetDevice(&dev) != cudaSuccess) return JFA_ERR_CUDA;
-  const Block k = block_of(H, Hkv, D, sms);
+  const Block k = block_of(bits, H, Hkv, D, sms);
   if (!block || block_bytes < k.bytes) return JFA_ERR_WORKSPACE;
   auto* base = static_cast<unsigned char*>(block);
   if (cudaMemsetAsync(base, 0, k.part_ml, static_cast<cudaStream_t>(stream)) != cudaSuccess) return JFA_ERR_CUDA;
@@ -273,7 +285,7 @@ int jfa_pager_create_ex(int max_seqs, int max_pages, int64_t num_pages, int page
   p->H = H;
   p->Hkv = Hkv;
   p->D = D;
-  p->bits = flags == JFA_PAGER_8BIT ? 8 : flags == JFA_PAGER_4BIT ? 4 : 16;
+  p->bits = bits;
   p->device = dev;
   p->sms = sms;
   p->parts = k.parts;
