@@ -30,25 +30,25 @@ static_assert(kCodedTile == DecodeCfg<4, 128, 1>::kTile, "units of either");
 
 }  // namespace
 
-cudaError_t launch_decode_coded(const DecodeArgs& given, int sms, cudaStream_t stream) {
-  DecodeArgs a = given;
-  const int row_bytes = a.D * a.bits / 8;
-  const int mates = decode_mates(a.bits, a.D, a.Hkv, {a.parts, a.together, a.passes, a.part_heads});
+cudaError_t launch_decode_coded(const DecodeArgs& given, const Scales& scales, int bits, int sms, cudaStream_t stream) {
+  CodedDecodeArgs a{given, scales, 1, 0, 0};
+  const int row_bytes = a.D * bits / 8;
+  const int mates = decode_mates(bits, a.D, a.Hkv, {a.parts, a.together, a.passes, a.part_heads});
   if (mates > 1 && a.head == row_bytes) {
     const int64_t unit = int64_t(2) * row_bytes * kCodedTile * a.Hkv;  // bytes of a tile of all heads
     auto units = [&](int mb) { return static_cast<uint32_t>((int64_t(mb) << 20) / unit); };
     a.mates = mates;
     a.mates_units = units(row_bytes < 128 ? kLineMb : kPairMb);
-    a.far_units = a.bits == 4 ? units(kFarMb) : UINT32_MAX;
+    a.far_units = bits == 4 ? units(kFarMb) : UINT32_MAX;
   }
   // whether 32 bits hold offsets as the kernel counts them
-  const int n = a.bits == 8 ? 1 : a.D / kBlock;
+  const int n = bits == 8 ? 1 : a.D / kBlock;
   auto beyond = [&](int64_t page, int64_t row, int64_t head, int unit) {
     using Wide = __int128;
     return ((a.num_pages - 1) * Wide(page) + (a.div.d - 1) * Wide(row) + (a.Hkv - 1) * Wide(head)) / unit > UINT32_MAX;
   };
   const bool wide = beyond(a.page, a.row, a.head, 16) || beyond(a.scales.page, a.scales.row, a.scales.head, n);
-  return a.bits == 8 ? launch_by_size<8>(a, sms, stream, wide) : launch_by_size<4>(a, sms, stream, wide);
+  return bits == 8 ? launch_by_size<8>(a, sms, stream, wide) : launch_by_size<4>(a, sms, stream, wide);
 }
 
 }  // namespace jfa

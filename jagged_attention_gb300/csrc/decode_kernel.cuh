@@ -289,11 +289,18 @@ struct Deal {
   }
 };
 
+// x / a.parts, which is a power of two times a.passes, mostly 1.  Divisions cost every CTA
+// instructions before its first row: 16 requests of 64 heads on 2 28.7 us with, 28.1 without.
+__device__ __forceinline__ int kv_of(const DecodeArgs& a, int x) {
+  const int y = x >> (__ffs(a.together) - 1);
+  return a.passes == 1 ? y : y / a.passes;
+}
+
 // Query heads [first, first + count) of part x of all, a.parts to a key/value head:
 // one where the parts are not side by side.
 template <bool kSide>
 __device__ __forceinline__ void heads_of(const DecodeArgs& a, int x, int* first, int* count) {
-  const int kv = kSide ? x / a.parts : x, g0 = kSide ? (x - kv * a.parts) * a.part_heads : 0;
+  const int kv = kSide ? kv_of(a, x) : x, g0 = kSide ? (x - kv * a.parts) * a.part_heads : 0;
   *first = kv * a.group + g0;
   *count = kSide ? max(0, min(a.part_heads, a.group - g0)) : a.group;  // 0: more parts than heads fill
 }
@@ -320,12 +327,15 @@ __device__ __forceinline__ void store_joined(const DecodeArgs& a, int D, int b, 
   if (d == 0) a.lse[int64_t(head) * a.B + b] = lse_of<kBits>(s.top == -INFINITY ? 0.f : s.top, s.sum);
 }
 
+template <int kBits>
+using ArgsOf = std::conditional_t<kBits == 16, DecodeArgs, CodedDecodeArgs>;
+
 // U: unsigned type that counts all units.  32 bits hold them unless the table is
 // wide enough for more; 64 bits cost 0.3 to 0.6 us.
 // kSide: parts of query heads side by side.
 template <int kBits, int D, int NT, bool kSide, typename U>
 __global__ void __launch_bounds__(DecodeCfg<kBits, D, NT>::kWarps * 32, DecodeCfg<kBits, D, NT>::kCtasPerSm)
-decode_kernel(const __grid_constant__ DecodeArgs a) {
+decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
   using C = DecodeCfg<kBits, D, NT>;
   constexpr int kTile = C::kTile, kSub = C::kSub, kWarps = C::kWarps;
   extern __shared__ __align__(256) unsigned char smem[];
@@ -379,16 +389,22 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   // A CTA's share is dealt to `subs` sets of `together` warps, one for each part of
   // the query heads, or for each of a few key/value heads whose rows lie side by side; a
   // line is a warp's place with those of its part in a row.
-  const bool mates = kBits < 16 && kSide && a.mates > 1 && total >= a.mates_units;
-  const bool far = total >= a.far_units;
-  const int vheads = mates ? a.Hkv / a.mates : kSide ? a.vheads : a.Hkv, together = mates ? a.mates : kSide ? a.together : 1;
-  const int sub_bits = kSide ? __ffs(kWarps / together) - 1 : __builtin_ctz(kWarps), subs = 1 << sub_bits;
-  const int part = kSide ? warp & (together - 1) : 0, sub = kSide ? warp / together : warp;
+  int vheads = a.Hkv * (kSide ? a.passes : 1), together = kSide ? a.together : 1;
+  bool twice = false;  // lines of the cache are read by two warps with more than L2 holds between
+  if constexpr (kBits < 16 && kSide) {
+    if (a.mates > 1 && total >= a.mates_units) {
+      vheads = a.Hkv / a.mates;
+      together = a.mates;
+      twice = total >= a.far_units;
+    }
+  }
+  const int side_bits = kSide ? __ffs(together) - 1 : 0, sub_bits = __builtin_ctz(kWarps) - side_bits, subs = 1 << sub_bits;
+  const int part = warp & (together - 1), sub = warp >> side_bits;
   const int line = (part << sub_bits) + sub;
   if (lane < 2) sh.part[2 * line + lane].n = 0;  // its own: no barrier stands before what it writes there
 
   // few and short rows: a CTA for each, so that nothing is left to be joined between CTAs
-  const bool apart = most <= kApartRows / C::kTile / together && int64_t(all_rows) * vheads <= gridDim.x;
+  const bool apart = most <= (kApartRows / C::kTile) >> side_bits && int64_t(all_rows) * vheads <= gridDim.x;
   if (apart) {
     units = U(rows) * U(most);
     units_to = U(rows_to) * U(most);
@@ -483,7 +499,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     int kv_at = 0;
     auto row_of_at = [&] {
       table = a.table + at.b * a.table_row;
-      kv_at = kSide ? (at.vh * together + part) / a.parts : at.vh;
+      kv_at = kSide ? kv_of(a, at.vh * together + part) : at.vh;
       head_off = kv_at * a.head;
     };
     row_of_at();
@@ -549,7 +565,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
     };
     // Rows of a tile into a stage.  bf16: 8 lanes copy 128 bytes of a row, chunk c of row
     // r to place c ^ (r % 8) of its 8.  Codes: the lanes that a row has chunks of 16 bytes.
-    const uint64_t policy = read_once_policy(mates && far);
+    const uint64_t policy = read_once_policy(twice);
     const uint32_t to_even = (lane >> 3) * (D * 2) + (((lane & 7) ^ (lane >> 3)) << 4), to_odd = to_even ^ 64;
     auto copy = [&](uint32_t stage, const uint16_t* from, bool v) {
       if constexpr (kBits == 16) {
@@ -1219,7 +1235,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
 }
 
 template <int kBits, int D, int NT, bool kSide, typename U>
-cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
+cudaError_t launch(const ArgsOf<kBits>& a, int sms, cudaStream_t stream) {
   using C = DecodeCfg<kBits, D, NT>;
   static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<C::kWarps, NT>) + 1024) <= 233472, "shared memory of an SM");
   cudaError_t e = set_smem_limit_once<decode_kernel<kBits, D, NT, kSide, U>>(C::kSmemBytes);
@@ -1229,19 +1245,21 @@ cudaError_t launch(const DecodeArgs& a, int sms, cudaStream_t stream) {
 }
 
 template <int kBits, int D, typename U>
-cudaError_t launch_by_heads(const DecodeArgs& a, int sms, cudaStream_t stream) {
-  if (kBits < 16 && a.mates > 1 && a.part_heads <= 8) return launch<kBits, D, kBits < 16 ? 1 : 2, true, U>(a, sms, stream);
-  if (a.together > 1 || a.mates > 1) return launch<kBits, D, 2, true, U>(a, sms, stream);
+cudaError_t launch_by_heads(const ArgsOf<kBits>& a, int sms, cudaStream_t stream) {
+  if constexpr (kBits < 16) {
+    if (a.mates > 1) return a.part_heads <= 8 ? launch<kBits, D, 1, true, U>(a, sms, stream) : launch<kBits, D, 2, true, U>(a, sms, stream);
+  }
+  if (a.together > 1) return launch<kBits, D, 2, true, U>(a, sms, stream);
   return a.part_heads <= 8 ? launch<kBits, D, 1, false, U>(a, sms, stream) : launch<kBits, D, 2, false, U>(a, sms, stream);
 }
 
 template <int kBits>
-cudaError_t launch_by_size(const DecodeArgs& a, int sms, cudaStream_t stream, bool wide = false) {
+cudaError_t launch_by_size(const ArgsOf<kBits>& a, int sms, cudaStream_t stream, bool wide = false) {
   // the units of B full table rows
   constexpr int kTile = DecodeCfg<kBits, 128, 1>::kTile;
   static_assert(kTile == DecodeCfg<kBits, 64, 2>::kTile, "tiles go by the bits alone");
   const int64_t most = int64_t(a.B) * (int64_t(a.max_pages) * a.div.d / kTile + 1 + kRowUnits<kBits>);
-  if (wide || most > UINT32_MAX / a.vheads)
+  if (wide || most > UINT32_MAX / (a.Hkv * a.passes))
     return a.D == 128 ? launch_by_heads<kBits, 128, uint64_t>(a, sms, stream) : launch_by_heads<kBits, 64, uint64_t>(a, sms, stream);
   return a.D == 128 ? launch_by_heads<kBits, 128, uint32_t>(a, sms, stream) : launch_by_heads<kBits, 64, uint32_t>(a, sms, stream);
 }

@@ -84,8 +84,6 @@ struct RowJob {
   int64_t out_page, out_head;  // out_page: scattered rows only
   int heads;
   bool f32, scatter, rotate;
-  uint8_t* scales;  // of rows scattered as codes, whose `out` and distances count bytes
-  int64_t scales_page, scales_row, scales_head;
 };
 
 struct RowsArgs {
@@ -100,16 +98,22 @@ struct RowsArgs {
   int64_t num_slots;
   PageDiv div;
   int* status;
-  int bits;  // of scattered rows: 16, or 8 or 4 as codes (coded.cuh)
   Turns turns;
 };
-cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream);
 
 // Where the scale bytes of a cache of 8 or 4 bits are, and their distances in bytes.
 struct Scales {
   uint8_t *k, *v;
   int64_t page, row, head;
 };
+
+// Jobs 0 and 1 scatter K and V as codes (coded.cuh), their `out` and its distances in
+// bytes.
+struct CodedRowsArgs : RowsArgs {
+  Scales scales;
+};
+cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_rows_coded(const CodedRowsArgs& a, int bits, int sms, cudaStream_t stream);
 
 struct GatherArgs {
   int B, Hkv, D, bits;
@@ -143,10 +147,6 @@ struct DecodeArgs {
   int B, H, Hkv, D;
   int group;                                // H / Hkv
   int parts, together, passes, part_heads;  // QueryParts
-  int vheads;           // Hkv * passes: sets of `together` parts
-  int mates;            // key/value heads that go side by side instead, 1 where none do,
-  uint32_t mates_units; // if the requests have so many units,
-  uint32_t far_units;   // and with so many their lines are not marked to leave L2 first
   int64_t num_pages;
   int max_pages;
   PageDiv div;
@@ -154,8 +154,6 @@ struct DecodeArgs {
   int64_t q_row;
   const uint16_t *k, *v;   // or codes, whose distances count bytes
   int64_t page, row, head;
-  int bits;                // 16, or 8 or 4
-  Scales scales;
   const int32_t *table, *lens;
   int64_t table_row;
   float scale;
@@ -164,6 +162,12 @@ struct DecodeArgs {
   int* status;
   int* counters;             // arrivals at the parts of split rows; zero between launches
   float *part_ml, *part_o;   // what CTAs leave of split rows
+};
+struct CodedDecodeArgs : DecodeArgs {
+  Scales scales;
+  int mates;            // key/value heads that go side by side, 1 where none do,
+  uint32_t mates_units; // if the requests have so many units,
+  uint32_t far_units;   // and with so many their lines are not marked to leave L2 first
 };
 // A key/value head's query heads in parts of at most 16: `together` of them (1, 2,
 // 4 or 8) side by side in a CTA, in `passes` over the cache.
@@ -181,6 +185,6 @@ struct DecodeSpace {
 };
 DecodeSpace decode_space(int bits, int D, int Hkv, const QueryParts& parts, int sms);
 cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t stream);
-cudaError_t launch_decode_coded(const DecodeArgs& a, int sms, cudaStream_t stream);  // 8 or 4 bits
+cudaError_t launch_decode_coded(const DecodeArgs& a, const Scales& scales, int bits, int sms, cudaStream_t stream);
 
 }  // namespace jfa

@@ -164,7 +164,7 @@ int check_heads(int H, int Hkv, int D) {
 
 jfa::RowJob dense_job(const void* in, int64_t in_row, void* out, int64_t out_row, int heads, int D,
                       bool f32, bool rotate) {
-  return {in, out, in_row, out_row, 0, D, heads, f32, false, rotate, nullptr, 0, 0, 0};
+  return {in, out, in_row, out_row, 0, D, heads, f32, false, rotate};
 }
 
 // rows of one launch: the grid's first dimension holds 2^31 - 1 blocks of at least 8 rows
@@ -237,7 +237,6 @@ int jfa_rotate(jfa_rotary_t rotary, const int32_t* positions, int64_t pos_row, i
   a.pos_row = pos_row;
   a.pos_axis = pos_axis;
   a.inverse = flags & JFA_ROTATE_INVERSE;
-  a.bits = 16;
   a.turns = rotary->turns;
   return jfa::launch_rows(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
@@ -383,13 +382,10 @@ int jfa_paged_append_ex(jfa_pager_t pager, int64_t rows, const void* k, int64_t 
     if (int rc = check_rows(q_out, q_out_row, pager->H, D, false)) return rc;
   }
   if (int rc = check_device(pager)) return rc;
-  jfa::RowsArgs a{};
-  const jfa::Scales n = scales_of(scales);
-  a.job[0] = {k, pages->k, k_row, pages->row, pages->page, pages->head, pager->Hkv, false, true, rotary != nullptr,
-              n.k, n.page, n.row, n.head};
-  a.job[1] = {v, pages->v, v_row, pages->row, pages->page, pages->head, pager->Hkv, false, true, false,
-              n.v, n.page, n.row, n.head};
-  a.bits = pager->bits;
+  jfa::CodedRowsArgs a{};
+  a.job[0] = {k, pages->k, k_row, pages->row, pages->page, pages->head, pager->Hkv, false, true, rotary != nullptr};
+  a.job[1] = {v, pages->v, v_row, pages->row, pages->page, pages->head, pager->Hkv, false, true, false};
+  a.scales = scales_of(scales);
   if (q) a.job[2] = dense_job(q, q_row, q_out, q_out_row, pager->H, D, false, true);
   a.heads = 2 * pager->Hkv + (q ? pager->H : 0);
   a.D = D;
@@ -402,7 +398,9 @@ int jfa_paged_append_ex(jfa_pager_t pager, int64_t rows, const void* k, int64_t 
   a.div = pager->div;
   a.status = pager->d_status;
   if (rotary) a.turns = rotary->turns;
-  return jfa::launch_rows(a, pager->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+  const auto s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = pager->bits == 16 ? jfa::launch_rows(a, pager->sms, s) : jfa::launch_rows_coded(a, pager->bits, pager->sms, s);
+  return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
 int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, const jfa_pages* pages,
@@ -434,8 +432,6 @@ int jfa_paged_decode_ex(jfa_pager_t pager, int B, const void* q, int64_t q_row, 
   a.together = pager->parts.together;
   a.passes = pager->parts.passes;
   a.part_heads = pager->parts.part_heads;
-  a.vheads = pager->Hkv * pager->parts.passes;
-  a.mates = 1;
   a.num_pages = pager->num_pages;
   a.max_pages = pager->max_pages;
   a.div = pager->div;
@@ -446,8 +442,6 @@ int jfa_paged_decode_ex(jfa_pager_t pager, int B, const void* q, int64_t q_row, 
   a.page = pages->page;
   a.row = pages->row;
   a.head = pages->head;
-  a.bits = pager->bits;
-  a.scales = scales_of(scales);
   a.table = table;
   a.table_row = table_row;
   a.lens = lens;
@@ -458,8 +452,10 @@ int jfa_paged_decode_ex(jfa_pager_t pager, int B, const void* q, int64_t q_row, 
   a.counters = pager->d_counters;
   a.part_ml = pager->d_part_ml;
   a.part_o = pager->d_part_o;
-  const auto launch = a.bits == 16 ? jfa::launch_decode : jfa::launch_decode_coded;
-  return launch(a, pager->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+  const auto s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = pager->bits == 16 ? jfa::launch_decode(a, pager->sms, s)
+                                          : jfa::launch_decode_coded(a, scales_of(scales), pager->bits, pager->sms, s);
+  return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
 int jfa_paged_gather(jfa_pager_t pager, int B, const jfa_pages* pages, const jfa_scales* scales,

@@ -142,9 +142,9 @@ constexpr int kCodedBlocksPerSm = 14, kCodedHeadsAThread = 16;
 // The threads of a row exchange the largest magnitudes of their runs; with 4 bits a
 // scale's 16 values are two runs, r and r ^ 1, which two threads may hold.
 // Whole warps come here, so that lanes exchange without regard to rows; `stores`: whether
-// the thread's row has a slot.  scales: where those of the row's head 0 go.
+// the thread's row has a slot.  bytes: where the scales of the row's head h0 go, `head` from head to head.
 template <bool kInterleaved, int kBits>
-__device__ __forceinline__ void walk_coded(const RowJob& job, int D, int64_t in, int64_t out, int64_t scales, int h0,
+__device__ __forceinline__ void walk_coded(const RowJob& job, int D, int64_t in, int64_t out, uint8_t* bytes, int64_t head, int h0,
                                            int h1, int u, int turn_units, bool turn, bool stores, const float (&c)[8],
                                            const float (&s)[8]) {
   const int units = D / 16, base = (threadIdx.x & 31) & -units;
@@ -157,7 +157,6 @@ __device__ __forceinline__ void walk_coded(const RowJob& job, int D, int64_t in,
   const int from_a = holder(2 * u), from_b = holder(2 * u + 1), shift_a = shift(2 * u), shift_b = shift(2 * u + 1);
   const auto* p = static_cast<const uint16_t*>(job.in) + in + int64_t(h0) * D;
   auto* codes = static_cast<unsigned char*>(job.out) + out + h0 * job.out_head;
-  uint8_t* bytes = job.scales + scales + h0 * job.scales_head;
   Run<false> next_a, next_b;  // the next head's, under way
   if (h0 < h1) {
     next_a.load(p, lo);
@@ -207,14 +206,17 @@ __device__ __forceinline__ void walk_coded(const RowJob& job, int D, int64_t in,
       }
     }
     codes += job.out_head;
-    bytes += job.scales_head;
+    bytes += head;
   }
 }
+
+template <int kBits>
+using RowsArgsOf = std::conditional_t<kBits == 16, RowsArgs, CodedRowsArgs>;
 
 // kBits: of scattered rows.
 template <bool kInterleaved, int kBits>
 __global__ void __launch_bounds__(kRowThreads, kBits == 16 ? kBlocksPerSm : kCodedBlocksPerSm)
-rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
+rows_kernel(const __grid_constant__ RowsArgsOf<kBits> a, int heads_per_block) {
   wait_for_launch_before();
   const int units = a.D / 16;  // threads of a row: 4 or 8
   const int u = threadIdx.x % units;
@@ -228,13 +230,14 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
   const int lo = turning ? 8 * u : 2 * pairs + 16 * (u - pairs / 8);
   const int hi = turning ? lo + pairs : lo + 8;
 
-  const int first = blockIdx.y * heads_per_block;
-  const int last = min(a.heads, first + heads_per_block);
-  // of codes, blocks without a head that turns form no sines
-  const bool sines = kBits == 16 || first < (a.job[0].rotate ? a.job[0].heads : 0) || last > a.job[0].heads + a.job[1].heads;
-
   float c[8], s[8];
-  if (turning && sines) {
+  // of codes, blocks without a head that turns form no sines
+  bool sines = turning;
+  if constexpr (kBits < 16) {
+    const int first = blockIdx.y * heads_per_block, last = min(a.heads, first + heads_per_block);
+    sines = turning && (first < (a.job[0].rotate ? a.job[0].heads : 0) || last > a.job[0].heads + a.job[1].heads);
+  }
+  if (sines) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int pair = !kInterleaved ? lo + i : i < 4 ? lo / 2 + i : hi / 2 + i - 4;
@@ -259,6 +262,8 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
     }
   }
 
+  const int first = blockIdx.y * heads_per_block;
+  const int last = min(a.heads, first + heads_per_block);
   int before = 0;
 #pragma unroll
   for (int j = 0; j < 3; ++j) {
@@ -269,19 +274,23 @@ rows_kernel(const __grid_constant__ RowsArgs a, int heads_per_block) {
     if (kBits < 16 && !job.scatter && !here) continue;
     const int64_t in = row * job.in_row;
     const int64_t out = job.scatter ? page * job.out_page + in_page * job.out_row : row * job.out_row;
-    if (kBits < 16 && job.scatter)
-      walk_coded<kInterleaved, kBits>(job, a.D, in, out, page * job.scales_page + in_page * job.scales_row, h0, h1, u,
-                                      pairs / 8, turning && job.rotate, placed, c, s);
-    else if (job.f32)
+    if constexpr (kBits < 16) {
+      if (job.scatter) {
+        uint8_t* bytes = (j == 0 ? a.scales.k : a.scales.v) + page * a.scales.page + in_page * a.scales.row + h0 * a.scales.head;
+        walk_coded<kInterleaved, kBits>(job, a.D, in, out, bytes, a.scales.head, h0, h1, u, pairs / 8, turning && job.rotate, placed,
+                                        c, s);
+        continue;
+      }
+    }
+    if (job.f32)
       walk_heads<kInterleaved, true>(job, a.D, in, out, h0, h1, lo, hi, turning && job.rotate, c, s);
     else
       walk_heads<kInterleaved, false>(job, a.D, in, out, h0, h1, lo, hi, turning && job.rotate, c, s);
   }
 }
 
-}  // namespace
-
-cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
+template <int kBits>
+cudaError_t launch(const RowsArgsOf<kBits>& a, int sms, cudaStream_t stream) {
   if (a.rows == 0 || a.heads == 0) return cudaSuccess;
   const int64_t per_block = kRowThreads / (a.D / 16);
   const int64_t blocks = (a.rows + per_block - 1) / per_block;
@@ -291,20 +300,23 @@ cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   // dealt by their number alone: of fp32 and bf16 heads some threads have more weight.
   int64_t weight = 0;
   for (const RowJob& job : a.job) weight += int64_t(job.heads) * (job.f32 ? 2 : 1);
-  const int64_t fill = int64_t(sms) * (a.bits == 16 ? kBlocksPerSm : kCodedBlocksPerSm);
-  const int64_t most = a.bits == 16 ? kHeadsAThread : kCodedHeadsAThread;
+  const int64_t fill = int64_t(sms) * (kBits == 16 ? kBlocksPerSm : kCodedBlocksPerSm);
+  const int64_t most = kBits == 16 ? kHeadsAThread : kCodedHeadsAThread;
   constexpr int64_t kMostSplit = 65535;  // the grid's second dimension
   const int split = static_cast<int>(std::min<int64_t>(
       {a.heads, kMostSplit, std::max({fill / blocks, (weight + most - 1) / most, int64_t(1)})}));
   const int per = (a.heads + split - 1) / split;
   const dim3 grid(static_cast<unsigned>(blocks), (a.heads + per - 1) / per);
-  auto kernel = [&](auto bits) {
-    return a.turns.interleaved ? rows_kernel<true, decltype(bits)::value> : rows_kernel<false, decltype(bits)::value>;
-  };
-  return launch_overlapped(a.bits == 8   ? kernel(std::integral_constant<int, 8>())
-                           : a.bits == 4 ? kernel(std::integral_constant<int, 4>())
-                                         : kernel(std::integral_constant<int, 16>()),
-                           grid, kRowThreads, 0, stream, a, per);
+  return launch_overlapped(a.turns.interleaved ? rows_kernel<true, kBits> : rows_kernel<false, kBits>, grid, kRowThreads, 0,
+                           stream, a, per);
+}
+
+}  // namespace
+
+cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) { return launch<16>(a, sms, stream); }
+
+cudaError_t launch_rows_coded(const CodedRowsArgs& a, int bits, int sms, cudaStream_t stream) {
+  return bits == 8 ? launch<8>(a, sms, stream) : launch<4>(a, sms, stream);
 }
 
 }  // namespace jfa
