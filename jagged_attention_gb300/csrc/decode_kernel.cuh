@@ -79,6 +79,11 @@ constexpr int kMostHeads = 16;   // query heads that a warp holds
 constexpr int kMostTogether = 8;  // warps side by side
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kWeightBits = 15.f;  // of codes: the largest weight is 2^15, as fp16 has it
+// The largest running reference, in units of log2 e, that 15 is taken off as it is: 4 bits:
+// it is rounded by 1/8 at most then, and the largest weight is 2^15.125; 8 bits: scores
+// with their powers of two are rounded by 2^-14 at most.
+template <int kBits>
+constexpr float kNear = kBits == 8 ? 0x1p10f : 0x1p22f;
 
 template <int kBits, int D, int NT>  // NT: tiles of 8 query heads
 struct DecodeCfg {
@@ -641,6 +646,10 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
     if (more) find_next();
 
     float o_acc[D / 16][NT][4], m[NT][2], l[NT][2];
+    // Of codes, of stretches with a reference beyond kNear: m is the largest score then, and
+    // O is o_acc 2^(rho - 15), with rho the largest z = score + power - m.
+    float rho[NT][2];
+    bool beyond[NT];
     uint32_t qf[D / 16][NT][2];
     const int g = lane >> 2, j = lane & 3;
     int t0 = 0, first = 0, heads = 0;
@@ -793,6 +802,8 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
           }
           m[n][0] = m[n][1] = -INFINITY;
           l[n][0] = l[n][1] = 0.f;
+          rho[n][0] = rho[n][1] = kWeightBits;
+          beyond[n] = false;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -908,10 +919,8 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
             if constexpr (kBits == 16) {
               const bool counts = (live_now[0] >> (16 * x + g + (e >> 1) * 8)) & 1;
               s[x][n][e] = counts ? s[x][n][e] * scale_log2 : -INFINITY;
-            } else if constexpr (kBits == 8) {
-              s[x][n][e] = fmaf(s[x][n][e], unit_of[x][e >> 1], v_log2[x][e >> 1]);
             }
-            top[e & 1] = fmaxf(top[e & 1], s[x][n][e]);
+            top[e & 1] = fmaxf(top[e & 1], kBits == 8 ? fmaf(s[x][n][e], unit_of[x][e >> 1], v_log2[x][e >> 1]) : s[x][n][e]);
           }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
@@ -921,6 +930,11 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
         if constexpr (kBits == 8) top[0] -= kWeightBits, top[1] -= kWeightBits;
         if constexpr (kBits == 4) top[0] = fmaf(top[0], unit_log2, -kWeightBits), top[1] = fmaf(top[1], unit_log2, -kWeightBits);
         if (__any_sync(~0u, top[0] > m[n][0] || top[1] > m[n][1])) {
+          if constexpr (kBits < 16) {
+            auto is_beyond = [&](float ref) { return fabsf(ref) > kNear<kBits> && fabsf(ref) < INFINITY; };
+            beyond[n] |= __any_sync(~0u, is_beyond(fmaxf(m[n][0], top[0])) || is_beyond(fmaxf(m[n][1], top[1])));
+            if (beyond[n]) top[0] = top[1] = -INFINITY;  // m is moved below
+          }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float up = fmaxf(m[n][e], top[e]);
@@ -932,17 +946,64 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
             for (int i = 0; i < D / 16; ++i) o_acc[i][n][e] *= keep, o_acc[i][n][2 + e] *= keep;
           }
         }
+        if constexpr (kBits < 16) {
+          if (beyond[n]) {
+            // Scores are rounded first, so that the largest less the reference is 0 whatever
+            // its size; s becomes what the weights are powers of two of.
+            top[0] = top[1] = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kGroups; ++x)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s[x][n][e] = kBits == 8 && v_log2[x][e >> 1] == -INFINITY ? -INFINITY
+                                                                         : s[x][n][e] * (kBits == 8 ? unit_of[x][e >> 1] : unit_log2);
+                top[e & 1] = fmaxf(top[e & 1], s[x][n][e]);
+              }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(~0u, top[e], x));
+              const float up = fmaxf(m[n][e], top[e]), ref = up == -INFINITY ? 0.f : up, down = m[n][e] - up;
+              const bool first_rows = m[n][e] == -INFINITY;
+              l[n][e] *= first_rows ? 0.f : fast_exp2(down);
+              float most = -INFINITY;
+#pragma unroll
+              for (int x = 0; x < kGroups; ++x)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float d = s[x][n][2 * i + e] - ref;
+                  l[n][e] += fast_exp2(d);
+                  s[x][n][2 * i + e] = kBits == 8 ? d + v_log2[x][i] : d;
+                  most = fmaxf(most, s[x][n][2 * i + e]);
+                }
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, x));
+              const float was = rho[n][e] + down;  // NaN where there were no rows
+              rho[n][e] = fmaxf(fmaxf(was, most), -48.f);
+              const float keep = first_rows ? 0.f : fast_exp2(was - rho[n][e]);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) o_acc[i][n][e] *= keep, o_acc[i][n][2 + e] *= keep;
+              m[n][e] = up;
+#pragma unroll
+              for (int x = 0; x < kGroups; ++x) s[x][n][e] += kWeightBits - rho[n][e], s[x][n][2 + e] += kWeightBits - rho[n][e];
+            }
+          }
+        }
         const float ref[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
 #pragma unroll
         for (int x = 0; x < kGroups; ++x) {
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e] = fast_exp2(kBits == 4 ? fmaf(s[x][n][e], unit_log2, -ref[e & 1]) : s[x][n][e] - ref[e & 1]);
-            if constexpr (kBits == 8)
+            if (kBits < 16 && beyond[n]) {
+              p[e] = fast_exp2(s[x][n][e]);
+            } else if constexpr (kBits == 8) {
+              p[e] = fast_exp2(fmaf(s[x][n][e], unit_of[x][e >> 1], v_log2[x][e >> 1]) - ref[e & 1]);
               l[n][e & 1] = fmaf(p[e], v_inverse[x][e >> 1], l[n][e & 1]);
-            else
+            } else {
+              p[e] = fast_exp2(kBits == 4 ? fmaf(s[x][n][e], unit_log2, -ref[e & 1]) : s[x][n][e] - ref[e & 1]);
               l[n][e & 1] += p[e];
+            }
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -1014,7 +1075,8 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
               sh.m[slot][head] = m[n][e];
               sh.l[slot][head] = l[n][e];
             }
-            const float by = whole ? inverse_of(l[n][e]) : 1.f;
+            float by = whole ? inverse_of(l[n][e]) : 1.f;
+            if (kBits < 16 && beyond[n]) by *= fast_exp2(rho[n][e] - kWeightBits);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               if constexpr (kBits == 16) {

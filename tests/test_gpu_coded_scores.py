@@ -1,0 +1,146 @@
+"""GPU tests of decode over 8 and 4 bits with scores of any size that the header allows: of
+rows alike, where the output is known whatever the score, and of rows far below others."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import jagged_attention_gb300 as jfa
+from tests import coded_ref
+
+pytestmark = pytest.mark.gpu
+BF16, I32, U8 = torch.bfloat16, torch.int32, torch.uint8
+STEP = torch.finfo(BF16).eps / 2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    jfa.build()
+
+
+def _draw(shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(BF16)
+
+
+class Case:
+    """A cache of requests of `lens` rows, of given values, on pages in order."""
+
+    def __init__(self, bits, lens, hq, hk, D, page, k, v):
+        self.bits, self.lens, self.scale = bits, lens, None
+        count = [-(-n // page) for n in lens]
+        self.pager = jfa.Pager(max_seqs=len(lens), max_pages=max(count), num_pages=sum(count), page_size=page, H=hq, Hkv=hk, D=D,
+                               bits=bits)
+        self.held = self.pager.pages()
+        table, slots, at = np.full((len(lens), max(count)), -1), [], 0
+        for b, n in enumerate(count):
+            table[b, :n] = np.arange(at, at + n)
+            slots.append(at * page + np.arange(lens[b]))
+            at += n
+        self.table = torch.as_tensor(table, dtype=I32).cuda()
+        self.offsets = torch.as_tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=I32).cuda()
+        self.scales = dict(k_scales=self.held[2], v_scales=self.held[3])
+        jfa.paged_append(self.pager, k, v, torch.as_tensor(np.concatenate(slots), dtype=I32).cuda(), *self.held[:2], **self.scales)
+
+    def rows(self):
+        """Cached values of each request, [n, Hkv, D] in 64 bits: (k, v)."""
+        k, v = jfa.paged_gather(self.pager, *self.held[:2], self.table, self.offsets, rows=sum(self.lens), **self.scales)
+        return list(zip(k.double().split(self.lens), v.double().split(self.lens)))
+
+    def decode(self, q, scale):
+        lens = torch.as_tensor(self.lens, dtype=I32).cuda()
+        got = jfa.paged_decode(self.pager, q, *self.held[:2], self.table, lens, scale, **self.scales)
+        again = jfa.paged_decode(self.pager, q, *self.held[:2], self.table, lens, scale, **self.scales)
+        assert self.pager.status() == 0 and torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+        return got
+
+
+def _bound(w, v, n, delta):
+    """Of |out error| for weights w [rows] right to delta in their exponents, as coded_ref.decode: the
+    sums, a weight's rounding to fp16, or half its smallest number, and the output's rounding."""
+    mass, most = w @ v.abs(), v.abs().amax()
+    off = (2 * delta + coded_ref.FP16_HALF_STEP) * mass + n * 2.0 ** -39 * most
+    return off * (1 + STEP) + STEP * (w @ v).abs()
+
+
+SIZES = [-3, 9, 10, 13, 20, 22, 23, 24, 25, 26, 27, 28, 31, 40, 77, 100]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D,hq,hk", [(64, 4, 2), (128, 8, 1), (128, 24, 1), (64, 12, 1)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rows_of_one_key(bits, D, hq, hk, sign):
+    """All rows of a request have the same key: whatever their score, the output is the mean of the
+    values, and log-sum-exp the score and log n.  One row, a tile of them, and many CTAs' worth."""
+    lens = [1, 2, 64, 70, 3000, 1]
+    rows = sum(lens)
+    key = _draw((1, hk, D), 1).expand(rows, hk, D).contiguous()
+    v = (_draw((rows, hk, D), 2).float() * torch.exp2(torch.randint(-20, 20, (rows, hk, 1), device="cuda").float())).to(BF16)
+    case = Case(bits, lens, hq, hk, D, 16, key, v)
+    cached = case.rows()
+    base = _draw((len(lens), hq, D), 3) * sign
+    for size in SIZES:
+        # powers of two shared by q and the scale, each within its type
+        q = (base.float() * 2.0 ** min(size, 60)).to(BF16)
+        scale = 2.0 ** max(0, size - 60) / 8
+        out, lse = case.decode(q, scale)
+        for b, n in enumerate(lens):
+            k, val = cached[b]
+            for h in range(hq):
+                g = h // (hq // hk)
+                score = scale * float(q[b, h].double() @ k[0, g])
+                # equal scores leave no error but what the powers of values add: scores up to 2^10 times log2 e
+                # are rounded with them, to 2^-14 (half a step at 2^10 is 2^-14)
+                delta = 2.0 ** -14 + 2.0 ** -17 + 2 * n * 2.0 ** -24
+                w = torch.full((n,), 1.0 / n, dtype=torch.float64, device="cuda")
+                err = (out[b, h].double() - w @ val[:, g]).abs()
+                assert (err <= _bound(w, val[:, g], n, delta)).all(), (size, b, h, float(err.max()))
+                size_of = scale * float(q[b, h].double().abs() @ k[0, g].abs())
+                off = 2 * D * 2.0 ** -24 * size_of + 2.0 ** -22 * (abs(score) + math.log(n) + 1) + delta
+                assert abs(float(lse[h, b]) - score - math.log(n)) <= off, (size, b, h)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 24, 2.0 ** 26, 2.0 ** 33, 2.0 ** 90])
+@pytest.mark.parametrize("hq,hk", [(4, 2), (8, 1), (24, 1)])
+@pytest.mark.parametrize("where", ["first", "last", "spread", "one"])
+def test_rows_far_above_and_below(bits, size, hq, hk, where):
+    """Some rows' scores are so far above the rest that these count for nothing, or (q turned round) the
+    other way: the output is the mean of the rows on top, wherever a stretch meets them."""
+    D, lens = 64, [3, 200, 2500]
+    rows = sum(lens)
+    key, flags = _draw((hk, D), 1), []
+    for n in lens:
+        flag = np.zeros(n, dtype=bool)
+        if where == "first":
+            flag[:max(1, n // 3)] = True
+        elif where == "last":
+            flag[-max(1, n // 3):] = True
+        elif where == "spread":
+            flag[::7] = True
+        else:
+            flag[n // 2] = True
+        flags.append(torch.as_tensor(flag).cuda())
+    big = torch.cat(flags)
+    k = torch.where(big[:, None, None], key, key / 8)
+    v = _draw((rows, hk, D), 2)
+    case = Case(bits, lens, hq, hk, D, 16, k, v)
+    cached = case.rows()
+    # a query that has the same sign as its key everywhere: scores of size and an eighth of it
+    q = (key.sign()[:, None].expand(hk, hq // hk, D).reshape(1, hq, D).expand(len(lens), hq, D)).contiguous()
+    per = float((q[0].double().view(hk, -1, D) * cached[1][0][big[3:203]][0][:, None].double()).sum(-1).min())
+    scale = size / per
+    for sign in (1, -1):
+        out, lse = case.decode(q * sign, scale)
+        for b, n in enumerate(lens):
+            on_top = flags[b] if sign == 1 else ~flags[b]
+            count = int(on_top.sum())
+            val = cached[b][1][on_top]
+            for h in range(hq):
+                g = h // (hq // hk)
+                w = torch.full((count,), 1.0 / count, dtype=torch.float64, device="cuda")
+                delta = 2.0 ** -14 + 2.0 ** -17 + 2 * n * 2.0 ** -24
+                # rows of 4 bits that are alike in bf16 are alike in codes; those below weigh exp(-size 7 / 8) at most
+                assert ((out[b, h].double() - w @ val[:, g]).abs() <= _bound(w, val[:, g], n, delta)).all(), (sign, b, h)
+                assert torch.isfinite(lse[h, b])
