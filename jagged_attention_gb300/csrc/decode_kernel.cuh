@@ -345,6 +345,10 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
   constexpr int kTile = C::kTile, kSub = C::kSub, kWarps = C::kWarps;
   extern __shared__ __align__(256) unsigned char smem[];
   __shared__ DecodeShared<kWarps, NT> sh;
+  // Of a warp's stretch with large scores, for each head: its largest score m; rho, the largest
+  // score + power - m; and the unit.  The registers m are 0 then, that of the unit 1, and l
+  // and O are over 2^(rho - 15) more than m: what else is done is the same for all scores.
+  __shared__ struct { float m, rho, unit; } large_of[kBits < 16 ? kWarps : 1][8 * NT];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   wait_for_launch_before();
   // ---- units of all requests, and where this CTA's warps begin.  Up to 32 requests
@@ -646,10 +650,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
     if (more) find_next();
 
     float o_acc[D / 16][NT][4], m[NT][2], l[NT][2];
-    // Of codes, of stretches with a reference beyond kNear: m is the largest score then, and
-    // O is o_acc 2^(rho - 15), with rho the largest z = score + power - m.
-    float rho[NT][2];
-    bool beyond[NT];
+    bool beyond = false;  // of codes: the stretch has a reference beyond kNear
     uint32_t qf[D / 16][NT][2];
     const int g = lane >> 2, j = lane & 3;
     int t0 = 0, first = 0, heads = 0;
@@ -783,6 +784,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
     while (now.u < hi) {
       if (fresh) {
         fresh = false;
+        beyond = false;
         t0 = now.t;
         heads_of<kSide>(a, now.vh * together + part, &first, &heads);
 #pragma unroll
@@ -802,8 +804,6 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
           }
           m[n][0] = m[n][1] = -INFINITY;
           l[n][0] = l[n][1] = 0.f;
-          rho[n][0] = rho[n][1] = kWeightBits;
-          beyond[n] = false;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -908,10 +908,9 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
         }
       }
 
-      uint32_t hi_f[kGroups][NT][2], lo_f[kGroups][NT][2]  /* of codes: weights as fp16 alone */;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float top[2] = {-INFINITY, -INFINITY};
+      // The heads' largest scores, of codes plus their rows' powers.
+      auto tops_of = [&](int n, float (&top)[2]) {
+        top[0] = top[1] = -INFINITY;
 #pragma unroll
         for (int x = 0; x < kGroups; ++x)
 #pragma unroll
@@ -929,76 +928,81 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
         }
         if constexpr (kBits == 8) top[0] -= kWeightBits, top[1] -= kWeightBits;
         if constexpr (kBits == 4) top[0] = fmaf(top[0], unit_log2, -kWeightBits), top[1] = fmaf(top[1], unit_log2, -kWeightBits);
-        if (__any_sync(~0u, top[0] > m[n][0] || top[1] > m[n][1])) {
-          if constexpr (kBits < 16) {
-            auto is_beyond = [&](float ref) { return fabsf(ref) > kNear<kBits> && fabsf(ref) < INFINITY; };
-            beyond[n] |= __any_sync(~0u, is_beyond(fmaxf(m[n][0], top[0])) || is_beyond(fmaxf(m[n][1], top[1])));
-            if (beyond[n]) top[0] = top[1] = -INFINITY;  // m is moved below
-          }
+      };
+      // The reference to the larger one of itself and top.
+      auto raise = [&](int n, const float (&top)[2]) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float up = fmaxf(m[n][e], top[e]);
-            // all scores so far -inf: there is nothing to keep
-            const float keep = m[n][e] == -INFINITY ? 0.f : fast_exp2(m[n][e] - up);
-            m[n][e] = up;
-            l[n][e] *= keep;
+        for (int e = 0; e < 2; ++e) {
+          const float up = fmaxf(m[n][e], top[e]);
+          // all scores so far -inf: there is nothing to keep
+          const float keep = m[n][e] == -INFINITY ? 0.f : fast_exp2(m[n][e] - up);
+          m[n][e] = up;
+          l[n][e] *= keep;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) o_acc[i][n][e] *= keep, o_acc[i][n][2 + e] *= keep;
-          }
+          for (int i = 0; i < D / 16; ++i) o_acc[i][n][e] *= keep, o_acc[i][n][2 + e] *= keep;
         }
-        if constexpr (kBits < 16) {
-          if (beyond[n]) {
-            // Scores are rounded first, so that the largest less the reference is 0 whatever
-            // its size; s becomes what the weights are powers of two of.
-            top[0] = top[1] = -INFINITY;
+      };
+      // The same in a stretch with large scores.  These are rounded first, so that the largest
+      // less the reference is 0 whatever its size.  s becomes the exponents of the weights.
+      auto raise_beyond = [&](int n) {
+        auto* const kept = large_of[warp] + 8 * n + 2 * j;  // heads 2 j and 2 j + 1
+        if (!beyond) {
+          if (g == 0) kept[0] = {m[n][0], kWeightBits, unit_log2}, kept[1] = {m[n][1], kWeightBits, unit_log2};
+          __syncwarp();
+        }
 #pragma unroll
-            for (int x = 0; x < kGroups; ++x)
+        for (int e = 0; e < 2; ++e) {
+          const float m_was = kept[e].m, unit = kept[e].unit;
+          float top = -INFINITY, most = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                s[x][n][e] = kBits == 8 && v_log2[x][e >> 1] == -INFINITY ? -INFINITY
-                                                                         : s[x][n][e] * (kBits == 8 ? unit_of[x][e >> 1] : unit_log2);
-                top[e & 1] = fmaxf(top[e & 1], s[x][n][e]);
-              }
+          for (int x = 0; x < kGroups; ++x)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(~0u, top[e], x));
-              const float up = fmaxf(m[n][e], top[e]), ref = up == -INFINITY ? 0.f : up, down = m[n][e] - up;
-              const bool first_rows = m[n][e] == -INFINITY;
-              l[n][e] *= first_rows ? 0.f : fast_exp2(down);
-              float most = -INFINITY;
-#pragma unroll
-              for (int x = 0; x < kGroups; ++x)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const float d = s[x][n][2 * i + e] - ref;
-                  l[n][e] += fast_exp2(d);
-                  s[x][n][2 * i + e] = kBits == 8 ? d + v_log2[x][i] : d;
-                  most = fmaxf(most, s[x][n][2 * i + e]);
-                }
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, x));
-              const float was = rho[n][e] + down;  // NaN where there were no rows
-              rho[n][e] = fmaxf(fmaxf(was, most), -48.f);
-              const float keep = first_rows ? 0.f : fast_exp2(was - rho[n][e]);
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) o_acc[i][n][e] *= keep, o_acc[i][n][2 + e] *= keep;
-              m[n][e] = up;
-#pragma unroll
-              for (int x = 0; x < kGroups; ++x) s[x][n][e] += kWeightBits - rho[n][e], s[x][n][2 + e] += kWeightBits - rho[n][e];
+            for (int i = 0; i < 2; ++i) {
+              const bool out = kBits == 8 && v_log2[x][i] == -INFINITY;  // with 4 bits s is -infinity
+              float& t = s[x][n][2 * i + e];
+              t = out ? -INFINITY : t * (kBits == 8 ? unit_of[x][i] : unit);
+              top = fmaxf(top, t);
             }
-          }
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+          const float up = fmaxf(m_was, top), ref = up == -INFINITY ? 0.f : up;
+#pragma unroll
+          for (int x = 0; x < kGroups; ++x)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float& t = s[x][n][2 * i + e];
+              t -= ref;
+              if constexpr (kBits == 8) t += v_log2[x][i];
+              most = fmaxf(most, t);
+            }
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, x));
+          const float was = kept[e].rho + (m_was - up);  // NaN or -infinity where there was no score
+          const float rho = fmaxf(fmaxf(was, most), -48.f);
+          const float keep = m_was == -INFINITY ? 0.f : fast_exp2(was - rho);
+          __syncwarp();
+          if (g == 0) kept[e].m = up, kept[e].rho = rho;
+          m[n][e] = 0.f;
+          l[n][e] *= keep;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) o_acc[i][n][e] *= keep, o_acc[i][n][2 + e] *= keep;
+#pragma unroll
+          for (int x = 0; x < kGroups; ++x) s[x][n][e] += kWeightBits - rho, s[x][n][2 + e] += kWeightBits - rho;
         }
+        __syncwarp();
+      };
+
+      uint32_t hi_f[kGroups][NT][2], lo_f[kGroups][NT][2]  /* of codes: weights as fp16 alone */;
+      // Weights exp2(s - m), of codes exp2(s unit + power - m), and their sums.
+      auto weights = [&](int n) {
         const float ref[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
 #pragma unroll
         for (int x = 0; x < kGroups; ++x) {
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (kBits < 16 && beyond[n]) {
-              p[e] = fast_exp2(s[x][n][e]);
-            } else if constexpr (kBits == 8) {
-              p[e] = fast_exp2(fmaf(s[x][n][e], unit_of[x][e >> 1], v_log2[x][e >> 1]) - ref[e & 1]);
+            if constexpr (kBits == 8) {
+              p[e] = fast_exp2(fmaf(s[x][n][e], unit_of[x][e >> 1], v_log2[x][e >> 1] - ref[e & 1]));
               l[n][e & 1] = fmaf(p[e], v_inverse[x][e >> 1], l[n][e & 1]);
             } else {
               p[e] = fast_exp2(kBits == 4 ? fmaf(s[x][n][e], unit_log2, -ref[e & 1]) : s[x][n][e] - ref[e & 1]);
@@ -1019,6 +1023,47 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
             }
           }
         }
+      };
+      if constexpr (kBits == 16) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float top[2];
+          tops_of(n, top);
+          if (__any_sync(~0u, top[0] > m[n][0] || top[1] > m[n][1])) raise(n, top);
+          weights(n);
+        }
+      } else {
+        float top[NT][2];
+        bool higher = beyond, large = beyond;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          tops_of(n, top[n]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float up = fmaxf(m[n][e], top[n][e]);
+            higher |= top[n][e] > m[n][e];
+            large |= fabsf(up) > kNear<kBits> && fabsf(up) < INFINITY;
+          }
+        }
+        if (__any_sync(~0u, higher)) {
+          if (__any_sync(~0u, large)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) raise_beyond(n);
+            beyond = true;
+            if (kBits == 4) unit_log2 = 1.f;
+            if constexpr (kBits == 8) {
+#pragma unroll
+              for (int x = 0; x < kGroups; ++x)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) unit_of[x][i] = 1.f, v_log2[x][i] = 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) raise(n, top[n]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) weights(n);
       }
       cp_async_wait<1>();  // V is here, the next K may be on its way
       __syncwarp();
@@ -1069,14 +1114,15 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(~0u, l[n][e], x);
             const int head = 8 * n + 2 * j + e;
+            float back = 1.f;
+            if (kBits < 16 && beyond) m[n][e] = large_of[warp][head].m, back = fast_exp2(large_of[warp][head].rho - kWeightBits);
             if (whole) {
-              if (g == 0 && head < heads) a.lse[int64_t(first + head) * a.B + now.b] = lse_of<kBits>(m[n][e], l[n][e]);
+              if (g == 0 && head < heads) a.lse[int64_t(first + head) * a.B + now.b] = lse_of<kBits>(m[n][e], l[n][e] * back);
             } else if (g == 0) {
               sh.m[slot][head] = m[n][e];
-              sh.l[slot][head] = l[n][e];
+              sh.l[slot][head] = l[n][e] * back;
             }
-            float by = whole ? inverse_of(l[n][e]) : 1.f;
-            if (kBits < 16 && beyond[n]) by *= fast_exp2(rho[n][e] - kWeightBits);
+            const float by = whole ? inverse_of(l[n][e]) : back;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               if constexpr (kBits == 16) {
@@ -1299,7 +1345,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
 template <int kBits, int D, int NT, bool kSide, typename U>
 cudaError_t launch(const ArgsOf<kBits>& a, int sms, cudaStream_t stream) {
   using C = DecodeCfg<kBits, D, NT>;
-  static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<C::kWarps, NT>) + 1024) <= 233472, "shared memory of an SM");
+  static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<C::kWarps, NT>) + (kBits < 16 ? C::kWarps : 1) * C::kHeads * 12 + 1024) <= 233472, "shared memory of an SM");
   cudaError_t e = set_smem_limit_once<decode_kernel<kBits, D, NT, kSide, U>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   return launch_overlapped(decode_kernel<kBits, D, NT, kSide, U>, dim3(sms * C::kCtasPerSm), C::kWarps * 32,
