@@ -666,42 +666,32 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
     // with V are four neighbours; its places along D are the lane's own bytes of a row.
     constexpr int kGroups = kTile / 16;  // of 16 rows
     const int row_a = 4 * (g >> 1) + (g & 1);
-    float unit_log2 = 0.f;  // of a product of q and codes, in units of log2 e; not negative
+    float unit_log2[NT][2];  // of a product of a head's q and codes, in units of log2 e; not negative
     // first of the 4 values of D that the lane has in step ks
     auto k_first = [&](int ks) { return kBits == 4 ? D / 4 * j + 4 * ks : 16 * (j + 4 * (ks / 4)) + 4 * (ks % 4); };
-    // q as fp16, times the sign of the scale and the power of two that takes the largest of
-    // all heads to 2^14 and more, and its inverse: what 2^-39 of the largest and less loses
-    // is below the roundings of the sums.
-    auto to_halves = [&](uint32_t (&w)[D / 16][NT][2]) -> float {
-      uint32_t top = 0;
+    // q as fp16, times the sign of the scale and for each head the power of two that takes its
+    // largest value to 2^14 and more: heads do not touch each other.
+    auto to_halves = [&](uint32_t (&w)[D / 16][NT][2]) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
+      for (int n = 0; n < NT; ++n) {
+        uint32_t top = 0;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) top = max_of(top, max_of(w[ks][n][0], w[ks][n][1]));
-      top = __reduce_max_sync(~0u, top_of(top));
-      if (top >= 0x7f80u) {  // the largest that is finite: heads have their own infinities and NaN
-        top = 0;
+        for (int ks = 0; ks < D / 16; ++ks) top = max_of(top, max_of(w[ks][n][0], w[ks][n][1]));
+        top = top_of(top);
+        top = max(top, __shfl_xor_sync(~0u, top, 1));  // a head's values are in four lanes
+        top = max(top, __shfl_xor_sync(~0u, top, 2));
+        const int e = max(static_cast<int>(top >> 7) - 127 - 14, -126);
+        const float by = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), scale_log2);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t lo = w[ks][n][i] & 0x7fffu, hi = (w[ks][n][i] >> 16) & 0x7fffu;
-              top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-            }
-        top = __reduce_max_sync(~0u, top);
-      }
-      const int e = max(static_cast<int>(top >> 7) - 127 - 14, -126);
-      const float by = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), scale_log2);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
           for (int i = 0; i < 2; ++i)
             w[ks][n][i] = pack_f16x2(__uint_as_float(w[ks][n][i] << 16) * by, __uint_as_float(w[ks][n][i] & 0xffff0000u) * by);
-      return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        // at least the smallest normal number, so that times -infinity it is that
+        const float unit = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(scale_log2), 0x1p-126f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) unit_log2[n][i] = __shfl_sync(~0u, unit, 4 * (2 * j + i));  // of the heads whose scores it has
+      }
     };
     // Words of codes of K that a lane takes up at a time from a row: 4 (of 8 codes for 2
     // steps, or of 4 for one), a 16-byte chunk, or the 2 that there are.
@@ -809,8 +799,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o_acc[i][n][e] = 0.f;
         }
-        // at least the smallest normal number, so that times -infinity it is that
-        if constexpr (kBits < 16) unit_log2 = fmaxf(to_halves(qf) * fabsf(scale_log2), 0x1p-126f);
+        if constexpr (kBits < 16) to_halves(qf);
       }
       cp_async_wait<1>();  // K is here, V may be on its way
       __syncwarp();
@@ -872,22 +861,24 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
       }
       cp_async_commit();
 
-      // 8 bits, of a row's score: its unit, what its values' power of two adds to the
-      // exponent, and 2 to the minus that.
-      float unit_of[kGroups][2], v_log2[kGroups][2], v_inverse[kGroups][2];
+      // 8 bits, of a row: its keys' power of two, by which its products are multiplied; what
+      // its values' adds to the exponent, and 2 to the minus that.
+      float v_log2[kGroups][2], v_inverse[kGroups][2];
       uint32_t nan_now[kSub] = {};
       bool nan_rows = false;
       if constexpr (kBits == 8) {
 #pragma unroll
         for (int z = 0; z < kSub; ++z) {
-          const float unit = power_value(k_power_now[z]) * unit_log2;
+          const float power_of_k = power_value(k_power_now[z]);
           nan_now[z] = __ballot_sync(~0u, v_power_now[z] == kNanScale);
           nan_rows |= nan_now[z] != 0;
           const int power = v_power_now[z] == kNanScale ? 127 : min(max(v_power_now[z], kLeastPower), kMostPower);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int x = 2 * z + i / 2, from = 16 * (i / 2) + row_a + 2 * (i % 2);
-            unit_of[x][i % 2] = __shfl_sync(~0u, unit, from);
+            const float of_k = __shfl_sync(~0u, power_of_k, from);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[x][n][2 * (i % 2)] *= of_k, s[x][n][2 * (i % 2) + 1] *= of_k;
             const int c = __shfl_sync(~0u, power, from);
             v_log2[x][i % 2] = static_cast<float>(c - 127);
             v_inverse[x][i % 2] = __uint_as_float(static_cast<uint32_t>(254 - c) << 23);
@@ -901,7 +892,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
               if (!((live_now[x / 2] >> (16 * (x % 2) + row_a + 2 * e)) & 1)) {
-                if constexpr (kBits == 8) unit_of[x][e] = 0.f, v_log2[x][e] = -INFINITY;
+                if constexpr (kBits == 8) v_log2[x][e] = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) s[x][n][2 * e] = s[x][n][2 * e + 1] = kBits == 8 ? 0.f : -INFINITY;
               }
@@ -919,7 +910,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
               const bool counts = (live_now[0] >> (16 * x + g + (e >> 1) * 8)) & 1;
               s[x][n][e] = counts ? s[x][n][e] * scale_log2 : -INFINITY;
             }
-            top[e & 1] = fmaxf(top[e & 1], kBits == 8 ? fmaf(s[x][n][e], unit_of[x][e >> 1], v_log2[x][e >> 1]) : s[x][n][e]);
+            top[e & 1] = fmaxf(top[e & 1], kBits == 8 ? fmaf(s[x][n][e], unit_log2[n][e & 1], v_log2[x][e >> 1]) : s[x][n][e]);
           }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
@@ -927,7 +918,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
           top[1] = fmaxf(top[1], __shfl_xor_sync(~0u, top[1], x));
         }
         if constexpr (kBits == 8) top[0] -= kWeightBits, top[1] -= kWeightBits;
-        if constexpr (kBits == 4) top[0] = fmaf(top[0], unit_log2, -kWeightBits), top[1] = fmaf(top[1], unit_log2, -kWeightBits);
+        if constexpr (kBits == 4) top[0] = fmaf(top[0], unit_log2[n][0], -kWeightBits), top[1] = fmaf(top[1], unit_log2[n][1], -kWeightBits);
       };
       // The reference to the larger one of itself and top.
       auto raise = [&](int n, const float (&top)[2]) {
@@ -947,7 +938,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
       auto raise_beyond = [&](int n) {
         auto* const kept = large_of[warp] + 8 * n + 2 * j;  // heads 2 j and 2 j + 1
         if (!beyond) {
-          if (g == 0) kept[0] = {m[n][0], kWeightBits, unit_log2}, kept[1] = {m[n][1], kWeightBits, unit_log2};
+          if (g == 0) kept[0] = {m[n][0], kWeightBits, unit_log2[n][0]}, kept[1] = {m[n][1], kWeightBits, unit_log2[n][1]};
           __syncwarp();
         }
 #pragma unroll
@@ -960,7 +951,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
             for (int i = 0; i < 2; ++i) {
               const bool out = kBits == 8 && v_log2[x][i] == -INFINITY;  // with 4 bits s is -infinity
               float& t = s[x][n][2 * i + e];
-              t = out ? -INFINITY : t * (kBits == 8 ? unit_of[x][i] : unit);
+              t = out ? -INFINITY : t * unit;
               top = fmaxf(top, t);
             }
 #pragma unroll
@@ -983,6 +974,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
           __syncwarp();
           if (g == 0) kept[e].m = up, kept[e].rho = rho;
           m[n][e] = 0.f;
+          unit_log2[n][e] = 1.f;
           l[n][e] *= keep;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) o_acc[i][n][e] *= keep, o_acc[i][n][2 + e] *= keep;
@@ -1002,10 +994,10 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if constexpr (kBits == 8) {
-              p[e] = fast_exp2(fmaf(s[x][n][e], unit_of[x][e >> 1], v_log2[x][e >> 1] - ref[e & 1]));
+              p[e] = fast_exp2(fmaf(s[x][n][e], unit_log2[n][e & 1], v_log2[x][e >> 1] - ref[e & 1]));
               l[n][e & 1] = fmaf(p[e], v_inverse[x][e >> 1], l[n][e & 1]);
             } else {
-              p[e] = fast_exp2(kBits == 4 ? fmaf(s[x][n][e], unit_log2, -ref[e & 1]) : s[x][n][e] - ref[e & 1]);
+              p[e] = fast_exp2(kBits == 4 ? fmaf(s[x][n][e], unit_log2[n][e & 1], -ref[e & 1]) : s[x][n][e] - ref[e & 1]);
               l[n][e & 1] += p[e];
             }
           }
@@ -1050,12 +1042,11 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) raise_beyond(n);
             beyond = true;
-            if (kBits == 4) unit_log2 = 1.f;
             if constexpr (kBits == 8) {
 #pragma unroll
               for (int x = 0; x < kGroups; ++x)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) unit_of[x][i] = 1.f, v_log2[x][i] = 0.f;
+                for (int i = 0; i < 2; ++i) v_log2[x][i] = 0.f;
             }
           } else {
 #pragma unroll

@@ -52,7 +52,9 @@ class Case:
         lens = torch.as_tensor(self.lens, dtype=I32).cuda()
         got = jfa.paged_decode(self.pager, q, *self.held[:2], self.table, lens, scale, **self.scales)
         again = jfa.paged_decode(self.pager, q, *self.held[:2], self.table, lens, scale, **self.scales)
-        assert self.pager.status() == 0 and torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+        assert self.pager.status() == 0
+        assert torch.equal(got[0].view(torch.int16), again[0].view(torch.int16))  # bit for bit, NaN too
+        assert torch.equal(got[1].view(I32), again[1].view(I32))
         return got
 
 
@@ -144,3 +146,57 @@ def test_rows_far_above_and_below(bits, size, hq, hk, where):
                 # rows of 4 bits that are alike in bf16 are alike in codes; those below weigh exp(-size 7 / 8) at most
                 assert ((out[b, h].double() - w @ val[:, g]).abs() <= _bound(w, val[:, g], n, delta)).all(), (sign, b, h)
                 assert torch.isfinite(lse[h, b])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("size", [2.0 ** 11, 2.0 ** 25, 2.0 ** 33, 2.0 ** 60, 2.0 ** 100, math.inf])
+@pytest.mark.parametrize("hq,hk,D", [(8, 1, 64), (12, 1, 128), (16, 2, 128)])
+def test_heads_beside_one_of_large_scores(bits, size, hq, hk, D):
+    """One head's large scores, as of what an unused head may hold up to the type's largest number
+    (inf here), leave the heads beside it within their bounds."""
+    lens = [700, 40, 5000]
+    case = Case(bits, lens, hq, hk, D, 16, _draw((sum(lens), hk, D), 1), _draw((sum(lens), hk, D), 2))
+    q = _draw((len(lens), hq, D), 3)
+    if size < math.inf:
+        q[:, 3] = (q[:, 3].float() * (size / 8)).to(BF16)
+    else:
+        q[:, 3] = torch.finfo(BF16).max * q[:, 3].sign()
+    out, lse = case.decode(q, D ** -0.5)
+    others = [h for h in range(hq) if h != 3]
+    assert torch.isfinite(out[:, others]).all() and torch.isfinite(lse[others]).all()
+    assert size == math.inf or torch.isfinite(out).all() and torch.isfinite(lse).all()
+    for b, (k, v) in enumerate(case.rows()):
+        n = lens[b]
+        for h in others:
+            g = h // (hq // hk)
+            s = D ** -0.5 * (k[:, g] @ q[b, h].double())
+            w = torch.softmax(s, 0)
+            reach = D ** -0.5 * float((k[:, g].abs() @ q[b, h].double().abs()).max())
+            delta = 2 * D * 2.0 ** -24 * reach + 2.0 ** -17 + 2 * n * 2.0 ** -24
+            assert ((out[b, h].double() - w @ v[:, g]).abs() <= _bound(w, v[:, g], n, delta)).all(), (b, h)
+            assert abs(float(lse[h, b]) - float(torch.logsumexp(s, 0))) <= delta + 2.0 ** -23 * abs(float(lse[h, b]))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("hq,hk,D", [(8, 1, 64), (24, 1, 128), (16, 4, 128)])
+def test_heads_of_very_different_sizes(bits, hq, hk, D):
+    """Heads from 2^-60 to 2^60 of one another, each with scores of its own size."""
+    lens = [300, 64, 1]
+    case = Case(bits, lens, hq, hk, D, 16, _draw((sum(lens), hk, D), 1), _draw((sum(lens), hk, D), 2))
+    power = torch.linspace(-60, 60, hq, device="cuda").round()
+    base = _draw((len(lens), hq, D), 3)
+    q = (base.float() * torch.exp2(power)[:, None]).to(BF16)
+    for scale in (2.0 ** -60, 2.0 ** 20):
+        out, lse = case.decode(q, scale)
+        for b, (k, v) in enumerate(case.rows()):
+            n = lens[b]
+            for h in range(hq):
+                g = h // (hq // hk)
+                s = scale * (k[:, g] @ q[b, h].double())
+                reach = scale * float((k[:, g].abs() @ q[b, h].double().abs()).max())
+                if reach > 100:
+                    continue  # the bound says nothing any more
+                w = torch.softmax(s, 0)
+                delta = 2 * D * 2.0 ** -24 * reach + 2.0 ** -17 + 2 * n * 2.0 ** -24
+                assert ((out[b, h].double() - w @ v[:, g]).abs() <= _bound(w, v[:, g], n, delta)).all(), (b, h)
+                assert abs(float(lse[h, b]) - float(torch.logsumexp(s, 0))) <= delta + 2.0 ** -23 * abs(float(lse[h, b]))
