@@ -348,6 +348,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
   // Of a warp's stretch with large scores, for each head: its largest score m; rho, the largest
   // score + power - m; and the unit.  The registers m are 0 then, that of the unit 1, and l
   // and O are over 2^(rho - 15) more than m: what else is done is the same for all scores.
+  __shared__ __align__(8) float q_units[kBits < 16 ? kWarps : 1][8 * NT];
   __shared__ struct { float m, rho, unit; } large_of[kBits < 16 ? kWarps : 1][8 * NT];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   wait_for_launch_before();
@@ -626,13 +627,16 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
     cp_async_commit();
     copy(v_stage, a.v, true);
     cp_async_commit();
-    uint32_t live_now[kSub];
-    int k_power_now[kSub], v_power_now[kSub];
+    // 8 bits: the upper half of its keys' power of two, the byte of its values', kNanValues
+    constexpr uint32_t kNanValues = 0x100;
+    uint32_t live_now[kSub], powers_now[kSub];
     auto take_over = [&] {  // the tile asked for is the one computed next
 #pragma unroll
       for (int z = 0; z < kSub; ++z) {
         live_now[z] = live[z];
-        if constexpr (kBits == 8) k_power_now[z] = k_power[z], v_power_now[z] = v_power[z];
+        if constexpr (kBits == 8)
+          powers_now[z] = (__float_as_uint(power_value(k_power[z])) & 0xffff0000u) |
+                          (v_power[z] == kNanScale ? kNanValues | 127u : static_cast<uint32_t>(min(max(v_power[z], kLeastPower), kMostPower)));
       }
     };
     take_over();
@@ -666,7 +670,6 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
     // with V are four neighbours; its places along D are the lane's own bytes of a row.
     constexpr int kGroups = kTile / 16;  // of 16 rows
     const int row_a = 4 * (g >> 1) + (g & 1);
-    float unit_log2[NT][2];  // of a product of a head's q and codes, in units of log2 e; not negative
     // first of the 4 values of D that the lane has in step ks
     auto k_first = [&](int ks) { return kBits == 4 ? D / 4 * j + 4 * ks : 16 * (j + 4 * (ks / 4)) + 4 * (ks % 4); };
     // q as fp16, times the sign of the scale and for each head the power of two that takes its
@@ -689,9 +692,9 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
             w[ks][n][i] = pack_f16x2(__uint_as_float(w[ks][n][i] << 16) * by, __uint_as_float(w[ks][n][i] & 0xffff0000u) * by);
         // at least the smallest normal number, so that times -infinity it is that
         const float unit = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(scale_log2), 0x1p-126f);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) unit_log2[n][i] = __shfl_sync(~0u, unit, 4 * (2 * j + i));  // of the heads whose scores it has
+        if (j == 0) q_units[warp][8 * n + g] = unit;
       }
+      __syncwarp();
     };
     // Words of codes of K that a lane takes up at a time from a row: 4 (of 8 codes for 2
     // steps, or of 4 for one), a 16-byte chunk, or the 2 that there are.
@@ -869,19 +872,17 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
       if constexpr (kBits == 8) {
 #pragma unroll
         for (int z = 0; z < kSub; ++z) {
-          const float power_of_k = power_value(k_power_now[z]);
-          nan_now[z] = __ballot_sync(~0u, v_power_now[z] == kNanScale);
+          nan_now[z] = __ballot_sync(~0u, (powers_now[z] & kNanValues) != 0);
           nan_rows |= nan_now[z] != 0;
-          const int power = v_power_now[z] == kNanScale ? 127 : min(max(v_power_now[z], kLeastPower), kMostPower);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int x = 2 * z + i / 2, from = 16 * (i / 2) + row_a + 2 * (i % 2);
-            const float of_k = __shfl_sync(~0u, power_of_k, from);
+            const uint32_t both = __shfl_sync(~0u, powers_now[z], from), c = both & 0xffu;
+            const float of_k = __uint_as_float(both & 0xffff0000u);
 #pragma unroll
             for (int n = 0; n < NT; ++n) s[x][n][2 * (i % 2)] *= of_k, s[x][n][2 * (i % 2) + 1] *= of_k;
-            const int c = __shfl_sync(~0u, power, from);
-            v_log2[x][i % 2] = static_cast<float>(c - 127);
-            v_inverse[x][i % 2] = __uint_as_float(static_cast<uint32_t>(254 - c) << 23);
+            v_log2[x][i % 2] = __uint_as_float(0x4b000000u | c) - (0x1p23f + 127.f);  // 2^23 + c: c as a number
+            v_inverse[x][i % 2] = __uint_as_float((254u - c) << 23);
           }
         }
       }
@@ -899,6 +900,14 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
         }
       }
 
+      float unit_log2[NT][2];
+      if constexpr (kBits < 16) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float2 of = *reinterpret_cast<const float2*>(q_units[warp] + 8 * n + 2 * j);
+          unit_log2[n][0] = of.x, unit_log2[n][1] = of.y;
+        }
+      }
       // The heads' largest scores, of codes plus their rows' powers.
       auto tops_of = [&](int n, float (&top)[2]) {
         top[0] = top[1] = -INFINITY;
@@ -972,7 +981,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
           const float rho = fmaxf(fmaxf(was, most), -48.f);
           const float keep = m_was == -INFINITY ? 0.f : fast_exp2(was - rho);
           __syncwarp();
-          if (g == 0) kept[e].m = up, kept[e].rho = rho;
+          if (g == 0) kept[e].m = up, kept[e].rho = rho, q_units[warp][8 * n + 2 * j + e] = 1.f;
           m[n][e] = 0.f;
           unit_log2[n][e] = 1.f;
           l[n][e] *= keep;
@@ -1031,13 +1040,16 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
         for (int n = 0; n < NT; ++n) {
           tops_of(n, top[n]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float up = fmaxf(m[n][e], top[n][e]);
-            higher |= top[n][e] > m[n][e];
-            large |= fabsf(up) > kNear<kBits> && fabsf(up) < INFINITY;
-          }
+          for (int e = 0; e < 2; ++e) higher |= top[n][e] > m[n][e];
         }
         if (__any_sync(~0u, higher)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float up = fabsf(fmaxf(m[n][e], top[n][e]));
+              large |= up > kNear<kBits> && up < INFINITY;
+            }
           if (__any_sync(~0u, large)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) raise_beyond(n);
@@ -1336,7 +1348,7 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
 template <int kBits, int D, int NT, bool kSide, typename U>
 cudaError_t launch(const ArgsOf<kBits>& a, int sms, cudaStream_t stream) {
   using C = DecodeCfg<kBits, D, NT>;
-  static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<C::kWarps, NT>) + (kBits < 16 ? C::kWarps : 1) * C::kHeads * 12 + 1024) <= 233472, "shared memory of an SM");
+  static_assert(C::kCtasPerSm * (C::kSmemBytes + sizeof(DecodeShared<C::kWarps, NT>) + (kBits < 16 ? C::kWarps : 1) * C::kHeads * 16 + 1024) <= 233472, "shared memory of an SM");
   cudaError_t e = set_smem_limit_once<decode_kernel<kBits, D, NT, kSide, U>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   return launch_overlapped(decode_kernel<kBits, D, NT, kSide, U>, dim3(sms * C::kCtasPerSm), C::kWarps * 32,
