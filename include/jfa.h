@@ -698,7 +698,8 @@ int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, con
  * jfa_paged_decode).  With 8 or 4 bits the attention is that over the values the codes
  * stand for: scores, softmax statistics and sums are fp32, a weight enters the product
  * with V as one fp16 number, 11 bits down to 2^-29 of the largest, and values of q below
- * 2^-28 of the largest of their head lose bits, below 2^-39 all of them.  A NaN key of
+ * 2^-28 of the largest of their head lose bits, below 2^-39 all of them.  The largest of a
+ * head times |scale| is below 2^140 (beyond, scores of its keys may come out smaller).  A NaN key of
  * a counted row makes its heads' out and lse NaN, a NaN value its place of out. */
 int jfa_paged_decode_ex(jfa_pager_t pager, int B, const void* q, int64_t q_row, const jfa_pages* pages,
                         const jfa_scales* scales, const int32_t* table, int64_t table_row,

@@ -690,8 +690,8 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             w[ks][n][i] = pack_f16x2(__uint_as_float(w[ks][n][i] << 16) * by, __uint_as_float(w[ks][n][i] & 0xffff0000u) * by);
-        // at least the smallest normal number, so that times -infinity it is that
-        const float unit = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(scale_log2), 0x1p-126f);
+        // normal numbers: times a product of 0 it is that, and times -infinity
+        const float unit = fminf(fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * fabsf(scale_log2), 0x1p-126f), 0x1.fffffep127f);
         if (j == 0) q_units[warp][8 * n + g] = unit;
       }
       __syncwarp();

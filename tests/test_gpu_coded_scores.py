@@ -200,3 +200,40 @@ def test_heads_of_very_different_sizes(bits, hq, hk, D):
                 delta = 2 * D * 2.0 ** -24 * reach + 2.0 ** -17 + 2 * n * 2.0 ** -24
                 assert ((out[b, h].double() - w @ v[:, g]).abs() <= _bound(w, v[:, g], n, delta)).all(), (b, h)
                 assert abs(float(lse[h, b]) - float(torch.logsumexp(s, 0))) <= delta + 2.0 ** -23 * abs(float(lse[h, b]))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("power,scale", [(120, 2.0 ** 30), (127, 2.0 ** 126), (-126, 2.0 ** -126), (120, 0.0), (0, -(2.0 ** 126))])
+def test_keys_of_zeros(bits, power, scale):
+    """The score of a key of zeros is 0 whatever the query and the scale, each within its limit."""
+    lens, hq, hk, D = [1, 100, 2000], 8, 2, 64
+    v = _draw((sum(lens), hk, D), 2)
+    case = Case(bits, lens, hq, hk, D, 16, torch.zeros_like(v), v)
+    out, lse = case.decode((_draw((len(lens), hq, D), 3).sign().float() * 2.0 ** power).to(BF16), scale)
+    for b, (_, val) in enumerate(case.rows()):
+        n = lens[b]
+        w = torch.full((n,), 1.0 / n, dtype=torch.float64, device="cuda")
+        delta = 2.0 ** -17 + 2 * n * 2.0 ** -24
+        for h in range(hq):
+            assert ((out[b, h].double() - w @ val[:, h // 4]).abs() <= _bound(w, val[:, h // 4], n, delta)).all(), (b, h)
+            assert abs(float(lse[h, b]) - math.log(n)) <= delta + 2.0 ** -22 * (1 + math.log(n))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_queries_and_scales_at_their_limit(bits):
+    """A query times the scale of 2^138, and keys small enough for a score of 2^124."""
+    lens, hq, hk, D = [1, 100, 2000], 8, 2, 64
+    v = _draw((sum(lens), hk, D), 2)
+    key = torch.zeros_like(v)
+    key[..., 0] = 6 * 2.0 ** -17
+    case = Case(bits, lens, hq, hk, D, 16, key, v)
+    q = torch.full((len(lens), hq, D), 2.0 ** 110, device="cuda").to(BF16)
+    for scale in (2.0 ** 28, -(2.0 ** 28)):
+        out, lse = case.decode(q, scale)
+        for b, (k, val) in enumerate(case.rows()):
+            n, score = lens[b], scale * 2.0 ** 110 * float(k[0, 0].sum())
+            assert 2.0 ** 110 < abs(score) < 2.0 ** 127
+            w = torch.full((n,), 1.0 / n, dtype=torch.float64, device="cuda")
+            for h in range(hq):
+                assert ((out[b, h].double() - w @ val[:, h // 4]).abs() <= _bound(w, val[:, h // 4], n, 2.0 ** -17 + 2 * n * 2.0 ** -24)).all()
+                assert abs(float(lse[h, b]) / score - 1) <= 2 * D * 2.0 ** -24
