@@ -664,7 +664,7 @@ int jfa_paged_append_ex(jfa_pager_t pager, int64_t rows, const void* k, int64_t 
  * Rows before offsets[0] and from offsets[B] on stay as they were.  A row whose place
  * is negative or beyond the table is zeros (JFA_PAGER_BAD_LENGTH), so is one on a page
  * outside the cache (JFA_PAGER_BAD_PAGE); offsets beyond `rows` set JFA_PAGER_BAD_LENGTH
- * too.  Outputs overlap no input, nor each other (JFA_ERR_INVALID_ARG; as slices of
+ * too (rows = 0: nothing else is looked at).  Outputs overlap no input, nor each other (JFA_ERR_INVALID_ARG; as slices of
  * one tensor, whose rows lie side by side, they may alternate).
  */
 int jfa_paged_gather(jfa_pager_t pager, int B, const jfa_pages* pages, const jfa_scales* scales,

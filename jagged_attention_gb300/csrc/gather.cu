@@ -53,6 +53,10 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
   constexpr int64_t kZeros = -1, kLeft = -2;
   __shared__ int64_t codes_at[kGatherRows], scales_at[kGatherRows];
   wait_for_launch_before();
+  if (a.rows == 0) {  // launched for this alone
+    if (threadIdx.x == 0 && a.offsets[a.B] > 0) atomicOr(a.status, kPagerBadLength);
+    return;
+  }
   const int64_t r0 = int64_t(blockIdx.x) * block_rows;
   const int rows = static_cast<int>(min(int64_t(block_rows), a.rows - r0));
   if (threadIdx.x < 32) {
@@ -153,13 +157,13 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
 cudaError_t launch_gather(const GatherArgs& a, int sms, cudaStream_t stream) {
   // As many rows to a block as have that many pieces, fewer where that would not make two
   // blocks an SM: 64 rows of 8 heads take 2.3 us so, with 16 rows a block 6.0.
-  const int per_row = a.Hkv * (a.D / 16);
+  const int per_row = std::max(1, a.Hkv * (a.D / 16));
   const int64_t few = a.rows / (2 * sms), many = std::max(1, kGatherUnits / per_row);
   const int block_rows = static_cast<int>(std::max<int64_t>(1, std::min({few, many, int64_t(kGatherRows)})));
   // A piece's 32 bytes go out at once where they are a sector of memory: 1.6 GB from 4 bits
   // take 240 us so, in halves 297.
   const bool whole = (reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.v_out) | 2 * a.k_row | 2 * a.v_row) % 32 == 0;
-  const dim3 grid(static_cast<unsigned>((a.rows + block_rows - 1) / block_rows));
+  const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, (a.rows + block_rows - 1) / block_rows)));
   auto* kernel = a.bits == 8 ? gather_kernel<8> : a.bits == 4 ? gather_kernel<4> : gather_kernel<16>;
   return launch_overlapped(kernel, grid, kGatherThreads, 0, stream, a, block_rows, make_page_div(per_row), whole);
 }

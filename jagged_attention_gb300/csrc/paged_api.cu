@@ -463,23 +463,31 @@ int jfa_paged_gather(jfa_pager_t pager, int B, const jfa_pages* pages, const jfa
                      const int32_t* offsets, int64_t rows, void* k_out, int64_t k_row, void* v_out,
                      int64_t v_row, void* stream) {
   if (!pager || B < 1 || B > pager->max_seqs || rows < 0 || rows > INT_MAX) return JFA_ERR_INVALID_ARG;
-  if (rows == 0) return JFA_OK;
-  if (!table || !offsets || table_row < pager->max_pages) return JFA_ERR_INVALID_ARG;
-  if (!aligned(table, 4) || !aligned(offsets, 4) || !aligned(starts, 4)) return JFA_ERR_ALIGNMENT;
+  if (!offsets) return JFA_ERR_INVALID_ARG;
+  if (!aligned(offsets, 4)) return JFA_ERR_ALIGNMENT;
+  jfa::GatherArgs a{};
+  a.B = B;
+  a.bits = pager->bits;
+  a.rows = rows;
+  a.offsets = offsets;
+  a.status = pager->d_status;
+  const auto s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {  // whether the offsets say so too
+    if (int rc = check_device(pager)) return rc;
+    return jfa::launch_gather(a, pager->sms, s) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+  }
+  if (!table || table_row < pager->max_pages) return JFA_ERR_INVALID_ARG;
+  if (!aligned(table, 4) || !aligned(starts, 4)) return JFA_ERR_ALIGNMENT;
   if (int rc = check_cache(pager, pages, scales)) return rc;
   if (int rc = check_rows(k_out, k_row, pager->Hkv, pager->D, false)) return rc;
   if (int rc = check_rows(v_out, v_row, pager->Hkv, pager->D, false)) return rc;
   if (!side_by_side(k_out, k_row, v_out, v_row, rows, int64_t(pager->Hkv) * pager->D)) return JFA_ERR_INVALID_ARG;
   if (int rc = check_device(pager)) return rc;
   const int unit = pager->bits == 16 ? 2 : 1;  // bytes of an element of the pages
-  jfa::GatherArgs a{};
-  a.B = B;
   a.Hkv = pager->Hkv;
   a.D = pager->D;
-  a.bits = pager->bits;
   a.max_pages = pager->max_pages;
   a.num_pages = pager->num_pages;
-  a.rows = rows;
   a.div = pager->div;
   a.k = static_cast<const unsigned char*>(pages->k);
   a.v = static_cast<const unsigned char*>(pages->v);
@@ -489,14 +497,12 @@ int jfa_paged_gather(jfa_pager_t pager, int B, const jfa_pages* pages, const jfa
   a.scales = scales_of(scales);
   a.table = table;
   a.starts = starts;
-  a.offsets = offsets;
   a.table_row = table_row;
   a.k_out = static_cast<uint16_t*>(k_out);
   a.v_out = static_cast<uint16_t*>(v_out);
   a.k_row = k_row;
   a.v_row = v_row;
-  a.status = pager->d_status;
-  return jfa::launch_gather(a, pager->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
+  return jfa::launch_gather(a, pager->sms, s) == cudaSuccess ? JFA_OK : JFA_ERR_CUDA;
 }
 
 }  // extern "C"
