@@ -619,7 +619,8 @@ typedef struct jfa_pages {
 
 /* Scale bytes of a cache of 8 or 4 bits: a row of a head has n = 1 (8 bits) or D / 16 (4
  * bits) of them, one behind the other; distances in bytes, multiples of n as the
- * addresses are.  The pages' distances count bytes then, multiples of 16.  Scales of a
+ * addresses are, rows less than 2^32 apart (decode: else JFA_ERR_UNSUPPORTED, as for the
+ * pages).  The pages' distances count bytes then, multiples of 16.  Scales of a
  * head's rows that lie one behind the other (row = n) are read in the fewest pieces. */
 typedef struct jfa_scales {
   void* k;
@@ -664,8 +665,9 @@ int jfa_paged_append_ex(jfa_pager_t pager, int64_t rows, const void* k, int64_t 
  * Rows before offsets[0] and from offsets[B] on stay as they were.  A row whose place
  * is negative or beyond the table is zeros (JFA_PAGER_BAD_LENGTH), so is one on a page
  * outside the cache (JFA_PAGER_BAD_PAGE); offsets beyond `rows` set JFA_PAGER_BAD_LENGTH
- * too (rows = 0: nothing else is looked at).  Outputs overlap no input, nor each other (JFA_ERR_INVALID_ARG; as slices of
- * one tensor, whose rows lie side by side, they may alternate).
+ * too (rows = 0: nothing else is looked at).  Outputs overlap no input.  Nor do they
+ * overlap each other, which is JFA_ERR_INVALID_ARG; as slices of one tensor, whose rows
+ * lie side by side, they may alternate.
  */
 int jfa_paged_gather(jfa_pager_t pager, int B, const jfa_pages* pages, const jfa_scales* scales,
                      const int32_t* table, int64_t table_row, const int32_t* starts,
@@ -697,10 +699,12 @@ int jfa_paged_decode(jfa_pager_t pager, int B, const void* q, int64_t q_row, con
 /* jfa_paged_decode for a pager of any number of bits: scales is NULL for 16 (then it is
  * jfa_paged_decode).  With 8 or 4 bits the attention is that over the values the codes
  * stand for: scores, softmax statistics and sums are fp32, a weight enters the product
- * with V as one fp16 number, 11 bits down to 2^-29 of the largest, and values of q below
- * 2^-28 of the largest of their head lose bits, below 2^-39 all of them.  The largest of a
- * head times |scale| is below 2^140 (beyond, scores of its keys may come out smaller).  A NaN key of
- * a counted row makes its heads' out and lse NaN, a NaN value its place of out. */
+ * with V as one fp16 number, 11 bits down to 2^-29 of the largest (8 bits: the largest of
+ * weights times their rows' powers of two of V, so that rows of values far below others'
+ * lose bits at any weight).  Values of q below 2^-28 of the largest of their head lose
+ * bits, below 2^-39 all of them; that largest one times |scale| is below 2^140 (beyond,
+ * scores may come out smaller than they are).  A NaN key of a counted row makes its heads'
+ * out and lse NaN, a NaN value its place of out. */
 int jfa_paged_decode_ex(jfa_pager_t pager, int B, const void* q, int64_t q_row, const jfa_pages* pages,
                         const jfa_scales* scales, const int32_t* table, int64_t table_row,
                         const int32_t* lens, float scale, void* out, float* lse, void* stream);

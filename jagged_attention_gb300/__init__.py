@@ -885,7 +885,9 @@ def paged_gather(pager: Pager, k_pages, v_pages, table, offsets, *, rows: int, s
     as they were.  offsets [B + 1], starts [B], table [B, max_pages], B at least 1.  Returns
     (k_out, v_out), which fwd takes as k and v where Hkv is its H; with grouped heads q
     [n, H, D] goes there as q.view(n, Hkv, H // Hkv, D).transpose(1, 2).reshape(-1, Hkv, D),
-    its offsets times H // Hkv."""
+    its offsets times H // Hkv.  fwd is not causal: each of a prompt's rows would attend to
+    all rows gathered of its request, those behind it too, which is not what a causal model
+    wants of them (its newest row is paged_decode's)."""""
     if stream is not None:
         with _on(stream):
             return paged_gather(pager, k_pages, v_pages, table, offsets, rows=rows, starts=starts, k_scales=k_scales,

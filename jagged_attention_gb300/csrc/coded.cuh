@@ -4,7 +4,7 @@
 // 8 bits: e4m3 codes and one byte c for the row's head, value = code * 2^(c - 127).  A
 // power of two: codes have the same 3 mantissa bits anywhere in their range, so a finer
 // scale would gain nothing, and this one multiplies and divides exactly.  The range of
-// c keeps weights times scales far within fp32 (decode_coded.cuh).
+// c keeps weights times scales far within fp32 (decode_kernel.cuh).
 // 4 bits: e2m1 codes, the first value of two in the lower nibble, and a byte for each
 // 16 values, their scale as bits 14 .. 7 of the fp16 number (5 exponent bits, 3 of the
 // mantissa, no sign): a code has 2 mantissa bits, its product with a scale 6, exact in
@@ -84,7 +84,7 @@ __device__ __forceinline__ uint2 code8(const float (&x)[8], int c) {
   for (int i = 0; i < 8; i += 2) f2_unpack(f2_mul(f2_pack(x[i], x[i + 1]), by2), y[i], y[i + 1]);
   return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
 }
-// 1 / s for a block with scale byte c; 0 where s is 0 or NaN, and all codes are 0.
+// 1 / s for a block with scale byte c; 0 where s is 0, and all codes are 0, or NaN, and they do not matter.
 __device__ __forceinline__ float inverse_scale(int c) {
   const float s = scale_value(c);
   float r;

@@ -10,19 +10,21 @@ namespace {
 // Memory gives 128 bytes at a time, and gives 256 in a row faster.  Rows of neighbouring
 // heads that lie within so much are read side by side, by warps of one CTA, where there is
 // enough to read; in between the lines are in L2.  That halves the warps along a row and
-// doubles the parts that CTAs join.
-//   rows of 64 and 32 bytes: 96 requests up to 32768 rows, 8 heads: 4 bits of 128 values 394
-//   us, one head after the other 596; 8 bits of 64 values 284 and 531; 128 mixed requests,
-//   126 MB, 40.5 and 42.5, 96, 95 MB, 33.9 and 34.5, 32, 32 MB, 21.3 and 18.9; one of 131072
-//   rows, 76 MB, 33.1 and 30.1.
-//   rows of 128 bytes: the full cache of 8 bits 540 us and 605 (of one GPU; of another 539
-//   and 546), 512 mixed requests, 0.9 GB, 152 and 164, 128, 224 MB, 46 either way; one of
-//   131072 rows, 134 MB, 35 and 31.
+// doubles the parts that CTAs join, which a single row feels most: just above the bounds it
+// loses up to 3%, batches gain or lose nothing there.
+//   rows of 64 and 32 bytes: 96 requests up to 32768 rows, 8 heads: 4 bits of 128 values 391
+//   us, one head after the other 592; 8 bits of 64 values 288 and 542; 128 mixed requests,
+//   126 MB, 40.4 and 42.9, 96, 95 MB, 33.5 and 34.7, 64, 64 MB, 27.2 and 27.5, 32, 34 MB, 20.9
+//   and 18.8; one of 524288 rows of 4 heads, 302 MB, 75.3 and 86.2, of 262144, 151 MB, 48.1
+//   and 46.9, of 131072, 76 MB, 32.5 and 29.8.
+//   rows of 128 bytes: the full cache of 8 bits 541 us and 604 (of one GPU; of another 539
+//   and 546), 512 mixed requests, 0.9 GB, 147 and 159, 128, 224 MB, 45 either way; one of
+//   524288 rows, 541 MB, 90.4 and 89.1, of 131072, 135 MB, 34.1 and 29.7.
 constexpr int kLineMb = 80, kPairMb = 256;
 
 // Where so much is read as comes and goes in L2 meanwhile, 4-bit lines are not marked to
-// leave first, or their second reader would miss them: the full cache 394 us, marked 472;
-// 256 mixed requests, 250 MB, 70.2 and 67.7.  Of 8 bits they always are (548 and 540).
+// leave first, or their second reader might miss them: the full cache 391 us, marked 398;
+// 256 mixed requests, 250 MB, 69.9 and 67.9.  Of 8 bits they always are (not 549, marked 541).
 constexpr int kFarMb = 512;
 
 constexpr int kCodedTile = DecodeCfg<8, 128, 1>::kTile;

@@ -11,7 +11,7 @@
 //
 // Codes (coded.cuh) become fp16 on their way from shared memory to the tensor cores, which
 // is exact: cvt takes two e4m3 or e2m1 codes, 4-bit ones are then multiplied by their
-// scale.  q becomes fp16 too, times a power of two that leaves its 8 bits.  8 bits: with
+// scale.  q becomes fp16 too, times a power of two of its head that leaves its 8 bits.  8 bits: with
 // 2^e_t and 2^f_t the powers of two of row t of K and V, s_t = scale 2^e_t q . c_t and
 //     out = sum 2^(s_t + f_t - r) c'_t / sum 2^(s_t - r)   (s_t in units of log2 e),
 // where r is the running maximum of s_t + f_t rather than of s_t: the weights of the codes
@@ -19,6 +19,10 @@
 // A weight enters the product as one fp16 number of 11 bits, times 2^15 so that it is not
 // subnormal before 2^-29 of the largest; its rounding, 2^-11 at most, is an eighth of that
 // of the output to bf16, and a second number would cost as many products again.
+// The 2^15 is taken off r in fp32, which is exact enough while r is small (kNear).  In a
+// stretch of larger scores r is the largest score as it is, rounded to fp32; weights are
+// powers of two of z = (s_t - r) + f_t, over 2^(rho - 15) with rho the largest z, and l and
+// O are held over that too until the stretch ends.
 //
 // Bound: every cached row is read once, 4 D bytes for 4 D G flops (G query heads
 // to a key/value head), so memory bandwidth bounds it while G is small.  The
@@ -55,9 +59,9 @@
 // the stages of 8 warps measured best: with 192 KB the full cache took 1126 us for
 // 1070, with 6 warps 1094 for 1064.
 //
-// Codes, same GPU as the above: the full cache, 3.6 GB of 8 bits in 526 to 541 us, 6.9 to 6.7
-// TB/s; 2.0 GB of 4 bits in 394 us, 5.1 TB/s (by heads outside rows 389); 128 mixed requests, 224 MB
-// in 45 us and 126 MB in 41; one of 131072, 76 MB of 4 bits in 30 us; one of 300 rows in 6.3.
+// Codes, by GPU: the full cache, 3.6 GB of 8 bits in 525 to 543 us, 6.9 to 6.7 TB/s; 2.0 GB of
+// 4 bits in 391 to 395 us, 5.1 TB/s (by heads outside rows 398); 128 mixed requests, 224 MB in 43
+// to 45 us and 126 MB in 40; one of 131072, 76 MB of 4 bits in 30 us; one of 300 rows in 6.3.
 // Codes in the warps' registers want tiles of 64 rows: of 32 the full caches take 590 and 417 us.
 // 4 bits run best with 16 warps an SM of 128 registers each; with 8 of 255 they take 8% fewer
 // instructions and 415 us.  Scores of two groups of 16 rows are summed side by side (4% of the
@@ -79,9 +83,9 @@ constexpr int kMostHeads = 16;   // query heads that a warp holds
 constexpr int kMostTogether = 8;  // warps side by side
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kWeightBits = 15.f;  // of codes: the largest weight is 2^15, as fp16 has it
-// The largest running reference, in units of log2 e, that 15 is taken off as it is: 4 bits:
-// it is rounded by 1/8 at most then, and the largest weight is 2^15.125; 8 bits: scores
-// with their powers of two are rounded by 2^-14 at most.
+// The largest running reference, in units of log2 e, that 15 is taken off as it is.  4 bits:
+// it is rounded by 1/8 at most then, and the largest weight is 2^15.125.  8 bits: a weight's
+// exponent is off by 2^-13 at most for its row's power of two, a sixth of fp16's rounding.
 template <int kBits>
 constexpr float kNear = kBits == 8 ? 0x1p10f : 0x1p22f;
 
@@ -98,8 +102,8 @@ struct DecodeCfg {
   static constexpr int kWarpBytes = kStageBytes + kVBytes + kOutBytes;  // K, V, park
   static constexpr int kWarps = 8;
   static constexpr int kSmemBytes = kWarps * kWarpBytes;
-  // 8 bits of 64 values with 16 heads a warp: 380 us for the full cache so, with two CTAs of
-  // 128 registers, which spill, 568; 4 bits 377 and 333.
+  // 64 values with 16 heads a warp, the full cache: 8 bits 398 us so, with two CTAs of 128
+  // registers, which spill, 596; 4 bits with two, which spill less, 352, with one 357.
   static constexpr int kCtasPerSm = kBits == 16 ? (D == 64 ? 2 : 1) : kBits == 8 ? (D == 64 && NT == 1 ? 2 : 1)
                                                                               : (D == 64 || NT == 1 ? 2 : 1);
 };
@@ -107,8 +111,8 @@ struct DecodeCfg {
 // Units of work: the n tiles of a (request, key/value head) count n units, and
 // kRowUnits behind them stand for its beginning and end (256 requests up to 300
 // rows: 34.6 us without, 32.5 with; 128 mixed ones 74.7 and 74.2).  Of codes, whose tiles
-// are larger, one: 500 requests up to 900 rows in 4 bits 55.7 us, with two 59.0, none 60.8,
-// 512 mixed ones in 8 bits 147, 152 and 149.
+// are larger, one: 500 requests up to 900 rows in 4 bits 69.2 us, with two 72.0, none 73.2,
+// 512 mixed ones in 8 bits 147, 152 and 149, 128 mixed ones 45.2, 46.2 and 52.0.
 template <int kBits>
 constexpr int kRowUnits = kBits == 16 ? 2 : 1;
 
@@ -345,9 +349,10 @@ decode_kernel(const __grid_constant__ ArgsOf<kBits> a) {
   constexpr int kTile = C::kTile, kSub = C::kSub, kWarps = C::kWarps;
   extern __shared__ __align__(256) unsigned char smem[];
   __shared__ DecodeShared<kWarps, NT> sh;
-  // Of a warp's stretch with large scores, for each head: its largest score m; rho, the largest
-  // score + power - m; and the unit.  The registers m are 0 then, that of the unit 1, and l
-  // and O are over 2^(rho - 15) more than m: what else is done is the same for all scores.
+  // Of codes, for each head of a warp the unit of a product of its q and codes, in units of
+  // log2 e, not negative (in registers the full cache of 4 bits takes 404 us for 395).  Of a
+  // stretch with large scores its largest score m, rho, and the unit: q_units is 1 then and
+  // the register m 0, so that what else is done is the same for all scores.
   __shared__ __align__(8) float q_units[kBits < 16 ? kWarps : 1][8 * NT];
   __shared__ struct { float m, rho, unit; } large_of[kBits < 16 ? kWarps : 1][8 * NT];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

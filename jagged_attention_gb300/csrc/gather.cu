@@ -9,7 +9,7 @@
 // threads then take 16 values of a row's head of K and of V at a time.
 //
 // Measured (GB300, 6.79 TB/s copied): 394,687 rows of 8 heads, 1.6 GB from 4 bits in 240 us,
-// 6.7 TB/s; from 8 bits, 1.9 GB in 279 us, 6.8 TB/s; 32,657 rows, 171 MB from 4 bits in 30.5
+// 6.7 TB/s; from 8 bits, 1.9 GB in 279 us, 6.8 TB/s; from 16, 2.5 GB in 366 us, 6.9 TB/s; 32,657 rows, 171 MB from 4 bits in 30.5
 // us, 5.6 TB/s; 720 rows of 4 heads in 2.1 us, which is the launch.
 #include <algorithm>
 

@@ -134,8 +134,10 @@ __device__ __forceinline__ void walk_heads(const RowJob& job, int D, int64_t in,
   }
 }
 
-// Codes: registers for 14 blocks an SM, the next head's loads under way: 44.8 us for the rows
-// above, 49.3 with 16 blocks (spills), 50.9 with 12.  Up to 16 heads a thread: 12 take 3% more.
+// Codes: registers for 14 blocks an SM, the next head's loads under way: the rows above and their
+// gather take 76.1 us, with 16 blocks, which spill 248 bytes a thread, 78.9; with 12, which
+// spill 124 and are fewer threads, 81.7.  14 spill 148 (of 8 bits 124).  Up to 16 heads a
+// thread: 12 take 3% more.
 constexpr int kCodedBlocksPerSm = 14, kCodedHeadsAThread = 16;
 
 // As walk_heads, into codes of 8 or 4 bits: what a bf16 cache would hold, quantised.
