@@ -237,3 +237,51 @@ def test_queries_and_scales_at_their_limit(bits):
             for h in range(hq):
                 assert ((out[b, h].double() - w @ val[:, h // 4]).abs() <= _bound(w, val[:, h // 4], n, 2.0 ** -17 + 2 * n * 2.0 ** -24)).all()
                 assert abs(float(lse[h, b]) / score - 1) <= 2 * D * 2.0 ** -24
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("hq,hk,D", [(8, 2, 64), (12, 1, 128), (24, 1, 128)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_requests_beside_ones_of_large_scores(bits, hq, hk, D, captured):
+    """A warp's share goes over several requests, every second of large scores, and a graph is
+    replayed with queries that are large where they were not: nothing is left over from one to the next."""
+    B, page = 12000, 64
+    rng = np.random.default_rng(hq)
+    lens = rng.integers(1, page + 1, B).tolist()
+    owner = torch.repeat_interleave(torch.arange(B), torch.tensor(lens)).cuda()
+    odd = (torch.arange(B, device="cuda") % 2 == 1)[:, None, None]
+    k = torch.where(odd[owner], _draw((B, hk, D), 1)[owner], _draw((sum(lens), hk, D), 4))  # odd ones' rows have one key
+    case = Case(bits, lens, hq, hk, D, page, k, _draw((sum(lens), hk, D), 2))
+    dl, at = torch.as_tensor(lens, dtype=I32).cuda(), torch.arange(B + 1, device="cuda", dtype=I32) * page
+    kd, vd = jfa.paged_gather(case.pager, *case.held[:2], case.table, at, rows=B * page, **case.scales)
+    dead = torch.arange(page, device="cuda")[None, None] >= dl[:, None, None]
+    base, q = _draw((B, hq, D), 3), torch.empty((B, hq, D), dtype=BF16, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((hq, B), device="cuda")
+
+    def call():
+        jfa.paged_decode(case.pager, q, *case.held[:2], case.table, dl, D ** -0.5, **case.scales, out=out, lse=lse)
+
+    q.copy_(base)
+    graph = torch.cuda.CUDAGraph()
+    if captured:
+        with torch.cuda.graph(graph):
+            call()
+    for size in (2.0 ** 30, 1.0, -(2.0 ** 60), 2.0 ** 13):
+        q.copy_(torch.where(odd, base.float() * size, base.float()).to(BF16))
+        graph.replay() if captured else call()
+        assert case.pager.status() == 0
+        for g in range(hk):
+            heads = slice(g * hq // hk, (g + 1) * hq // hk)
+            key, val = (x.view(B, page, hk, D)[:, :, g].double() for x in (kd, vd))
+            s = D ** -0.5 * torch.einsum("bhd,btd->bht", q[:, heads].double(), key)
+            reach = D ** -0.5 * torch.einsum("bhd,btd->bht", q[:, heads].double().abs(), key.abs()).amax(2, keepdim=True)
+            s = s.masked_fill(dead, -math.inf)
+            # rows of one key have one score, whatever its error
+            delta = 2.0 ** -14 + 2.0 ** -17 + 2 * page * 2.0 ** -24 + torch.where(odd, 0.0, 2 * D * 2.0 ** -24 * reach)
+            w = torch.where(odd, (~dead) / dl.double()[:, None, None], torch.softmax(s, 2))
+            want, mass = torch.einsum("bht,btd->bhd", w, val), torch.einsum("bht,btd->bhd", w, val.abs())
+            off = (2 * delta + coded_ref.FP16_HALF_STEP) * mass + page * 2.0 ** -39 * val.abs().amax((1, 2))[:, None, None]
+            assert ((out[:, heads].double() - want).abs() <= off * (1 + STEP) + STEP * want.abs()).all(), size
+            ref, reach = torch.logsumexp(s, 2), reach[..., 0]
+            off = 2 * D * 2.0 ** -24 * reach + 2.0 ** -22 * (ref.abs() + 1) + delta[..., 0]
+            assert ((lse[heads].T.double() - ref).abs() <= off).all(), size
